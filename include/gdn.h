@@ -248,6 +248,161 @@ size_t gdn_bwd_workspace_bytes(const gdn_args* args);
 int gdn_recurrent_bwd(const gdn_args* args, const void* d_o, const float* d_s_final,
                       const gdn_grads* grads, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Linear attention with one decay a head ----------------------------------------
+ *
+ * The recurrence above without the erase: with S in R^{dk x dv} per value head h and a
+ * constant log decay g_h <= 0,
+ *
+ *     S_t = e^{g_h} S_{t-1} + k_t v_t^T,     o_t = S_t^T q_t
+ *
+ * Layouts (row-major; pointers aligned to 16 bytes):
+ *   q, k                 [B, T, Hk, dk]   key head h / (H / Hk) serves value head h
+ *   v, o                 [B, T, H, dv]
+ *   log_decay            [H] float32; e^{g} below e^-128 is taken as 0 (-Inf included);
+ *                        values above 0 are not checked (they grow the state)
+ *   seq_lens             [B] int32 on the device, or NULL: T tokens each. Sequence b has
+ *                        min(max(seq_lens[b], 0), T) tokens; rows of o behind them are
+ *                        left as they were, and the states are those after its last token
+ *   s0, s_final, state   [B, H, dk, dv] float32
+ * q, k and v may be views of a larger array: *_stride is the distance in elements from
+ * one token to the next (0: contiguous), a multiple of 16 bytes and at least one token's
+ * heads; the heads of a token are contiguous, and a sequence starts T strides after the
+ * one before. o is contiguous and must not overlap an input.
+ * Ownership, asynchrony, determinism and errors as above; the current device must be
+ * the stream's. A NaN or Inf in token t reaches o from token t on, never an earlier row. */
+typedef struct gdn_linear_args {
+  int32_t dtype;          /* enum gdn_dtype: q, k, v and o                    */
+  int32_t reserved;       /* must be 0                                        */
+  int64_t B, T, H, Hk;    /* sequences, tokens (T >= 0), value heads, key heads (H % Hk == 0) */
+  int64_t dk, dv;         /* head dims, each in {16, 32, 64, 128}             */
+  int64_t q_stride, k_stride, v_stride;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_decay;
+  const int32_t* seq_lens;
+  const float* s0;        /* NULL means zero; ignored by the step             */
+  float* s_final;         /* NULL means not written; may alias s0; ignored by the step */
+  void* o;
+} gdn_linear_args;
+
+/* Bytes of device workspace gdn_linear_chunk_fwd needs (0 for an invalid set). */
+size_t gdn_linear_workspace_bytes(const gdn_linear_args* args);
+
+/* Chunked pass over prompts: o for every token, and the state after the last one. The
+ * sequence is cut into segments that run in parallel: one pass adds up each segment's own
+ * k v^T, a second carries the state over the segments, and a third computes the outputs
+ * chunk by chunk from the state before each segment (one launch where a sequence is one
+ * segment). ws must hold gdn_linear_workspace_bytes(args) bytes, 256-byte aligned. */
+int gdn_linear_chunk_fwd(const gdn_linear_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* The recurrence token by token on state_inout ([B, H, dk, dv] float32, updated in
+ * place): T = 1 is one decode step. A sequence of length 0 (seq_lens) keeps its state and
+ * its row of o. No workspace. */
+int gdn_linear_recurrent_step(const gdn_linear_args* args, float* state_inout, void* stream);
+
+/* ---- Norms of queries and keys a head, with the position rotation --------------------
+ *
+ * The delta-rule and linear entry points take q and k as they are (keys of unit norm
+ * where the method asks for them); this pass makes them from a projection's output. Per
+ * token and head, with x a row of d channels:
+ *     n = x r w,   r = (sum x^2 / d + eps)^{-1/2} (RMS) or (sum x^2 + eps)^{-1/2} (L2)
+ * then channels 0 .. rot-1 of n are rotated by the token's position p in pairs (a, b),
+ *     a' = a cos[p][i] - b sin[p][i],   b' = b cos[p][i] + a sin[p][i],
+ * where pair i is channels (i, i + rot/2), or (2i, 2i + 1) when interleaved; queries are
+ * multiplied by q_scale. Sums and products are float32, rounded once.
+ *   q, k          [B, T, Hq, d], [B, T, Hk, d]; strides as for the linear entry points
+ *   wq, wk        [d] float32, NULL means ones
+ *   cos, sin      [n_pos, rot/2] float32 (NULL when rot == 0)
+ *   positions     [B, T] int32, NULL means 0 .. T-1 (then n_pos >= T). A position outside
+ *                 [0, n_pos) gives a row of NaN; nothing is read out of bounds
+ *   q_out, k_out  contiguous; may be q / k themselves when those are contiguous */
+enum gdn_norm { GDN_NORM_RMS = 1, GDN_NORM_L2 = 2 };
+
+typedef struct gdn_qk_norm_args {
+  int32_t dtype;        /* enum gdn_dtype: q, k, q_out, k_out                  */
+  int32_t norm;         /* enum gdn_norm                                       */
+  int64_t B, T, Hq, Hk; /* Hq, Hk >= 1                                         */
+  int64_t d;            /* head dim in {16, 32, 64, 128}                       */
+  int64_t q_stride, k_stride;
+  int64_t rot;          /* rotated channels: 0, or a multiple of 8 up to d     */
+  int64_t n_pos;        /* rows of cos and sin                                 */
+  int32_t interleaved;  /* 0 or 1                                              */
+  float eps;            /* >= 0                                                */
+  float q_scale;
+  int32_t reserved;     /* must be 0                                           */
+  const void* q;
+  const void* k;
+  const float* wq;
+  const float* wk;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  void* q_out;
+  void* k_out;
+} gdn_qk_norm_args;
+
+int gdn_qk_norm_fwd(const gdn_qk_norm_args* args, void* stream);
+
+/* Gradients: dq_out, dk_out (contiguous, grad_dtype: args->dtype, or GDN_DTYPE_F32 as
+ * gdn_recurrent_bwd returns them) in; dq, dk (contiguous, args->dtype) and dwq, dwk [d]
+ * float32 (NULL: not written) out. args->q_out and k_out are ignored. The weight sums run
+ * in a fixed order. */
+typedef struct gdn_qk_norm_grads {
+  int32_t grad_dtype;
+  int32_t reserved; /* must be 0 */
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dwq;
+  float* dwk;
+} gdn_qk_norm_grads;
+
+/* Bytes of device workspace gdn_qk_norm_bwd needs (0 for an invalid set). */
+size_t gdn_qk_norm_bwd_workspace_bytes(const gdn_qk_norm_args* args);
+int gdn_qk_norm_bwd(const gdn_qk_norm_args* args, const gdn_qk_norm_grads* grads, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* ---- Gated norm of a layer's outputs ----------------------------------------------------
+ *
+ * Per token and head, y = x (sum x^2 / d + eps)^{-1/2} w act(gate), act(z) = z / (1 + e^-z)
+ * (SILU) or 1 / (1 + e^-z) (SIGMOID): what follows o in a gated layer.
+ *   x, gate    [B, T, H, d]; strides as for the linear entry points
+ *   weight     [d] float32, NULL means ones
+ *   y          contiguous; may be x or gate when that is contiguous */
+enum gdn_activation { GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 };
+
+typedef struct gdn_gated_norm_args {
+  int32_t dtype;      /* enum gdn_dtype: x, gate, y   */
+  int32_t activation; /* enum gdn_activation          */
+  int64_t B, T, H;
+  int64_t d;          /* head dim in {16, 32, 64, 128} */
+  int64_t x_stride, gate_stride;
+  float eps;          /* >= 0 */
+  int32_t reserved;   /* must be 0 */
+  const void* x;
+  const void* gate;
+  const float* weight;
+  void* y;
+} gdn_gated_norm_args;
+
+int gdn_gated_norm_fwd(const gdn_gated_norm_args* args, void* stream);
+
+/* Gradients: dy (contiguous, args->dtype) in; dx, dgate (contiguous, args->dtype) and
+ * dweight [d] float32 (NULL: not written) out. args->y is ignored. */
+typedef struct gdn_gated_norm_grads {
+  const void* dy;
+  void* dx;
+  void* dgate;
+  float* dweight;
+} gdn_gated_norm_grads;
+
+/* Bytes of device workspace gdn_gated_norm_bwd needs (0 for an invalid set). */
+size_t gdn_gated_norm_bwd_workspace_bytes(const gdn_gated_norm_args* args);
+int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_grads* grads, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_str(int status);
 

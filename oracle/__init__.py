@@ -15,6 +15,8 @@ Modules
   stabilize   the GDN2 stabilisers (decay clip, j projection), token-wise
   backward    reverse-mode gradients of the token recurrence (all variants but
               DeltaProduct), pinned by finite differences of ``recurrence``
+  layer       linear attention with one decay a head, the q / k norms with rotation and
+              the gated norm, with gradients, pinned by finite differences
   metrics     rel-L2 and normwise max-rel error (pinned by hand-computed values
               in tests/test_oracle_metrics.py)
 
@@ -24,4 +26,4 @@ pages' models, closed forms, hand-derivable cases); see tests/test_oracle_*.py.
 """
 from .recurrence import (deltanet, gdn, kda, fg2, deltaproduct, gdn2, forward)  # noqa: F401
 from .metrics import rel_l2, max_rel  # noqa: F401
-from . import stabilize, backward  # noqa: F401
+from . import stabilize, backward, layer  # noqa: F401

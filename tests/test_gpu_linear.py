@@ -1,0 +1,208 @@
+"""Linear attention with one decay a head against its float64 recurrence (oracle.layer)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+# B, T, H, Hk, dk, dv
+SIZES = [
+    (1, 1, 1, 1, 16, 16),
+    (2, 15, 3, 3, 16, 32),
+    (1, 64, 4, 2, 64, 64),
+    (3, 65, 2, 1, 32, 128),
+    (2, 130, 4, 4, 128, 16),
+    (1, 300, 6, 2, 128, 128),
+    (1, 1100, 2, 2, 64, 128),
+]
+
+
+def slopes(H):
+    """Heads that forget within a token or two up to heads that keep some hundreds."""
+    return (-torch.exp2(torch.linspace(0.5, -8, H))).float()
+
+
+def make(case, dt, seed, fuse=False):
+    from layer_util import DTYPES, dev, fused, rand
+    B, T, H, Hk, dk, dv = case
+    gen = torch.Generator().manual_seed(seed)
+    dtype = DTYPES[dt]
+    q, k, v = rand(gen, (B, T, Hk, dk), dtype, dk ** -0.5), rand(gen, (B, T, Hk, dk), dtype), rand(gen, (B, T, H, dv), dtype)
+    host = dict(q=q, k=k, v=v, g=slopes(H), s0=rand(gen, (B, H, dk, dv), torch.float32),
+                do=rand(gen, (B, T, H, dv), dtype), ds=rand(gen, (B, H, dk, dv), torch.float32))
+    on = {n: t.to(dev()) for n, t in host.items()}
+    if fuse:
+        on["q"], on["k"], on["v"] = fused([q, k, v])
+    return host, on
+
+
+def ref(host, **kw):
+    from layer_util import f64
+    return layer.linear_forward(*(f64(host[n]) for n in ("q", "k", "v", "g")), **kw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("case", SIZES, ids=lambda c: "-".join(map(str, c)))
+def test_chunk_and_step_against_the_recurrence(case, dt):
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make(case, dt, 31, fuse=case[1] % 2 == 1)
+    o_ref, S_ref = ref(host, s0=f64(host["s0"]))
+    print(f"linear {case} {dt} chunk", flush=True)
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"])
+    check(o, o_ref, "o")
+    check(S, S_ref, "s_final")
+    print(f"linear {case} {dt} step", flush=True)
+    state = on["s0"].clone()
+    o = gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=state)
+    check(o, o_ref, "o of the step")
+    check(state, S_ref, "state of the step")
+    o_ref, S_ref = ref(host)
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"])
+    check(o, o_ref, "o from zero")
+    check(S, S_ref, "s_final from zero")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_padded_batch_leaves_what_lies_behind(dt):
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    host, on = make((6, 200, 4, 2, 64, 64), dt, 32)
+    lens = [200, 0, 64, 131, -5, 1000]          # out of range: taken as 0 and as T
+    ld = torch.tensor(lens, dtype=torch.int32, device=dev())
+    keep = torch.full_like(on["v"], 3.0)
+    o_ref, S_ref = ref(host, s0=f64(host["s0"]), lens=lens, o=f64(keep))
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], seq_lens=ld, o=keep.clone())
+    check(o, o_ref, "o")
+    check(S, S_ref, "s_final")
+    assert torch.equal(S[1], on["s0"][1]) and torch.equal(S[4], on["s0"][4])
+    state = on["s0"].clone()
+    o2 = gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=state, seq_lens=ld, o=keep.clone())
+    check(o2, o_ref, "o of the step")
+    assert torch.equal(state[1], on["s0"][1])
+    for b, n in enumerate([200, 0, 64, 131, 0, 200]):
+        assert (o[b, n:] == 3.0).all() and (o2[b, n:] == 3.0).all()
+
+
+def test_split_sequence_and_state_in_place():
+    """[0, 77) then [77, 200) from the returned state equals one call; s_final may be s0."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make((1, 200, 3, 3, 64, 32), "f32", 33)
+    o_ref, S_ref = ref(host, s0=f64(host["s0"]))
+    S = on["s0"].clone()
+    parts = []
+    for t0, t1 in ((0, 77), (77, 200)):
+        q, k, v = (on[n][:, t0:t1] for n in "qkv")
+        o, S2 = gdn.gdn_linear_chunk_fwd(q, k, v, on["g"], s0=S, s_final=S)
+        assert S2 is S
+        parts.append(o)
+    check(torch.cat(parts, 1), o_ref, "o")
+    check(S, S_ref, "s_final")
+
+
+def test_extreme_decays():
+    """No decay, e^-50 a token, e^-200 and a state that is dropped at every token (-Inf)."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    host, on = make((1, 150, 4, 4, 32, 32), "f32", 34)
+    host["g"] = torch.tensor([0.0, -50.0, -200.0, float("-inf")])
+    on["g"] = host["g"].to(dev())
+    with np.errstate(all="ignore"):
+        o_ref, S_ref = ref(host, s0=f64(host["s0"]))
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"])
+    check(o, o_ref, "o")
+    check(S, S_ref, "s_final")
+    state = on["s0"].clone()
+    check(gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=state), o_ref, "o of the step")
+    check(state, S_ref, "state of the step")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nothing_reaches_an_earlier_row(dt, value):
+    """A NaN or Inf in token 70 (of q, k or v) leaves the rows before it as they were."""
+    import gated_delta_rule_69_amd as gdn
+    host, on = make((1, 140, 2, 2, 64, 64), dt, 35)
+    want, _ = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"])
+    for name in "qkv":
+        bad = {n: on[n].clone() for n in "qkv"}
+        bad[name][0, 70, 1, 5] = value
+        o, S = gdn.gdn_linear_chunk_fwd(bad["q"], bad["k"], bad["v"], on["g"], s0=on["s0"])
+        assert torch.equal(o[:, :70], want[:, :70]), name
+        assert torch.equal(o[:, :, 0], want[:, :, 0]), name
+        assert not torch.isfinite(o[0, 70, 1]).all(), name
+        if name == "q":
+            assert torch.equal(o[:, 71:], want[:, 71:])
+        if name == "v":  # one column of values: the others stay
+            rest = [c for c in range(64) if c != 5]
+            assert torch.equal(o[..., rest], want[..., rest])
+            assert not torch.isfinite(o[0, 70:, 1, 5]).any()
+
+
+def test_agrees_with_the_asym_entry_without_its_erase():
+    """The library's ASYM recurrence with j = 0, eta = 1 and one decay a head."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make((1, 130, 2, 2, 64, 64), "f32", 36)
+    alpha = torch.exp(on["g"])[:, None].expand(on["k"].shape).contiguous()
+    ones = torch.ones(on["v"].shape[:3], device=alpha.device)
+    o1, S1 = gdn.gdn_chunk_fwd("asym", on["q"], on["k"], on["v"], alpha, j=torch.zeros_like(on["k"]), eta=ones,
+                               s0=on["s0"], chunk=32)
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"])
+    check(o, f64(o1), "o")
+    check(S, f64(S1), "s_final")
+
+
+def test_no_tokens_and_no_state_wanted():
+    import gated_delta_rule_69_amd as gdn
+    host, on = make((2, 70, 2, 1, 32, 32), "bf16", 37)
+    none = {n: on[n][:, :0].contiguous() for n in "qkv"}
+    o, S = gdn.gdn_linear_chunk_fwd(none["q"], none["k"], none["v"], on["g"], s0=on["s0"])
+    assert o.numel() == 0 and torch.equal(S, on["s0"])
+    _, S = gdn.gdn_linear_chunk_fwd(none["q"], none["k"], none["v"], on["g"])
+    assert (S == 0).all()
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], want_state=False)
+    o2, _ = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"])
+    assert S is None and torch.equal(o, o2)
+
+
+def test_many_sequences_and_heads():
+    """More states than one wave of workgroups holds, each against its own sequence."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make((60, 3, 16, 8, 64, 64), "bf16", 38)
+    o_ref, S_ref = ref(host, s0=f64(host["s0"]))
+    state = on["s0"].clone()
+    check(gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=state), o_ref, "o")
+    check(state, S_ref, "state")
+
+
+def test_another_stream_and_a_captured_graph():
+    """The step and the chunked pass on a stream of their own, and captured: every replay
+    equals the eager result."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    host, on = make((2, 300, 4, 2, 64, 64), "bf16", 39)
+    want, S_want = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device=dev())
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], stream=side)
+    side.synchronize()
+    assert torch.equal(o, want) and torch.equal(S, S_want)
+    out, state = torch.zeros_like(want), on["s0"].clone()
+    step = [on[n][:, :1].contiguous() for n in "qkv"]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], o=out, s_final=S)
+        so = gdn.gdn_linear_recurrent_step(*step, on["g"], state=state)
+    eager = on["s0"].clone()
+    for _ in range(3):
+        out.zero_(), S.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want_step = gdn.gdn_linear_recurrent_step(*step, on["g"], state=eager)
+        assert torch.equal(out, want) and torch.equal(S, S_want)
+        assert torch.equal(so, want_step) and torch.equal(state, eager)
