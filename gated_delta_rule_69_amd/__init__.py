@@ -12,7 +12,7 @@ from ._lib import (GdnArgs, GdnError, VARIANTS, gdn_abi_version, gdn_asym_stabil
                    load_library,
                    make_args)
 
-_LAYER = ("gdn_linear_chunk_fwd", "gdn_linear_recurrent_step", "gdn_qk_norm_fwd",
+_LAYER = ("gdn_linear_chunk_fwd", "gdn_linear_recurrent_step", "gdn_linear_chunk_bwd", "gdn_qk_norm_fwd",
           "gdn_qk_norm_bwd", "gdn_gated_norm_fwd", "gdn_gated_norm_bwd")
 
 

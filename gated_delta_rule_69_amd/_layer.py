@@ -27,6 +27,10 @@ class GdnLinearArgs(ctypes.Structure):
                 ("s0", _ptr), ("s_final", _ptr), ("o", _ptr)]
 
 
+class GdnLinearGrads(ctypes.Structure):
+    _fields_ = [("dq", _ptr), ("dk", _ptr), ("dv", _ptr), ("ds0", _ptr)]
+
+
 class GdnQkNormArgs(ctypes.Structure):
     _fields_ = [("dtype", _i32), ("norm", _i32), ("B", _i64), ("T", _i64), ("Hq", _i64), ("Hk", _i64),
                 ("d", _i64), ("q_stride", _i64), ("k_stride", _i64), ("rot", _i64), ("n_pos", _i64),
@@ -63,6 +67,8 @@ def _library():
                 ("gdn_linear_workspace_bytes", [la], size),
                 ("gdn_linear_chunk_fwd", [la, _ptr, size, _ptr], ctypes.c_int),
                 ("gdn_linear_recurrent_step", [la, _ptr, _ptr], ctypes.c_int),
+                ("gdn_linear_bwd_workspace_bytes", [la], size),
+                ("gdn_linear_chunk_bwd", [la, _ptr, _ptr, P(GdnLinearGrads), _ptr, size, _ptr], ctypes.c_int),
                 ("gdn_qk_norm_fwd", [qa, _ptr], ctypes.c_int),
                 ("gdn_qk_norm_bwd_workspace_bytes", [qa], size),
                 ("gdn_qk_norm_bwd", [qa, P(GdnQkNormGrads), _ptr, size, _ptr], ctypes.c_int),
@@ -210,6 +216,30 @@ def gdn_linear_recurrent_step(q, k, v, log_decay, *, state, o=None, seq_lens=Non
     a = _linear_args(q, k, v, log_decay, seq_lens, state, None, o)
     _done(_library().gdn_linear_recurrent_step(ctypes.byref(a), a.s0, _stream()), "gdn_linear_recurrent_step")
     return o
+
+
+def gdn_linear_chunk_bwd(q, k, v, log_decay, *, d_o, s0=None, ds_final=None, seq_lens=None, workspace=None,
+                         stream=None):
+    """Gradients of (o, s_final) of gdn_linear_chunk_fwd for upstream d_o (shape and dtype of
+    o) and ds_final (float32 state, optional): {"dq", "dk", "dv"} in the inputs' dtype and
+    "ds0" in float32. Rows behind a sequence's length are zero."""
+    if _elsewhere(v, "v", stream):
+        with _on(v, stream):
+            return gdn_linear_chunk_bwd(q, k, v, log_decay, d_o=d_o, s0=s0, ds_final=ds_final, seq_lens=seq_lens,
+                                        workspace=workspace)
+    lib = _library()
+    args = _linear_args(q, k, v, log_decay, seq_lens, s0, None, None)
+    dev, dtype = v.device, v.dtype
+    state = (args.B, args.H, args.dk, args.dv)
+    up = _whole(d_o, "d_o", v.shape, dtype, dev)
+    up_state = _whole(ds_final, "ds_final", state, torch.float32, dev)
+    out = {"dq": torch.empty(q.shape, dtype=dtype, device=dev), "dk": torch.empty(k.shape, dtype=dtype, device=dev),
+           "dv": torch.empty(v.shape, dtype=dtype, device=dev), "ds0": torch.empty(state, dtype=torch.float32, device=dev)}
+    g = GdnLinearGrads(*(t.data_ptr() for t in out.values()))
+    a = ctypes.byref(args)
+    ws, at, size = _workspace(workspace, lib.gdn_linear_bwd_workspace_bytes(a), "gdn_linear_bwd_workspace_bytes", dev)
+    _done(lib.gdn_linear_chunk_bwd(a, up, up_state, ctypes.byref(g), at, size, _stream()), "gdn_linear_chunk_bwd")
+    return out
 
 
 # ---- norms of queries and keys -----------------------------------------------------------

@@ -9,7 +9,7 @@
 
 namespace gdn {
 
-// Linear attention after validation: strides resolved, segments chosen.
+// Linear attention after validation: strides resolved.
 struct LinearProblem {
   int64_t B, T, H, Hk, dk, dv;
   int64_t group;              // value heads a key head serves
@@ -23,7 +23,15 @@ struct LinearProblem {
   const float* s0;
   float* s_final;
   void* o;
-  int64_t seg, nseg;          // tokens a segment (a multiple of the chunk), segments
+};
+
+struct LinearGrads {
+  const void* d_o;
+  const float* d_s_final;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* ds0;
 };
 
 // Rows of a norm: [tokens][heads][d] with `ld` elements from token to token.
@@ -43,6 +51,8 @@ constexpr int64_t kNormPartials = 1024;
 int launch_linear_step(const LinearProblem& p, float* state, void* stream);
 int launch_linear_fwd(const LinearProblem& p, void* ws, void* stream);
 size_t linear_fwd_workspace(const LinearProblem& p);
+int launch_linear_bwd(const LinearProblem& p, const LinearGrads& g, void* ws, void* stream);
+size_t linear_bwd_workspace(const LinearProblem& p);
 int launch_qk_norm_fwd(const QkNormProblem& p, void* stream);
 int launch_qk_norm_bwd(const QkNormProblem& p, const gdn_qk_norm_grads& g, void* ws, void* stream);
 int launch_gated_norm_fwd(const GatedNormProblem& p, void* stream);

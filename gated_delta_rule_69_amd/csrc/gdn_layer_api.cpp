@@ -146,6 +146,27 @@ int gdn_linear_recurrent_step(const gdn_linear_args* args, float* state_inout, v
   return hip_status(launch_linear_step(p, state_inout, stream));
 }
 
+size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_args* args) {
+  LinearProblem p;
+  return linear_shapes(args, &p) == GDN_OK ? linear_bwd_workspace(p) : 0;
+}
+
+int gdn_linear_chunk_bwd(const gdn_linear_args* args, const void* d_o, const float* d_s_final,
+                         const gdn_linear_grads* grads, void* ws, size_t ws_bytes, void* stream) {
+  LinearProblem p;
+  int st = linear_shapes(args, &p);
+  if (st == GDN_OK) st = linear_pointers(p);
+  if (st != GDN_OK) return st;
+  if (grads == nullptr) return GDN_ERR_ARG;
+  auto need = [&](const void* x) { return p.T == 0 ? aligned16(x) : (x != nullptr && aligned16(x)); };
+  if (!need(d_o) || !need(grads->dq) || !need(grads->dk) || !need(grads->dv)) return GDN_ERR_ARG;
+  if (!aligned16(p.s0) || !aligned16(d_s_final) || !aligned16(grads->ds0)) return GDN_ERR_ARG;
+  if (!ws_ok(ws, ws_bytes, linear_bwd_workspace(p))) return GDN_ERR_WORKSPACE;
+  if (p.T == 0 && grads->ds0 == nullptr) return GDN_OK;
+  const LinearGrads g{d_o, d_s_final, grads->dq, grads->dk, grads->dv, grads->ds0};
+  return hip_status(launch_linear_bwd(p, g, ws, stream));
+}
+
 int gdn_qk_norm_fwd(const gdn_qk_norm_args* args, void* stream) {
   QkNormProblem p;
   int st = qk_norm_check(args, &p);

@@ -301,6 +301,30 @@ int gdn_linear_chunk_fwd(const gdn_linear_args* args, void* ws, size_t ws_bytes,
  * its row of o. No workspace. */
 int gdn_linear_recurrent_step(const gdn_linear_args* args, float* state_inout, void* stream);
 
+/* Gradient outputs of gdn_linear_chunk_bwd, contiguous: dq, dk [B, T, Hk, dk] and dv
+ * [B, T, H, dv] in args->dtype (dq and dk summed over the value heads of a key head);
+ * ds0 [B, H, dk, dv] float32, NULL means not written. Rows behind a sequence's length
+ * are written as zero. */
+typedef struct gdn_linear_grads {
+  void* dq;
+  void* dk;
+  void* dv;
+  float* ds0;
+} gdn_linear_grads;
+
+/* Bytes of device workspace gdn_linear_chunk_bwd needs (0 for an invalid set). */
+size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_args* args);
+
+/* Gradients of o and s_final with respect to q, k, v and s0 (log_decay is a constant of
+ * the model): with d_o [B, T, H, dv] in args->dtype (contiguous) and d_s_final
+ * [B, H, dk, dv] float32 (NULL: zero),
+ *     G_t = e^{g} G_{t+1} + q_t do_t^T  (G after the last token: d_s_final),
+ *     dq_t = S_t do_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds0 = e^{g} G_1.
+ * args->o and args->s_final are ignored. Rows of d_o behind a sequence's length are not
+ * used. ws must hold gdn_linear_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
+int gdn_linear_chunk_bwd(const gdn_linear_args* args, const void* d_o, const float* d_s_final,
+                         const gdn_linear_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- Norms of queries and keys a head, with the position rotation --------------------
  *
  * The delta-rule and linear entry points take q and k as they are (keys of unit norm

@@ -66,6 +66,76 @@ def test_chunk_and_step_against_the_recurrence(case, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("states", [False, True])
+@pytest.mark.parametrize("case", SIZES, ids=lambda c: "-".join(map(str, c)))
+def test_gradients_against_the_recurrence(case, states, dt):
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make(case, dt, 41, fuse=case[1] % 2 == 1)
+    s0, ds = (host["s0"], host["ds"]) if states else (None, None)
+    want = layer.linear_backward(*(f64(host[n]) for n in ("q", "k", "v", "g", "do")), s0=f64(s0), ds_final=f64(ds))
+    print(f"linear backward {case} {dt} states={states}", flush=True)
+    got = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"],
+                                   s0=on["s0"] if states else None, ds_final=on["ds"] if states else None)
+    for name in ("dq", "dk", "dv", "ds0"):
+        check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradients_of_a_padded_batch(dt):
+    """Rows behind a length get zero gradients, whatever d_o holds there."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    host, on = make((5, 150, 4, 2, 64, 32), dt, 42)
+    lens = [150, 0, 64, 97, -1]
+    for t in (host, on):
+        for b, n in enumerate(lens):
+            t["do"][b, max(n, 0):] = float("nan")
+    want = layer.linear_backward(*(f64(host[n]) for n in ("q", "k", "v", "g", "do")), s0=f64(host["s0"]),
+                                 ds_final=f64(host["ds"]), lens=lens)
+    got = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"], ds_final=on["ds"],
+                                   seq_lens=torch.tensor(lens, dtype=torch.int32, device=dev()))
+    for name in ("dq", "dk", "dv", "ds0"):
+        check(got[name], want[name], name)
+        if name != "ds0":
+            for b, n in enumerate(lens):
+                assert (got[name][b, max(n, 0):] == 0).all(), name
+    assert torch.equal(got["ds0"][1], on["ds"][1]) and torch.equal(got["ds0"][4], on["ds"][4])
+
+
+def test_gradients_at_extreme_decays_and_of_no_tokens():
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    host, on = make((1, 150, 4, 4, 32, 32), "f32", 43)
+    host["g"] = torch.tensor([0.0, -50.0, -200.0, float("-inf")])
+    on["g"] = host["g"].to(dev())
+    want = layer.linear_backward(*(f64(host[n]) for n in ("q", "k", "v", "g", "do")), s0=f64(host["s0"]), ds_final=f64(host["ds"]))
+    got = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"], ds_final=on["ds"])
+    for name in ("dq", "dk", "dv", "ds0"):
+        check(got[name], want[name], name)
+    none = {n: on[n][:, :0].contiguous() for n in ("q", "k", "v", "do")}
+    got = gdn.gdn_linear_chunk_bwd(none["q"], none["k"], none["v"], on["g"], d_o=none["do"], s0=on["s0"], ds_final=on["ds"])
+    assert got["dq"].numel() == 0 and torch.equal(got["ds0"], on["ds"])
+
+
+def test_long_sequence_of_many_segments():
+    """One head over thousands of tokens: many segments of one state, odd at the end."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, f64
+    host, on = make((1, 5003, 1, 1, 32, 32), "bf16", 44)
+    host["g"] = on["g"] = torch.tensor([-0.002], device=on["q"].device)
+    S0 = on["s0"].clone()
+    o_ref, S_ref = ref(host, s0=f64(host["s0"]))
+    o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=S0, s_final=S0)   # the state in place
+    check(o, o_ref, "o")
+    check(S, S_ref, "s_final")
+    want = layer.linear_backward(*(f64(host[n]) for n in ("q", "k", "v", "g", "do")), s0=f64(host["s0"]), ds_final=f64(host["ds"]))
+    got = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"], ds_final=on["ds"])
+    for name in ("dq", "dk", "dv", "ds0"):
+        check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_padded_batch_leaves_what_lies_behind(dt):
     import gated_delta_rule_69_amd as gdn
     from layer_util import check, dev, f64
@@ -198,8 +268,18 @@ def test_another_stream_and_a_captured_graph():
     with torch.cuda.graph(graph):
         gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], o=out, s_final=S)
         so = gdn.gdn_linear_recurrent_step(*step, on["g"], state=state)
+    grads = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"])
+    bwd = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(bwd):
+        caught = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"])
     eager = on["s0"].clone()
     for _ in range(3):
+        for t in caught.values():
+            t.zero_()
+        bwd.replay()
+        torch.cuda.synchronize()
+        for name in grads:
+            assert torch.equal(caught[name], grads[name]), name
         out.zero_(), S.zero_()
         graph.replay()
         torch.cuda.synchronize()

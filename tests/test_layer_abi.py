@@ -79,6 +79,22 @@ def test_linear_workspace_and_state_checks(lib):
     assert lib.gdn_linear_recurrent_step(linear(**none), FAKE, None) == 0
 
 
+def test_linear_backward_checks(lib):
+    from gated_delta_rule_69_amd._layer import GdnLinearGrads
+    full = dict(dq=FAKE, dk=FAKE, dv=FAKE, ds0=FAKE)
+    need = lib.gdn_linear_bwd_workspace_bytes(linear())
+    call = lambda a=None, n=need, ws=FAKE, do=FAKE, ds=None, **over: lib.gdn_linear_chunk_bwd(  # noqa: E731
+        a or linear(), do, ds, ctypes.byref(GdnLinearGrads(**{**full, **over})), ws, n, None)
+    assert need > 0 and lib.gdn_linear_bwd_workspace_bytes(linear(dk=48)) == 0
+    assert call(n=need - 1) == -3 and call(ws=None) == -3 and call(ws=FAKE + 16) == -3
+    assert call(do=None) == -1 and call(do=FAKE + 2) == -1 and call(ds=FAKE + 8) == -1
+    for field in ("dq", "dk", "dv"):
+        assert call(**{field: 0}) == -1 and call(**{field: FAKE + 4}) == -1
+    assert call(ds0=FAKE + 4) == -1 and call(a=linear(s0=FAKE + 4)) == -1 and call(a=linear(log_decay=0)) == -1
+    assert lib.gdn_linear_chunk_bwd(linear(), FAKE, None, None, FAKE, need, None) == -1
+    assert call(a=linear(T=0, q=0, k=0, v=0), ds0=0, do=None, dq=0, dk=0, dv=0) == 0
+
+
 @pytest.mark.parametrize("field,value,status", [
     ("dtype", 3, -1), ("norm", 0, -1), ("norm", 3, -1), ("interleaved", 2, -1), ("eps", -1.0, -1),
     ("eps", float("nan"), -1), ("q_scale", float("inf"), -1), ("B", 0, -1), ("Hq", 0, -1), ("Hk", 0, -1), ("d", 80, -2),
