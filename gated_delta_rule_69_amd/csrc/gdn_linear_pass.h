@@ -19,7 +19,7 @@
 // products are 2.7 times as fast as the float32 MFMA here.
 //
 // One workgroup runs one segment of a head. Its waves share the chunk's tiles in LDS and
-// split the DC columns of the state, whose slice a wave keeps in accumulators: an
+// split the DC columns of the state, sixteen a wave, which it keeps in accumulators: an
 // accumulator tile is, register for register, the operand of the next chunk's a X, with
 // its rows spread so that eight consecutive channels of `a` are one 16-byte LDS read.
 // Operands with positions as the summed index are read transposed (ds_read_b64_tr_b16).
@@ -72,18 +72,24 @@ template <typename E> struct PassShape {
   static constexpr int kScoreParts = kHalf ? 2 : 3; // parts of the scores and of the state
   static constexpr int kChunk = kHalf ? 64 : 32;
 };
-constexpr int pass_waves(int DC) { return DC >= 64 ? 4 : DC / 16; }
+constexpr int pass_waves(int DC) { return DC / 16; }  // sixteen columns of the state a wave
 
-// x[0..N) as PARTS sums of bf16: part[p][i].
+// x[0..N) as sums of PARTS bf16 values part[p][i], two at a time: one packed conversion,
+// and what is left by subtracting its halves, which are floats but for their position.
 template <int PARTS, int N>
 __device__ __forceinline__ void split_parts(const float* x, vec<__bf16, N>* part) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float rest = x[i];
+  for (int i = 0; i < N; i += 2) {
+    float2v rest = {x[i], x[i + 1]};
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-      part[p][i] = __bf16(rest);
-      if (p + 1 < PARTS) rest -= float(part[p][i]);
+      const bhalf2 r = __builtin_convertvector(rest, bhalf2);
+      part[p][i] = r[0], part[p][i + 1] = r[1];
+      if (p + 1 < PARTS) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, r);
+        rest[0] -= __uint_as_float(u << 16);
+        rest[1] -= __uint_as_float(u & 0xffff0000u);
+      }
     }
   }
 }
@@ -107,52 +113,108 @@ __device__ __forceinline__ bhalf4 read_tr(const __bf16* p) {
 }
 __device__ __forceinline__ bhalf8 join(bhalf4 lo, bhalf4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-// A tile of C rows of D channels: PARTS planes of rows padded by 16 bytes, so that sixteen
-// rows start in sixteen different groups of banks.
+// A tile of C rows of D channels, PARTS planes of 16-byte slots. Slot c of a row lies at
+// c ^ turn(row): sixteen rows' reads of one slot, and a transposed read's four rows of
+// four slots, then fall into sixteen different groups of banks.
 template <int C, int D, int PARTS> struct Tile {
-  static constexpr int kLd = D + 8;
-  static constexpr int kPlane = C * kLd;
-  __bf16 x[PARTS * kPlane];
+  static constexpr int kSlots = D / 8;
+  static constexpr int kPlane = C * D;
+  __align__(16) __bf16 x[PARTS * kPlane];
 
+  __device__ static __forceinline__ int turn(int row) {
+    if constexpr (kSlots == 16) return (row & 3) << 2 | (row >> 2 & 3);
+    if constexpr (kSlots == 8) return (row & 2) << 1 | (row >> 2 & 3);
+    if constexpr (kSlots == 4) return row >> 2 & 3;
+    return row >> 3 & 1;
+  }
+  // place of channels col .. col+3 (or a whole slot) of a row
+  __device__ static __forceinline__ int place(int row, int col) {
+    return row * D + ((col / 8) ^ turn(row)) * 8 + (col & 4);
+  }
   // rows 16 r + i, channels of k-block kb: the order of the state's accumulator tiles
   __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int i, int g) const {
-    const __bf16* at = x + p * kPlane + (16 * r + i) * kLd;
+    const __bf16* at = x + p * kPlane + 16 * r * D;
     if constexpr (D == 16) {
-      const bhalf4 lo = *reinterpret_cast<const bhalf4*>(at + 4 * g);
-      return join(lo, bhalf4{});
+      return join(*reinterpret_cast<const bhalf4*>(at + place(i, 4 * g)), bhalf4{});
     } else {
-      return *reinterpret_cast<const bhalf8*>(at + 32 * kb + 8 * g);
+      return *reinterpret_cast<const bhalf8*>(at + place(i, 32 * kb + 8 * g));
     }
   }
-  // positions 32 kb + 8 g + e of channel `column` + (i % 4) + step (i / 4), read transposed
+  // positions 32 kb + 8 g + e of channel `column` + (i / 4) step + i % 4, read transposed
   __device__ __forceinline__ bhalf8 columns(int p, int kb, int column, int step, int i, int g) const {
-    const __bf16* at = x + p * kPlane + (32 * kb + 8 * g + i / 4) * kLd + column + (i % 4) * step;
-    return join(read_tr(at), read_tr(at + 4 * kLd));
+    const __bf16* at = x + p * kPlane + 32 * kb * D;
+    const int row = 8 * g + i / 4, col = column + (i % 4) * step;
+    return join(read_tr(at + place(row, col)), read_tr(at + place(row + 4, col)));
+  }
+  __device__ __forceinline__ void put4(int p, int row, int col, bhalf4 v) {
+    *reinterpret_cast<bhalf4*>(x + p * kPlane + place(row, col)) = v;
+  }
+};
+
+// The masked scores of a chunk: of 64 positions, the first half's rows hold 32 columns.
+template <int C, int PARTS> struct Scores {
+  Tile<32, 32, PARTS> first;
+  Tile<C == 64 ? 32 : 1, 64, PARTS> second;
+  __device__ __forceinline__ void put4(int p, int row, int col, bhalf4 v) {
+    if (C == 64 && row >= 32) second.put4(p, row - 32, col, v);
+    else first.put4(p, row, col, v);
+  }
+  __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int i, int g) const {
+    return r < 2 ? first.row(p, r, kb, i, g) : second.row(p, r - 2, kb, i, g);
   }
 };
 
 template <typename E, int DA, int DC, bool OUT> struct PassShared {
   using S = PassShape<E>;
   static constexpr int C = S::kChunk;
-  Tile<C, DA, S::kParts> b;
-  Tile<C, DC, S::kParts> c;
+  Tile<C, DA, S::kParts> b[S::kHalf ? 2 : 1];
+  Tile<C, DC, S::kParts> c[S::kHalf && !OUT ? 2 : 1];
   Tile<OUT ? C : 1, DA, S::kParts> a;
-  Tile<OUT ? C : 1, C, S::kScoreParts> scores;
-  float end_weight[C];   // l^{n-1-j+shift}
-  int bad_from[DC];      // first position of the chunk whose c is not finite, a channel
-  int bad;
+  Scores<OUT ? C : 1, S::kScoreParts> scores;
+  float end_weight[2][C];   // l^{n-1-j+shift}
+  int bad_from[DC];         // first position of the chunk whose c is not finite, a channel
 };
 
-// Vectors of 16 bytes of a tile, held between their load and their store to LDS.
-template <typename E, int C, int D, int NT> struct Staged {
-  static constexpr int kPerRow = D * int(sizeof(E)) / 16;
+// A tile's way from memory to LDS. Rows 0 .. rows-1 come from `base` on, `step` bytes apart
+// (the last first, going backwards); the others are zero: their offsets lie outside the
+// range. Token strides are at most 2^24 elements, so a tile's offsets fit in 31 bits.
+//
+// bf16 rows go straight to LDS (buffer_load_dwordx4 ... lds: lane l's 16 bytes land at the
+// wave's base + 16 l, so the tile's slots are chosen by where a lane loads from). The
+// loads are written as assembly, which has no registers to guard and leaves the waiting to
+// wait_loads(); the compiler's own counts only ever wait for more.
+template <int C, int D, int NT, bool REV>
+__device__ __forceinline__ void load_direct(Tile<C, D, 1>& t, const __bf16* base, uint32_t step, int rows) {
+  typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+  constexpr int kSlots = D / 8, kAll = C * kSlots;
+  const uint64_t from = reinterpret_cast<uintptr_t>(base);
+  const uint4v range = {uint32_t(from), uint32_t(from >> 32) & 0xffffu, uint32_t(rows - 1) * step + 2 * D, 0x00020000u};
+  const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) __bf16*)(t.x)));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+#pragma unroll
+  for (int n = 0; n < (kAll + NT - 1) / NT; ++n) {
+    const int first = n * NT + 64 * wave;
+    if (kAll % NT != 0 && first >= kAll) break;
+    const uint32_t at = first + threadIdx.x % 64, row = at / kSlots, slot = at % kSlots ^ t.turn(row);
+    const uint32_t offset = (REV ? uint32_t(rows - 1) - row : row) * step + slot * 16;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds + 16 * first), "v"(offset), "s"(range) : "memory", "m0");
+  }
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// float32 rows pass through registers, where they become three bf16 planes.
+template <int C, int D, int NT> struct Staged {
+  static constexpr int kPerRow = D / 4;
   static constexpr int kCount = (C * kPerRow + NT - 1) / NT;
   uint4 v[kCount];
-  __device__ __forceinline__ void load(const E* base, int64_t step, int rows) {
+  template <bool REV>
+  __device__ __forceinline__ void load(const float* base, uint32_t step, int rows) {
+    const auto range = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), 0, uint32_t(rows - 1) * step + 4 * D, 0x00020000);
 #pragma unroll
     for (int n = 0; n < kCount; ++n) {
-      const int at = threadIdx.x + n * NT, row = at / kPerRow, col = at % kPerRow;
-      v[n] = row < rows ? *reinterpret_cast<const uint4*>(base + row * step + col * (16 / sizeof(E))) : uint4{0, 0, 0, 0};
+      const uint32_t at = threadIdx.x + n * NT, row = at / kPerRow, col = at % kPerRow;
+      v[n] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(range, (REV ? uint32_t(rows - 1) - row : row) * step + col * 16, 0, 0));
     }
   }
   template <int PARTS>
@@ -161,52 +223,38 @@ template <typename E, int C, int D, int NT> struct Staged {
     for (int n = 0; n < kCount; ++n) {
       const int at = threadIdx.x + n * NT, row = at / kPerRow, col = at % kPerRow;
       if (C * kPerRow % NT != 0 && row >= C) break;
-      if constexpr (sizeof(E) == 2) {
-        *reinterpret_cast<uint4*>(t.x + row * t.kLd + col * 8) = v[n];
-      } else {
-        const float f[4] = {__uint_as_float(v[n].x), __uint_as_float(v[n].y), __uint_as_float(v[n].z), __uint_as_float(v[n].w)};
-        bhalf4 part[PARTS];
-        split_parts<PARTS, 4>(f, part);
+      const float f[4] = {__uint_as_float(v[n].x), __uint_as_float(v[n].y), __uint_as_float(v[n].z), __uint_as_float(v[n].w)};
+      bhalf4 part[PARTS];
+      split_parts<PARTS, 4>(f, part);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) *reinterpret_cast<bhalf4*>(t.x + p * t.kPlane + row * t.kLd + col * 4) = part[p];
-      }
-    }
-  }
-  // Marks channels with a NaN or Inf: a masked score is 0, but 0 times Inf is not.
-  __device__ __forceinline__ void mark_bad(int* bad, int* bad_from) const {
-    constexpr uint32_t kExp = sizeof(E) == 2 ? 0x7f807f80u : 0x7f800000u, kOne = sizeof(E) == 2 ? 0x00800080u : 0x00800000u,
-                       kTop = sizeof(E) == 2 ? 0x80008000u : 0x80000000u;
-#pragma unroll
-    for (int n = 0; n < kCount; ++n) {
-      const uint32_t w[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
-      const uint32_t any = (((w[0] & kExp) + kOne) | ((w[1] & kExp) + kOne) | ((w[2] & kExp) + kOne) | ((w[3] & kExp) + kOne)) & kTop;
-      if (any == 0) continue;
-      const int at = threadIdx.x + n * NT, row = at / kPerRow, col = at % kPerRow;
-      *bad = 1;
-      for (int e = 0; e < int(16 / sizeof(E)); ++e) {
-        const uint32_t x = sizeof(E) == 2 ? w[e / 2] >> (16 * (e % 2)) & 0x7f80u : w[e] >> 16 & 0x7f80u;
-        if (x == 0x7f80u) atomicMin(&bad_from[col * int(16 / sizeof(E)) + e], row);
-      }
+      for (int p = 0; p < PARTS; ++p) t.put4(p, row, 4 * col, part[p]);
     }
   }
 };
 
+// Whether one of eight bf16 values is a NaN or Inf.
+__device__ __forceinline__ bool any_bad(bhalf8 x) {
+  typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+  const uint4v w = (__builtin_bit_cast(uint4v, x) & 0x7f807f80u) + 0x00800080u;
+  return ((w[0] | w[1] | w[2] | w[3]) & 0x80008000u) != 0;
+}
+__device__ __forceinline__ bool is_bad(__bf16 x) { return (__builtin_bit_cast(uint16_t, x) & 0x7f80u) == 0x7f80u; }
+
 // OUT: outputs, from the state before the segment. Otherwise the states after the segments
 // 0 .. nseg-2, each from zero (the first from x0), for scan_states to join.
 template <typename E, typename O, int DA, int DC, bool REV, bool OUT>
-__global__ __launch_bounds__(64 * pass_waves(DC)) void linear_pass_kernel(LinearPass s) {
+__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_pass_kernel(LinearPass s) {
   using S = PassShape<E>;
   constexpr int C = S::kChunk, NW = pass_waves(DC), NT = 64 * NW;
   constexpr int P = S::kParts, PS = S::kScoreParts;
   constexpr int RT = C / 16;          // row tiles of a chunk
-  constexpr int KT = DA / 16;         // state tiles along DA
+  constexpr int KT = DA / 16;         // state tiles of a wave
   constexpr int KB = (DA + 31) / 32;  // k-blocks along DA
-  constexpr int CT = DC / 16 / NW;    // state tiles of a wave along DC
   constexpr int PB = C / 32;          // k-blocks of positions
-  constexpr int kColStep = CT == 2 ? 8 : 4;  // channels between a wave's runs of four columns
   __shared__ PassShared<E, DA, DC, OUT> sh;
 
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, i = lane % 16, g = lane / 16;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  int i = lane % 16, g = lane / 16;
   const int h = int(blockIdx.x) % s.H;
   const int64_t bs = int64_t(blockIdx.x) / s.H;
   const int segs = OUT ? s.nseg : s.nseg - 1;
@@ -215,201 +263,224 @@ __global__ __launch_bounds__(64 * pass_waves(DC)) void linear_pass_kernel(Linear
   const int64_t bh = b * s.H + h;
   const int64_t n = length_of(s.seq_lens, b, s.T);
   const float lg = head_log_decay(s.log_decay, h) * 1.44269504088896341f;  // log2
-  auto power = [&](int m) { return __builtin_amdgcn_exp2f(lg * float(m)); };
+  float lg_now = lg;
+  auto power = [&](int m) { return __builtin_amdgcn_exp2f(lg_now * float(m)); };
 
   const int64_t begin = seg * s.seg;
   const int64_t last = begin + s.seg < s.T ? begin + s.seg : s.T;   // positions of the segment, real or not
   const int64_t end = last < n ? last : n;
-  constexpr int kDir = REV ? -1 : 1;
-  // rows of position p: token p, or n - 1 - p backwards
-  auto rows = [&](const void* x, int64_t ld, int group, int d, int64_t p) {
-    return static_cast<const E*>(x) + (b * s.T + (REV ? n - 1 - p : p)) * ld + int64_t(h / group) * d;
+  // first token in memory of positions p .. p + m - 1: token p, or n - m - p backwards
+  auto rows = [&](const void* x, int64_t ld, int group, int d, int64_t p, int m) {
+    return static_cast<const E*>(x) + (b * s.T + (REV ? n - m - p : p)) * ld + int64_t(h / group) * d;
   };
-  // channel of the state's row e of tile kt, and of its column of tile ct
+  // a lane's first channel in state tile kt (four rows), and its column
   auto row_channel = [&](int kt) { return KT == 1 ? 4 * g : 32 * (kt / 2) + 8 * g + 4 * (kt % 2); };
-  auto col_channel = [&](int ct) { return 16 * CT * wave + kColStep * (i / 4) + 4 * ct + i % 4; };
+  const int column = 16 * wave + i;
 
-  // the state of the wave's columns
-  float4v X[KT][CT];
-  // The outputs' pass takes x0 from slot 0 where there are several segments: x1 may be x0
-  // itself, and the last segment's workgroup may end before the first one's begins.
+  // The state of the wave's columns. The outputs' pass takes x0 from slot 0 where there are
+  // several segments: x1 may be x0 itself, and the last segment's workgroup may end before
+  // the first one's begins.
+  float4v X[KT];
   float* slots = s.states + bh * s.nseg * (DA * DC);
   const bool given = seg > 0 ? OUT : s.x0 != nullptr;
   const bool direct = seg == 0 && (!OUT || s.nseg == 1);
   const float* from = !given ? nullptr : direct ? s.x0 + bh * (DA * DC) : slots + seg * (DA * DC);
   const int64_t sa = direct ? s.x0_sa : s.st_sa, sc = direct ? s.x0_sc : s.st_sc;
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+  for (int kt = 0; kt < KT; ++kt) {
+    if (from == nullptr) {
+      X[kt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    } else if (sa == 1) {
+      X[kt] = *reinterpret_cast<const float4v*>(from + row_channel(kt) + column * sc);
+    } else {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      if (from == nullptr) {
-        X[kt][ct] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-      } else if (sa == 1) {
-        X[kt][ct] = *reinterpret_cast<const float4v*>(from + row_channel(kt) + col_channel(ct) * sc);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) X[kt][ct][e] = from[(row_channel(kt) + e) * sa + col_channel(ct) * sc];
-      }
+      for (int e = 0; e < 4; ++e) X[kt][e] = from[(row_channel(kt) + e) * sa + column * sc];
     }
-
+  }
   auto store_state = [&](float* to, int64_t ta, int64_t tc) {
     if (to == nullptr) return;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt) {
+      if (ta == 1) {
+        *reinterpret_cast<float4v*>(to + row_channel(kt) + column * tc) = X[kt];
+      } else {
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        if (ta == 1) {
-          *reinterpret_cast<float4v*>(to + row_channel(kt) + col_channel(ct) * tc) = X[kt][ct];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[(row_channel(kt) + e) * ta + col_channel(ct) * tc] = X[kt][ct][e];
-        }
+        for (int e = 0; e < 4; ++e) to[(row_channel(kt) + e) * ta + column * tc] = X[kt][e];
       }
+    }
   };
   if (!OUT && seg == 0 && given) store_state(slots, s.st_sa, s.st_sc);
 
-  Staged<E, C, DA, NT> ra, rb;
-  Staged<E, C, DC, NT> rc;
-  auto fetch = [&](int64_t p) {
-    const int m = int(end - p < C ? end - p : C);
-    if constexpr (OUT) ra.load(rows(s.a, s.lda, s.group_a, DA, p), kDir * s.lda, m);
-    rb.load(rows(s.b, s.ldb, s.group_b, DA, p), kDir * s.ldb, m);
-    rc.load(rows(s.c, s.ldc, s.group_c, DC, p), kDir * s.ldc, m);
+  constexpr bool kDirect = S::kHalf;
+  [[maybe_unused]] Staged<C, DA, NT> ra, rb;
+  [[maybe_unused]] Staged<C, DC, NT> rc;
+  auto size = [&](int64_t p) { return int(end - p < C ? end - p : C); };  // positions of the chunk at p
+  // the ways of the tiles of the chunk at p; bf16 ones land in `buf` of their buffers
+  auto fetch_a = [&](int64_t p) {
+    [[maybe_unused]] const E* from = rows(s.a, s.lda, s.group_a, DA, p, size(p));
+    if constexpr (!OUT) return;
+    else if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.a, from, uint32_t(s.lda * 2), size(p));
+    else ra.template load<REV>(from, uint32_t(s.lda * 4), size(p));
   };
-  if (begin < end) fetch(begin);
-  if constexpr (OUT) {
-    for (int at = threadIdx.x; at < DC; at += NT) sh.bad_from[at] = C;
-    if (threadIdx.x == 0) sh.bad = 0;
-    __syncthreads();
+  auto fetch_b = [&](int64_t p, int buf) {
+    const E* from = rows(s.b, s.ldb, s.group_b, DA, p, size(p));
+    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.b[buf], from, uint32_t(s.ldb * 2), size(p));
+    else rb.template load<REV>(from, uint32_t(s.ldb * 4), size(p));
+  };
+  auto fetch_c = [&](int64_t p, int buf) {
+    const E* from = rows(s.c, s.ldc, s.group_c, DC, p, size(p));
+    if constexpr (kDirect) load_direct<C, DC, NT, REV>(sh.c[buf], from, uint32_t(s.ldc * 2), size(p));
+    else rc.template load<REV>(from, uint32_t(s.ldc * 4), size(p));
+  };
+  // Order of a chunk's loads and barriers.
+  //   bf16 outputs: `a` and `b` are there at the start of a chunk; `c` arrives while scores
+  //     and a X are formed, the next `a` (its tile is read no more) and `b` (the other
+  //     buffer) while the chunk's rows are summed. Two workgroups fit a CU.
+  //   bf16 states: both tiles of the next chunk arrive during this one.
+  //   float32: the next chunk's rows wait in registers.
+  if (begin < end) {
+    if constexpr (OUT) fetch_a(begin);
+    fetch_b(begin, 0);
+    if constexpr (!kDirect || !OUT) fetch_c(begin, 0);
+    if constexpr (kDirect && OUT) {
+      wait_loads();
+      __syncthreads();
+    }
   }
 
+  int buf = 0;
   for (int64_t p = begin; p < end; p += C) {
-    const int m = int(end - p < C ? end - p : C);  // positions of the chunk
-    if constexpr (OUT) {
-      ra.store(sh.a);
-      rc.mark_bad(&sh.bad, sh.bad_from);
+    const int m = size(p);
+    const bool more = p + C < end;
+    // opaque in every chunk: powers and LDS addresses are formed where they are used, not held
+    asm volatile("" : "+v"(lg_now), "+v"(i), "+v"(g));
+    if constexpr (!kDirect) {
+      if constexpr (OUT) ra.store(sh.a);
+      rb.store(sh.b[0]);
+      rc.store(sh.c[0]);
+    } else if constexpr (OUT) {
+      fetch_c(p, 0);
+    } else {
+      wait_loads();
     }
-    rb.store(sh.b);
-    rc.store(sh.c);
     if (threadIdx.x < C) {
       const int left = m - 1 - int(threadIdx.x);
-      sh.end_weight[threadIdx.x] = left >= 0 ? power(left + s.shift) : 0.0f;
+      sh.end_weight[buf][threadIdx.x] = left >= 0 ? power(left + s.shift) : 0.0f;
     }
-    __syncthreads();
-    if (p + C < end) fetch(p + C);
+    if constexpr (!kDirect || !OUT) __syncthreads();
+    if constexpr (!kDirect) {
+      if (more) {
+        if constexpr (OUT) fetch_a(p + C);
+        fetch_b(p + C, 0);
+        fetch_c(p + C, 0);
+      }
+    } else if constexpr (!OUT) {
+      if (more) fetch_b(p + C, buf ^ 1), fetch_c(p + C, buf ^ 1);
+    }
+    Tile<C, DA, P>& tb = sh.b[kDirect ? buf : 0];
+    Tile<C, DC, P>& tc = sh.c[kDirect && !OUT ? buf : 0];
 
-    float4v acc[OUT ? RT : 1][CT];
+    float4v acc[OUT ? RT : 1];
     if constexpr (OUT) {
-      // scores, transposed: column i of a tile is position 16 r + i, its rows positions 16 jt + 4 g + e
-      for (int r = wave; r < RT; r += NW) {
-        bhalf8 av[KB][P];
+      // Scores, transposed: column i of tile (r, jt) is position 16 r + i, its rows are
+      // positions 16 jt + 4 g + e. The tiles at and under the diagonal go round the waves,
+      // then those right of it that a k-block of 32 positions reads as zeros.
+      constexpr int kLower = RT * (RT + 1) / 2;
+      for (int t = wave; t < kLower + RT / 2; t += NW) {
+        int r = 0, jt = t;
+        float x[4] = {};
+        if (t < kLower) {
+          while (jt > r) jt -= ++r;
+          float4v d{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+          for (int kb = 0; kb < KB; ++kb) {
+            bhalf8 av[P], bv[P];
 #pragma unroll
-          for (int q = 0; q < P; ++q) av[kb][q] = sh.a.row(q, r, kb, i, g);
-#pragma unroll
-        for (int jt = 0; jt < RT; ++jt) {
-          if (jt > (r | 1)) continue;
-          float x[4] = {};
-          if (jt <= r) {
-            float4v t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-              bhalf8 bv[P];
-#pragma unroll
-              for (int q = 0; q < P; ++q) bv[q] = sh.b.row(q, jt, kb, i, g);
-              t = mma_parts<P, P, P - 1>(bv, av[kb], t);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int ahead = 16 * r + i - (16 * jt + 4 * g + e);
-              x[e] = ahead >= 0 ? t[e] * power(ahead) : 0.0f;
-            }
+            for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g), bv[q] = tb.row(q, jt, kb, i, g);
+            d = mma_parts<P, P, P - 1>(bv, av, d);
           }
-          bhalf4 part[PS];
-          split_parts<PS, 4>(x, part);
 #pragma unroll
-          for (int q = 0; q < PS; ++q)
-            *reinterpret_cast<bhalf4*>(sh.scores.x + q * sh.scores.kPlane + (16 * r + i) * sh.scores.kLd + 16 * jt + 4 * g) = part[q];
+          for (int e = 0; e < 4; ++e) {
+            const int ahead = 16 * r + i - (16 * jt + 4 * g + e);
+            x[e] = ahead >= 0 ? d[e] * power(ahead) : 0.0f;
+          }
+        } else {
+          r = 2 * (t - kLower), jt = r + 1;
         }
+        bhalf4 part[PS];
+        split_parts<PS, 4>(x, part);
+#pragma unroll
+        for (int q = 0; q < PS; ++q)
+          sh.scores.put4(q, 16 * r + i, 16 * jt + 4 * g, part[q]);
       }
       // what the state before the chunk gives
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[r][ct] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r = 0; r < RT; ++r) acc[r] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        bhalf8 xv[CT][PS];
+        float x[8];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = X[2 * kb][ct][e];
-            x[4 + e] = KT > 1 ? X[KT > 1 ? 2 * kb + 1 : 0][ct][e] : 0.0f;
-          }
-          split_parts<PS, 8>(x, xv[ct]);
+        for (int e = 0; e < 4; ++e) {
+          x[e] = X[2 * kb][e];
+          x[4 + e] = KT > 1 ? X[KT > 1 ? 2 * kb + 1 : 0][e] : 0.0f;
         }
+        bhalf8 xv[PS];
+        split_parts<PS, 8>(x, xv);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           bhalf8 av[P];
 #pragma unroll
           for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[r][ct] = mma_parts<PS, P, PS - 1>(xv[ct], av, acc[r][ct]);
+          acc[r] = mma_parts<PS, P, PS - 1>(xv, av, acc[r]);
         }
       }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float w = power(16 * r + i + 1 - s.shift);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[r][ct] *= w;
-      }
+      for (int r = 0; r < RT; ++r) acc[r] *= power(16 * r + i + 1 - s.shift);
+      if constexpr (kDirect) wait_loads();
       __syncthreads();
+      if constexpr (kDirect) {
+        if (more) fetch_a(p + C), fetch_b(p + C, buf ^ 1);
+      }
     }
 
     // what the chunk's own rows give, and the state after it
-    const int bad = OUT ? sh.bad : 0;
+    bool bad = false;
     const float whole = power(m);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) X[kt][ct] *= whole;
+    for (int kt = 0; kt < KT; ++kt) X[kt] *= whole;
 #pragma unroll
     for (int kb = 0; kb < PB; ++kb) {
-      bhalf8 wv[CT][3];
-      float w[8];
+      bhalf8 cv[P], wv[3];
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = sh.end_weight[32 * kb + 8 * g + e];
+      for (int q = 0; q < P; ++q) {
+        cv[q] = tc.columns(q, kb, 16 * wave, 4, i, g);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        bhalf8 cv[P];
-        float x[8] = {};
+        for (int e = 0; e < 8; ++e) x[e] = q == 0 ? float(cv[q][e]) : x[e] + float(cv[q][e]);
+      }
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-          cv[q] = sh.c.columns(q, kb, 16 * CT * wave + 4 * ct, kColStep, i, g);
+      for (int e = 0; e < 8; ++e) x[e] *= sh.end_weight[buf][32 * kb + 8 * g + e];
+      split_parts<3, 8>(x, wv);
+      if constexpr (OUT) {
+        // A masked score is 0, but 0 times Inf is not: such values leave the product, and the
+        // rows from theirs on become NaN.
+        if (__builtin_expect(__any(any_bad(cv[0])), 0)) {
+          if (!bad && g == 0) sh.bad_from[column] = C;
+          bad = true;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += float(cv[q][e]);
+          for (int e = 0; e < 8; ++e) {
+            if (!is_bad(cv[0][e])) continue;
+            atomicMin(&sh.bad_from[column], 32 * kb + 8 * g + e);
+#pragma unroll
+            for (int q = 0; q < P; ++q) cv[q][e] = __bf16(0.0f);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= w[e];
-        split_parts<3, 8>(x, wv[ct]);
-        if constexpr (OUT) {
-          if (bad) {
+        for (int r = 2 * kb; r < RT; ++r) {
+          bhalf8 sv[PS];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if ((__builtin_bit_cast(uint16_t, (__bf16)cv[0][e]) & 0x7f80u) == 0x7f80u)
-#pragma unroll
-                for (int q = 0; q < P; ++q) cv[q][e] = __bf16(0.0f);
-          }
-#pragma unroll
-          for (int r = 2 * kb; r < RT; ++r) {
-            bhalf8 sv[PS];
-#pragma unroll
-            for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, i, g);
-            acc[r][ct] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r][ct]);
-          }
+          for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, i, g);
+          acc[r] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r]);
         }
       }
 #pragma unroll
@@ -417,42 +488,31 @@ __global__ __launch_bounds__(64 * pass_waves(DC)) void linear_pass_kernel(Linear
         bhalf8 bv[P];
 #pragma unroll
         for (int q = 0; q < P; ++q)
-          bv[q] = sh.b.columns(q, kb, KT == 1 ? 0 : 32 * (kt / 2) + 4 * (kt % 2), KT == 1 ? 4 : 8, i, g);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) X[kt][ct] = mma_parts<P, 3, 2>(bv, wv[ct], X[kt][ct]);
+          bv[q] = tb.columns(q, kb, KT == 1 ? 0 : 32 * (kt / 2) + 4 * (kt % 2), KT == 1 ? 4 : 8, i, g);
+        X[kt] = mma_parts<P, 3, 2>(bv, wv, X[kt]);
       }
     }
 
     if constexpr (OUT) {
+      if constexpr (kDirect) wait_loads();
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int at = 16 * r + i;
         if (at < m) {
           const int64_t token = b * s.T + (REV ? n - 1 - p - at : p + at);
-          const int ch = 16 * CT * wave + 4 * CT * g;
-          float x[4 * CT];
+          const int ch = 16 * wave + 4 * g;
+          float x[4] = {acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+          if (__builtin_expect(bad, 0)) {
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[4 * ct + e] = acc[r][ct][e];
-              if (bad && at >= sh.bad_from[ch + 4 * ct + e]) x[4 * ct + e] = __builtin_nanf("");
-            }
-          vec<O, 4 * CT> out;
-#pragma unroll
-          for (int e = 0; e < 4 * CT; ++e) out[e] = O(x[e]);
-          *reinterpret_cast<vec<O, 4 * CT>*>(static_cast<O*>(s.out) + (token * s.H + h) * DC + ch) = out;
+            for (int e = 0; e < 4; ++e)
+              if (at >= sh.bad_from[ch + e]) x[e] = __builtin_nanf("");
+          }
+          store4(static_cast<O*>(s.out) + (token * s.H + h) * DC + ch, x);
         }
       }
     }
-    __syncthreads();
-    if constexpr (OUT) {
-      if (bad) {
-        for (int at = threadIdx.x; at < DC; at += NT) sh.bad_from[at] = C;
-        if (threadIdx.x == 0) sh.bad = 0;
-        __syncthreads();
-      }
-    }
+    if constexpr (OUT || !kDirect) __syncthreads();
+    buf ^= 1;
   }
 
   if constexpr (OUT) {

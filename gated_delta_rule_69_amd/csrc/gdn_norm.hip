@@ -272,25 +272,24 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
   }
 }
 
-// out[i][c] = sum over blocks of partial[block][i][c], i = blockIdx.x: 256 threads add up
-// interleaved blocks, then one thread a channel adds the threads' sums.
-template <int D>
-__global__ __launch_bounds__(kThreads) void partial_sum_kernel(const float* __restrict__ partial, int blocks, int rows,
-                                                               float* out0, float* out1) {
-  constexpr int N = kThreads / D;
-  const int c = threadIdx.x % D, n = threadIdx.x / D;
-  const int row = blockIdx.x;
+// out[i][c] = sum over blocks of partial[block][i][c], a block for 16 channels of one i:
+// 64 threads a channel add up every 64th row, then a tree of fixed order.
+__global__ __launch_bounds__(1024) void partial_sum_kernel(const float* __restrict__ partial, int blocks, int rows, int d,
+                                                           float* out0, float* out1) {
+  const int c = int(blockIdx.x) * 16 % d + threadIdx.x % 16, row = int(blockIdx.x) * 16 / d;
+  const int n = threadIdx.x / 16;
   float s = 0.0f;
-  for (int b = n; b < blocks; b += N) s += partial[(int64_t(b) * rows + row) * D + c];
-  __shared__ float part[kThreads];
+#pragma unroll 8
+  for (int b = n; b < blocks; b += 64) s += partial[(int64_t(b) * rows + row) * d + c];
+  __shared__ float part[1024];
   part[threadIdx.x] = s;
-  __syncthreads();
-  float* out = row == 0 ? out0 : out1;
-  if (n == 0 && out != nullptr) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) s += part[i * D + c];
-    out[c] = s;
+  for (int step = 512; step >= 16; step /= 2) {
+    __syncthreads();
+    if (threadIdx.x < step) part[threadIdx.x] += part[threadIdx.x + step];
   }
+  float* out = row == 0 ? out0 : out1;
+  if (threadIdx.x < 16 && out != nullptr) out[c] = part[threadIdx.x];
 }
 
 // Blocks of a launch over `rows` rows, `per_step` at a time, and the rows each takes.
@@ -371,10 +370,8 @@ int launch_gated(GatedNorm n, const GatedNormProblem& p, int64_t most, int64_t* 
 }
 
 int launch_partial_sum(const float* partial, int64_t blocks, int rows, int64_t d, float* out0, float* out1, hipStream_t s) {
-  return by_dim(d, [&](auto dim) {
-    partial_sum_kernel<decltype(dim)::value><<<rows, kThreads, 0, s>>>(partial, int(blocks), rows, out0, out1);
-    return int(hipGetLastError());
-  });
+  partial_sum_kernel<<<unsigned(rows * d / 16), 1024, 0, s>>>(partial, int(blocks), rows, int(d), out0, out1);
+  return int(hipGetLastError());
 }
 
 }  // namespace
