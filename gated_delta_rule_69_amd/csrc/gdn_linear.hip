@@ -127,16 +127,23 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPass s, int per_
   const int64_t n = length_of(s.seq_lens, bh / s.H, s.T);
   const float lg = head_log_decay(s.log_decay, int(bh % s.H));
   float* slot = s.states + bh * s.nseg * per_state + at;
-  float x[4], y[4];
+  float x[4];
   load4(slot + per_state, x);
-  for (int seg = 2; seg < s.nseg; ++seg) {
-    const int64_t left = n - (seg - 1) * s.seg;
-    const int64_t m = left < 0 ? 0 : left > s.seg ? s.seg : left;
-    const float w = expf(lg * float(m));
-    load4(slot + int64_t(seg) * per_state, y);
+  // eight segments' loads at a time: the chain itself is one multiplication and addition each
+  for (int seg = 2; seg < s.nseg; seg += 8) {
+    float y[8][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = y[e] + w * x[e];
-    store4(slot + int64_t(seg) * per_state, x);
+    for (int k = 0; k < 8; ++k)
+      if (seg + k < s.nseg) load4(slot + int64_t(seg + k) * per_state, y[k]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (seg + k >= s.nseg) break;
+      const int64_t left = n - (seg + k - 1) * s.seg;
+      const float w = expf(lg * float(left < 0 ? 0 : left > s.seg ? s.seg : left));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = y[k][e] + w * x[e];
+      store4(slot + int64_t(seg + k) * per_state, x);
+    }
   }
 }
 

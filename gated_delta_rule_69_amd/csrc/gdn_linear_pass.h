@@ -114,18 +114,23 @@ __device__ __forceinline__ bhalf4 read_tr(const __bf16* p) {
 __device__ __forceinline__ bhalf8 join(bhalf4 lo, bhalf4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 // A tile of C rows of D channels, PARTS planes of 16-byte slots. Slot c of a row lies at
-// c ^ turn(row): sixteen rows' reads of one slot, and a transposed read's four rows of
-// four slots, then fall into sixteen different groups of banks.
+// c ^ turn(row), so that the lanes served together by a 16-byte read of rows (measured: rows
+// 0-3 and 12-15 of one k-group with 4-11 of the next) and those of a transposed read (four
+// rows, four slots) fall into different banks: 4.3 cycles a wave's 16-byte read and 4.3 or
+// 2.6 a transposed one, against 8.1 and 4.3 to 8.1 for simpler turns and 32 and 16 for none.
 template <int C, int D, int PARTS> struct Tile {
   static constexpr int kSlots = D / 8;
   static constexpr int kPlane = C * D;
   __align__(16) __bf16 x[PARTS * kPlane];
 
+  // Bits 2 and 3 of the row turn the low two bits of the slot (2 and 3: their sum is 1),
+  // bits 0 and 1 the high ones where a row fills or half fills the banks.
   __device__ static __forceinline__ int turn(int row) {
-    if constexpr (kSlots == 16) return (row & 3) << 2 | (row >> 2 & 3);
-    if constexpr (kSlots == 8) return (row & 2) << 1 | (row >> 2 & 3);
-    if constexpr (kSlots == 4) return row >> 2 & 3;
-    return row >> 3 & 1;
+    if constexpr (kSlots == 2) return row >> 3 & 1;
+    const int low = (row >> 1 & 2) ^ (row >> 3 & 1) * 3;
+    if constexpr (kSlots == 16) return (row & 3) << 2 | low;
+    if constexpr (kSlots == 8) return (row & 2) << 1 | low;
+    return low;
   }
   // place of channels col .. col+3 (or a whole slot) of a row
   __device__ static __forceinline__ int place(int row, int col) {
