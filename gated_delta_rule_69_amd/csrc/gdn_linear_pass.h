@@ -169,17 +169,6 @@ template <int C, int PARTS> struct Scores {
   }
 };
 
-template <typename E, int DA, int DC, bool OUT> struct PassShared {
-  using S = PassShape<E>;
-  static constexpr int C = S::kChunk;
-  Tile<C, DA, S::kParts> b[S::kHalf ? 2 : 1];
-  Tile<C, DC, S::kParts> c[S::kHalf && !OUT ? 2 : 1];
-  Tile<OUT ? C : 1, DA, S::kParts> a;
-  Scores<OUT ? C : 1, S::kScoreParts> scores;
-  float end_weight[2][C];   // l^{n-1-j+shift}
-  int bad_from[DC];         // first position of the chunk whose c is not finite, a channel
-};
-
 // A tile's way from memory to LDS. Rows 0 .. rows-1 come from `base` on, `step` bytes apart
 // (the last first, going backwards); the others are zero: their offsets lie outside the
 // range. Token strides are at most 2^24 elements, so a tile's offsets fit in 31 bits.
@@ -193,7 +182,8 @@ __device__ __forceinline__ void load_direct(Tile<C, D, 1>& t, const __bf16* base
   typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
   constexpr int kSlots = D / 8, kAll = C * kSlots;
   const uint64_t from = reinterpret_cast<uintptr_t>(base);
-  const uint4v range = {uint32_t(from), uint32_t(from >> 32) & 0xffffu, uint32_t(rows - 1) * step + 2 * D, 0x00020000u};
+  auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
+  const uint4v range = {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(uint32_t(rows - 1) * step + 2 * D), 0x00020000u};
   const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) __bf16*)(t.x)));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 #pragma unroll
@@ -202,8 +192,8 @@ __device__ __forceinline__ void load_direct(Tile<C, D, 1>& t, const __bf16* base
     if (kAll % NT != 0 && first >= kAll) break;
     const uint32_t at = first + threadIdx.x % 64, row = at / kSlots, slot = at % kSlots ^ t.turn(row);
     const uint32_t offset = (REV ? uint32_t(rows - 1) - row : row) * step + slot * 16;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds + 16 * first), "v"(offset), "s"(range) : "memory", "m0");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "{m0}"(uniform(lds + 16 * first)), "v"(offset), "s"(range) : "memory");
   }
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -245,10 +235,167 @@ __device__ __forceinline__ bool any_bad(bhalf8 x) {
 }
 __device__ __forceinline__ bool is_bad(__bf16 x) { return (__builtin_bit_cast(uint16_t, x) & 0x7f80u) == 0x7f80u; }
 
-// OUT: outputs, from the state before the segment. Otherwise the states after the segments
-// 0 .. nseg-2, each from zero (the first from x0), for scan_states to join.
-template <typename E, typename O, int DA, int DC, bool REV, bool OUT>
-__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_pass_kernel(LinearPass s) {
+// What both kernels of a pass know of their workgroup's segment, and the state of a wave's
+// sixteen columns in accumulators.
+template <typename E, int DA, int DC, bool REV> struct Segment {
+  static constexpr int C = PassShape<E>::kChunk, NT = 64 * pass_waves(DC), KT = DA / 16;
+  const LinearPass& s;
+  int wave, i, g, h, seg;
+  int64_t b, bh, n, begin, last, end;  // end: the segment's last real position + 1; last: of any
+  float lg;                            // log2 of the decay
+
+  __device__ __forceinline__ Segment(const LinearPass& s_, int segs) : s(s_) {
+    wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64;
+    i = lane % 16, g = lane / 16;
+    h = int(blockIdx.x) % s.H;
+    const int64_t bs = int64_t(blockIdx.x) / s.H;
+    seg = int(bs % segs);
+    b = bs / segs;
+    bh = b * s.H + h;
+    n = length_of(s.seq_lens, b, s.T);
+    lg = head_log_decay(s.log_decay, h) * 1.44269504088896341f;
+    begin = seg * s.seg;
+    last = begin + s.seg < s.T ? begin + s.seg : s.T;
+    end = last < n ? last : n;
+  }
+  __device__ __forceinline__ float power(int64_t m) const { return __builtin_amdgcn_exp2f(lg * float(m)); }
+  __device__ __forceinline__ int size(int64_t p) const { return int(end - p < C ? end - p : C); }  // positions of the chunk at p
+  // first token in memory of positions p .. p + m - 1: token p, or n - m - p backwards
+  __device__ __forceinline__ const E* rows(const void* x, int64_t ld, int group, int d, int64_t p) const {
+    return static_cast<const E*>(x) + (b * s.T + (REV ? n - size(p) - p : p)) * ld + int64_t(h / group) * d;
+  }
+  // a lane's first channel in state tile kt (four rows), and its column
+  __device__ __forceinline__ int row_channel(int kt) const { return KT == 1 ? 4 * g : 32 * (kt / 2) + 8 * g + 4 * (kt % 2); }
+  __device__ __forceinline__ int column() const { return 16 * wave + i; }
+
+  __device__ __forceinline__ void load_state(float4v (&X)[KT], const float* from, int64_t sa, int64_t sc) const {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      if (from == nullptr) {
+        X[kt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+      } else if (sa == 1) {
+        X[kt] = *reinterpret_cast<const float4v*>(from + row_channel(kt) + column() * sc);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) X[kt][e] = from[(row_channel(kt) + e) * sa + column() * sc];
+      }
+    }
+  }
+  __device__ __forceinline__ void store_state(const float4v (&X)[KT], float* to, int64_t sa, int64_t sc) const {
+    if (to == nullptr) return;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      if (sa == 1) {
+        *reinterpret_cast<float4v*>(to + row_channel(kt) + column() * sc) = X[kt];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[(row_channel(kt) + e) * sa + column() * sc] = X[kt][e];
+      }
+    }
+  }
+};
+
+// c of a k-block of positions for the wave's columns, and c times its positions' weights in
+// three parts.
+template <typename E, int DC, typename T>
+__device__ __forceinline__ void weighted(const T& tile, const float* weight, int kb, int wave, int i, int g, bhalf8* cv, bhalf8* wv) {
+  constexpr int P = PassShape<E>::kParts;
+  float x[8];
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    cv[q] = tile.columns(q, kb, 16 * wave, 4, i, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = q == 0 ? float(cv[q][e]) : x[e] + float(cv[q][e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= weight[32 * kb + 8 * g + e];
+  split_parts<3, 8>(x, wv);
+}
+
+// X += b^T (weighted c) of a k-block of positions.
+template <typename E, int DA, typename T>
+__device__ __forceinline__ void add_outer(float4v (&X)[DA / 16], const T& tile, int kb, int i, int g, const bhalf8* wv) {
+  constexpr int P = PassShape<E>::kParts, KT = DA / 16;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    bhalf8 bv[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      bv[q] = tile.columns(q, kb, KT == 1 ? 0 : 32 * (kt / 2) + 4 * (kt % 2), KT == 1 ? 4 : 8, i, g);
+    X[kt] = mma_parts<P, 3, 2>(bv, wv, X[kt]);
+  }
+}
+
+// The states after segments 0 .. nseg-2, each from zero (the first from x0): the sum of
+// l^{end-1-p} b_p c_p^T, for scan_states to join. A segment is walked from its end, so that
+// nothing is scaled on the way, the positions whose weight is under 2^-127 (0 in float32)
+// are never read, and what the outputs' kernel reads first was read here last.
+template <typename E, int DA, int DC, bool REV>
+__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_states_kernel(LinearPass s) {
+  using S = PassShape<E>;
+  constexpr int C = S::kChunk, NT = 64 * pass_waves(DC), P = S::kParts;
+  constexpr bool kDirect = S::kHalf;
+  struct Shared {
+    Tile<C, DA, P> b[kDirect ? 2 : 1];
+    Tile<C, DC, P> c[kDirect ? 2 : 1];
+    float weight[2][C];
+  };
+  __shared__ Shared sh;
+  const Segment<E, DA, DC, REV> me(s, s.nseg - 1);
+  float4v X[DA / 16];
+  float* slots = s.states + me.bh * s.nseg * (DA * DC);
+  const int64_t begin = me.begin, end = me.end;
+  const bool first = me.seg == 0 && s.x0 != nullptr;
+  me.load_state(X, first ? s.x0 + me.bh * (DA * DC) : nullptr, s.x0_sa, s.x0_sc);
+  // x0 may be overwritten by the last segment's state while the first segment's outputs are
+  // still to come: they read this copy
+  if (first) me.store_state(X, slots, s.st_sa, s.st_sc);
+  const float whole = me.power(end > begin ? end - begin : 0);
+#pragma unroll
+  for (int kt = 0; kt < DA / 16; ++kt) X[kt] *= whole;
+
+  [[maybe_unused]] Staged<C, DA, NT> rb;
+  [[maybe_unused]] Staged<C, DC, NT> rc;
+  auto fetch = [&](int64_t p, int buf) {
+    const E *fb = me.rows(s.b, s.ldb, s.group_b, DA, p), *fc = me.rows(s.c, s.ldc, s.group_c, DC, p);
+    if constexpr (kDirect) {
+      load_direct<C, DA, NT, REV>(sh.b[buf], fb, uint32_t(s.ldb * 2), me.size(p));
+      load_direct<C, DC, NT, REV>(sh.c[buf], fc, uint32_t(s.ldc * 2), me.size(p));
+    } else {
+      rb.template load<REV>(fb, uint32_t(s.ldb * 4), me.size(p));
+      rc.template load<REV>(fc, uint32_t(s.ldc * 4), me.size(p));
+    }
+  };
+  int64_t p = end > begin ? begin + (end - 1 - begin) / C * C : begin - C;
+  if (p >= begin) fetch(p, 0);
+  for (int buf = 0; p >= begin; p -= C, buf ^= 1) {
+    const bool more = p - C >= begin && me.lg * float(end - p + s.shift) > -127.0f;
+    if constexpr (kDirect) wait_loads();
+    else rb.store(sh.b[0]), rc.store(sh.c[0]);
+    if (threadIdx.x < C) {
+      const int64_t left = end - 1 - p - int(threadIdx.x);
+      sh.weight[buf][threadIdx.x] = left >= 0 ? me.power(left + s.shift) : 0.0f;
+    }
+    __syncthreads();
+    if (more) fetch(p - C, buf ^ 1);
+    const int at = kDirect ? buf : 0;
+#pragma unroll
+    for (int kb = 0; kb < C / 32; ++kb) {
+      bhalf8 cv[P], wv[3];
+      weighted<E, DC>(sh.c[at], sh.weight[buf], kb, me.wave, me.i, me.g, cv, wv);
+      add_outer<E, DA>(X, sh.b[at], kb, me.i, me.g, wv);
+    }
+    if (!more) break;
+    if constexpr (!kDirect) __syncthreads();
+  }
+  me.store_state(X, slots + (me.seg + 1) * (DA * DC), s.st_sa, s.st_sc);
+}
+
+// The outputs of a segment, chunk by chunk from the state before it; the last segment's
+// workgroup also has the pass's last state.
+template <typename E, typename O, int DA, int DC, bool REV>
+__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_outputs_kernel(LinearPass s) {
   using S = PassShape<E>;
   constexpr int C = S::kChunk, NW = pass_waves(DC), NT = 64 * NW;
   constexpr int P = S::kParts, PS = S::kScoreParts;
@@ -256,284 +403,202 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   constexpr int KT = DA / 16;         // state tiles of a wave
   constexpr int KB = (DA + 31) / 32;  // k-blocks along DA
   constexpr int PB = C / 32;          // k-blocks of positions
-  __shared__ PassShared<E, DA, DC, OUT> sh;
-
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  int i = lane % 16, g = lane / 16;
-  const int h = int(blockIdx.x) % s.H;
-  const int64_t bs = int64_t(blockIdx.x) / s.H;
-  const int segs = OUT ? s.nseg : s.nseg - 1;
-  const int seg = int(bs % segs);
-  const int64_t b = bs / segs;
-  const int64_t bh = b * s.H + h;
-  const int64_t n = length_of(s.seq_lens, b, s.T);
-  const float lg = head_log_decay(s.log_decay, h) * 1.44269504088896341f;  // log2
-  float lg_now = lg;
-  auto power = [&](int m) { return __builtin_amdgcn_exp2f(lg_now * float(m)); };
-
-  const int64_t begin = seg * s.seg;
-  const int64_t last = begin + s.seg < s.T ? begin + s.seg : s.T;   // positions of the segment, real or not
-  const int64_t end = last < n ? last : n;
-  // first token in memory of positions p .. p + m - 1: token p, or n - m - p backwards
-  auto rows = [&](const void* x, int64_t ld, int group, int d, int64_t p, int m) {
-    return static_cast<const E*>(x) + (b * s.T + (REV ? n - m - p : p)) * ld + int64_t(h / group) * d;
-  };
-  // a lane's first channel in state tile kt (four rows), and its column
-  auto row_channel = [&](int kt) { return KT == 1 ? 4 * g : 32 * (kt / 2) + 8 * g + 4 * (kt % 2); };
-  const int column = 16 * wave + i;
-
-  // The state of the wave's columns. The outputs' pass takes x0 from slot 0 where there are
-  // several segments: x1 may be x0 itself, and the last segment's workgroup may end before
-  // the first one's begins.
-  float4v X[KT];
-  float* slots = s.states + bh * s.nseg * (DA * DC);
-  const bool given = seg > 0 ? OUT : s.x0 != nullptr;
-  const bool direct = seg == 0 && (!OUT || s.nseg == 1);
-  const float* from = !given ? nullptr : direct ? s.x0 + bh * (DA * DC) : slots + seg * (DA * DC);
-  const int64_t sa = direct ? s.x0_sa : s.st_sa, sc = direct ? s.x0_sc : s.st_sc;
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    if (from == nullptr) {
-      X[kt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    } else if (sa == 1) {
-      X[kt] = *reinterpret_cast<const float4v*>(from + row_channel(kt) + column * sc);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) X[kt][e] = from[(row_channel(kt) + e) * sa + column * sc];
-    }
-  }
-  auto store_state = [&](float* to, int64_t ta, int64_t tc) {
-    if (to == nullptr) return;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      if (ta == 1) {
-        *reinterpret_cast<float4v*>(to + row_channel(kt) + column * tc) = X[kt];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) to[(row_channel(kt) + e) * ta + column * tc] = X[kt][e];
-      }
-    }
-  };
-  if (!OUT && seg == 0 && given) store_state(slots, s.st_sa, s.st_sc);
-
   constexpr bool kDirect = S::kHalf;
+  struct Shared {
+    Tile<C, DA, P> a, b[kDirect ? 2 : 1];
+    Tile<C, DC, P> c;
+    Scores<C, PS> scores;
+    float weight[2][C];  // l^{n-1-j+shift}
+    int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
+  };
+  __shared__ Shared sh;
+  Segment<E, DA, DC, REV> me(s, s.nseg);
+  const int wave = me.wave;
+  const int64_t begin = me.begin, end = me.end;
+  float4v X[KT];
+  if (s.nseg == 1)
+    me.load_state(X, s.x0 == nullptr ? nullptr : s.x0 + me.bh * (DA * DC), s.x0_sa, s.x0_sc);
+  else
+    me.load_state(X, me.seg == 0 && s.x0 == nullptr ? nullptr : s.states + (me.bh * s.nseg + me.seg) * (DA * DC), s.st_sa, s.st_sc);
+
   [[maybe_unused]] Staged<C, DA, NT> ra, rb;
   [[maybe_unused]] Staged<C, DC, NT> rc;
-  auto size = [&](int64_t p) { return int(end - p < C ? end - p : C); };  // positions of the chunk at p
-  // the ways of the tiles of the chunk at p; bf16 ones land in `buf` of their buffers
   auto fetch_a = [&](int64_t p) {
-    [[maybe_unused]] const E* from = rows(s.a, s.lda, s.group_a, DA, p, size(p));
-    if constexpr (!OUT) return;
-    else if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.a, from, uint32_t(s.lda * 2), size(p));
-    else ra.template load<REV>(from, uint32_t(s.lda * 4), size(p));
+    const E* from = me.rows(s.a, s.lda, s.group_a, DA, p);
+    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.a, from, uint32_t(s.lda * 2), me.size(p));
+    else ra.template load<REV>(from, uint32_t(s.lda * 4), me.size(p));
   };
   auto fetch_b = [&](int64_t p, int buf) {
-    const E* from = rows(s.b, s.ldb, s.group_b, DA, p, size(p));
-    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.b[buf], from, uint32_t(s.ldb * 2), size(p));
-    else rb.template load<REV>(from, uint32_t(s.ldb * 4), size(p));
+    const E* from = me.rows(s.b, s.ldb, s.group_b, DA, p);
+    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.b[buf], from, uint32_t(s.ldb * 2), me.size(p));
+    else rb.template load<REV>(from, uint32_t(s.ldb * 4), me.size(p));
   };
-  auto fetch_c = [&](int64_t p, int buf) {
-    const E* from = rows(s.c, s.ldc, s.group_c, DC, p, size(p));
-    if constexpr (kDirect) load_direct<C, DC, NT, REV>(sh.c[buf], from, uint32_t(s.ldc * 2), size(p));
-    else rc.template load<REV>(from, uint32_t(s.ldc * 4), size(p));
+  auto fetch_c = [&](int64_t p) {
+    const E* from = me.rows(s.c, s.ldc, s.group_c, DC, p);
+    if constexpr (kDirect) load_direct<C, DC, NT, REV>(sh.c, from, uint32_t(s.ldc * 2), me.size(p));
+    else rc.template load<REV>(from, uint32_t(s.ldc * 4), me.size(p));
   };
-  // Order of a chunk's loads and barriers.
-  //   bf16 outputs: `a` and `b` are there at the start of a chunk; `c` arrives while scores
-  //     and a X are formed, the next `a` (its tile is read no more) and `b` (the other
-  //     buffer) while the chunk's rows are summed. Two workgroups fit a CU.
-  //   bf16 states: both tiles of the next chunk arrive during this one.
-  //   float32: the next chunk's rows wait in registers.
+  // Order of a chunk's loads and barriers. bf16: `a` and `b` are there at the start of a
+  // chunk; `c` arrives while scores and a X are formed, the next `a` (its tile is read no
+  // more) and `b` (the other buffer) while the chunk's own rows are summed: two workgroups
+  // fit a CU. float32: the next chunk's rows wait in registers.
   if (begin < end) {
-    if constexpr (OUT) fetch_a(begin);
+    fetch_a(begin);
     fetch_b(begin, 0);
-    if constexpr (!kDirect || !OUT) fetch_c(begin, 0);
-    if constexpr (kDirect && OUT) {
+    if constexpr (kDirect) {
       wait_loads();
       __syncthreads();
+    } else {
+      fetch_c(begin);
     }
   }
 
   int buf = 0;
-  for (int64_t p = begin; p < end; p += C) {
-    const int m = size(p);
+  for (int64_t p = begin; p < end; p += C, buf ^= 1) {
+    const int m = me.size(p);
     const bool more = p + C < end;
     // opaque in every chunk: powers and LDS addresses are formed where they are used, not held
-    asm volatile("" : "+v"(lg_now), "+v"(i), "+v"(g));
-    if constexpr (!kDirect) {
-      if constexpr (OUT) ra.store(sh.a);
-      rb.store(sh.b[0]);
-      rc.store(sh.c[0]);
-    } else if constexpr (OUT) {
-      fetch_c(p, 0);
+    asm volatile("" : "+v"(me.lg), "+v"(me.i), "+v"(me.g));
+    const int i = me.i, g = me.g;
+    if constexpr (kDirect) {
+      fetch_c(p);
     } else {
-      wait_loads();
+      ra.store(sh.a);
+      rb.store(sh.b[0]);
+      rc.store(sh.c);
     }
     if (threadIdx.x < C) {
       const int left = m - 1 - int(threadIdx.x);
-      sh.end_weight[buf][threadIdx.x] = left >= 0 ? power(left + s.shift) : 0.0f;
+      sh.weight[buf][threadIdx.x] = left >= 0 ? me.power(left + s.shift) : 0.0f;
     }
-    if constexpr (!kDirect || !OUT) __syncthreads();
     if constexpr (!kDirect) {
-      if (more) {
-        if constexpr (OUT) fetch_a(p + C);
-        fetch_b(p + C, 0);
-        fetch_c(p + C, 0);
-      }
-    } else if constexpr (!OUT) {
-      if (more) fetch_b(p + C, buf ^ 1), fetch_c(p + C, buf ^ 1);
+      __syncthreads();
+      if (more) fetch_a(p + C), fetch_b(p + C, 0), fetch_c(p + C);
     }
     Tile<C, DA, P>& tb = sh.b[kDirect ? buf : 0];
-    Tile<C, DC, P>& tc = sh.c[kDirect && !OUT ? buf : 0];
 
-    float4v acc[OUT ? RT : 1];
-    if constexpr (OUT) {
-      // Scores, transposed: column i of tile (r, jt) is position 16 r + i, its rows are
-      // positions 16 jt + 4 g + e. The tiles at and under the diagonal go round the waves,
-      // then those right of it that a k-block of 32 positions reads as zeros.
-      constexpr int kLower = RT * (RT + 1) / 2;
-      for (int t = wave; t < kLower + RT / 2; t += NW) {
-        int r = 0, jt = t;
-        float x[4] = {};
-        if (t < kLower) {
-          while (jt > r) jt -= ++r;
-          float4v d{0.0f, 0.0f, 0.0f, 0.0f};
+    // Scores, transposed: column i of tile (r, jt) is position 16 r + i, its rows are
+    // positions 16 jt + 4 g + e. The tiles at and under the diagonal go round the waves,
+    // then those right of it that a k-block of 32 positions reads as zeros.
+    constexpr int kLower = RT * (RT + 1) / 2;
+    for (int t = wave; t < kLower + RT / 2; t += NW) {
+      int r = 0, jt = t;
+      float x[4] = {};
+      if (t < kLower) {
+        while (jt > r) jt -= ++r;
+        float4v d{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            bhalf8 av[P], bv[P];
+        for (int kb = 0; kb < KB; ++kb) {
+          bhalf8 av[P], bv[P];
 #pragma unroll
-            for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g), bv[q] = tb.row(q, jt, kb, i, g);
-            d = mma_parts<P, P, P - 1>(bv, av, d);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int ahead = 16 * r + i - (16 * jt + 4 * g + e);
-            x[e] = ahead >= 0 ? d[e] * power(ahead) : 0.0f;
-          }
-        } else {
-          r = 2 * (t - kLower), jt = r + 1;
+          for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g), bv[q] = tb.row(q, jt, kb, i, g);
+          d = mma_parts<P, P, P - 1>(bv, av, d);
         }
-        bhalf4 part[PS];
-        split_parts<PS, 4>(x, part);
-#pragma unroll
-        for (int q = 0; q < PS; ++q)
-          sh.scores.put4(q, 16 * r + i, 16 * jt + 4 * g, part[q]);
-      }
-      // what the state before the chunk gives
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[e] = X[2 * kb][e];
-          x[4 + e] = KT > 1 ? X[KT > 1 ? 2 * kb + 1 : 0][e] : 0.0f;
+          const int ahead = 16 * r + i - (16 * jt + 4 * g + e);
+          x[e] = ahead >= 0 ? d[e] * me.power(ahead) : 0.0f;
         }
-        bhalf8 xv[PS];
-        split_parts<PS, 8>(x, xv);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          bhalf8 av[P];
-#pragma unroll
-          for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g);
-          acc[r] = mma_parts<PS, P, PS - 1>(xv, av, acc[r]);
-        }
+      } else {
+        r = 2 * (t - kLower), jt = r + 1;
       }
+      bhalf4 part[PS];
+      split_parts<PS, 4>(x, part);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] *= power(16 * r + i + 1 - s.shift);
-      if constexpr (kDirect) wait_loads();
-      __syncthreads();
-      if constexpr (kDirect) {
-        if (more) fetch_a(p + C), fetch_b(p + C, buf ^ 1);
+      for (int q = 0; q < PS; ++q) sh.scores.put4(q, 16 * r + i, 16 * jt + 4 * g, part[q]);
+    }
+    // what the state before the chunk gives
+    float4v acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = X[2 * kb][e];
+        x[4 + e] = KT > 1 ? X[KT > 1 ? 2 * kb + 1 : 0][e] : 0.0f;
       }
+      bhalf8 xv[PS];
+      split_parts<PS, 8>(x, xv);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        bhalf8 av[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g);
+        acc[r] = mma_parts<PS, P, PS - 1>(xv, av, acc[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] *= me.power(16 * r + i + 1 - s.shift);
+    if constexpr (kDirect) wait_loads();
+    __syncthreads();
+    if constexpr (kDirect) {
+      if (more) fetch_a(p + C), fetch_b(p + C, buf ^ 1);
     }
 
     // what the chunk's own rows give, and the state after it
     bool bad = false;
-    const float whole = power(m);
+    const float whole = me.power(m);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) X[kt] *= whole;
 #pragma unroll
     for (int kb = 0; kb < PB; ++kb) {
       bhalf8 cv[P], wv[3];
-      float x[8];
+      weighted<E, DC>(sh.c, sh.weight[buf], kb, wave, i, g, cv, wv);
+      // A masked score is 0, but 0 times Inf is not: such values leave the product, and the
+      // rows from theirs on become NaN.
+      if (__builtin_expect(__any(any_bad(cv[0])), 0)) {
+        const int column = 16 * wave + i;
+        if (!bad && g == 0) sh.bad_from[column] = C;
+        bad = true;
 #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        cv[q] = tc.columns(q, kb, 16 * wave, 4, i, g);
+        for (int e = 0; e < 8; ++e) {
+          if (!is_bad(cv[0][e])) continue;
+          atomicMin(&sh.bad_from[column], 32 * kb + 8 * g + e);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = q == 0 ? float(cv[q][e]) : x[e] + float(cv[q][e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= sh.end_weight[buf][32 * kb + 8 * g + e];
-      split_parts<3, 8>(x, wv);
-      if constexpr (OUT) {
-        // A masked score is 0, but 0 times Inf is not: such values leave the product, and the
-        // rows from theirs on become NaN.
-        if (__builtin_expect(__any(any_bad(cv[0])), 0)) {
-          if (!bad && g == 0) sh.bad_from[column] = C;
-          bad = true;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!is_bad(cv[0][e])) continue;
-            atomicMin(&sh.bad_from[column], 32 * kb + 8 * g + e);
-#pragma unroll
-            for (int q = 0; q < P; ++q) cv[q][e] = __bf16(0.0f);
-          }
-        }
-#pragma unroll
-        for (int r = 2 * kb; r < RT; ++r) {
-          bhalf8 sv[PS];
-#pragma unroll
-          for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, i, g);
-          acc[r] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r]);
+          for (int q = 0; q < P; ++q) cv[q][e] = __bf16(0.0f);
         }
       }
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        bhalf8 bv[P];
+      for (int r = 2 * kb; r < RT; ++r) {
+        bhalf8 sv[PS];
 #pragma unroll
-        for (int q = 0; q < P; ++q)
-          bv[q] = tb.columns(q, kb, KT == 1 ? 0 : 32 * (kt / 2) + 4 * (kt % 2), KT == 1 ? 4 : 8, i, g);
-        X[kt] = mma_parts<P, 3, 2>(bv, wv, X[kt]);
+        for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, i, g);
+        acc[r] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r]);
       }
+      add_outer<E, DA>(X, tb, kb, i, g, wv);
     }
 
-    if constexpr (OUT) {
-      if constexpr (kDirect) wait_loads();
+    if constexpr (kDirect) wait_loads();
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int at = 16 * r + i;
-        if (at < m) {
-          const int64_t token = b * s.T + (REV ? n - 1 - p - at : p + at);
-          const int ch = 16 * wave + 4 * g;
-          float x[4] = {acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
-          if (__builtin_expect(bad, 0)) {
+    for (int r = 0; r < RT; ++r) {
+      const int at = 16 * r + i;
+      if (at < m) {
+        const int64_t token = me.b * s.T + (REV ? me.n - 1 - p - at : p + at);
+        const int ch = 16 * wave + 4 * g;
+        float x[4] = {acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+        if (__builtin_expect(bad, 0)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (at >= sh.bad_from[ch + e]) x[e] = __builtin_nanf("");
-          }
-          store4(static_cast<O*>(s.out) + (token * s.H + h) * DC + ch, x);
+          for (int e = 0; e < 4; ++e)
+            if (at >= sh.bad_from[ch + e]) x[e] = __builtin_nanf("");
         }
+        store4(static_cast<O*>(s.out) + (token * s.H + me.h) * DC + ch, x);
       }
     }
-    if constexpr (OUT || !kDirect) __syncthreads();
-    buf ^= 1;
+    __syncthreads();
   }
 
-  if constexpr (OUT) {
-    if (s.zero_tail) {
-      const int64_t first = begin > n ? begin : n;
-      constexpr int V = DC / 4;
-      for (int64_t at = threadIdx.x; at < (last - first) * V; at += NT) {
-        const float zero[4] = {};
-        store4(static_cast<O*>(s.out) + ((b * s.T + first + at / V) * s.H + h) * DC + at % V * 4, zero);
-      }
+  if (s.zero_tail) {
+    const int64_t first = begin > me.n ? begin : me.n;
+    constexpr int V = DC / 4;
+    for (int64_t at = threadIdx.x; at < (me.last - first) * V; at += NT) {
+      const float zero[4] = {};
+      store4(static_cast<O*>(s.out) + ((me.b * s.T + first + at / V) * s.H + me.h) * DC + at % V * 4, zero);
     }
   }
-
-  if (OUT && seg < s.nseg - 1) return;
-  store_state(OUT ? (s.x1 == nullptr ? nullptr : s.x1 + bh * (DA * DC)) : slots + (seg + 1) * (DA * DC),
-              OUT ? s.x0_sa : s.st_sa, OUT ? s.x0_sc : s.st_sc);
+  if (me.seg == s.nseg - 1)
+    me.store_state(X, s.x1 == nullptr ? nullptr : s.x1 + me.bh * (DA * DC), s.x0_sa, s.x0_sc);
 }
 
 // Launches of one direction and type, in the translation units of each element type.
@@ -544,12 +609,12 @@ template <typename E, typename O, int DA, int DC>
 int launch_pass_dims(const LinearPass& s, int64_t B, bool rev, bool out, hipStream_t stream) {
   constexpr int kThreads = 64 * pass_waves(DC);
   const unsigned grid = unsigned(B * s.H * (out ? s.nseg : s.nseg - 1));
-  if (rev) {
-    if (out) linear_pass_kernel<E, O, DA, DC, true, true><<<grid, kThreads, 0, stream>>>(s);
-    else linear_pass_kernel<E, E, DA, DC, true, false><<<grid, kThreads, 0, stream>>>(s);
+  if (!out) {
+    if (rev) linear_states_kernel<E, DA, DC, true><<<grid, kThreads, 0, stream>>>(s);
+    else linear_states_kernel<E, DA, DC, false><<<grid, kThreads, 0, stream>>>(s);
   } else {
-    if (out) linear_pass_kernel<E, O, DA, DC, false, true><<<grid, kThreads, 0, stream>>>(s);
-    else linear_pass_kernel<E, E, DA, DC, false, false><<<grid, kThreads, 0, stream>>>(s);
+    if (rev) linear_outputs_kernel<E, O, DA, DC, true><<<grid, kThreads, 0, stream>>>(s);
+    else linear_outputs_kernel<E, O, DA, DC, false><<<grid, kThreads, 0, stream>>>(s);
   }
   return int(hipGetLastError());
 }
