@@ -136,20 +136,25 @@ template <int C, int D, int PARTS> struct Tile {
   __device__ static __forceinline__ int place(int row, int col) {
     return row * D + ((col / 8) ^ turn(row)) * 8 + (col & 4);
   }
+  // A lane's place for row(): row i, its eight channels of a k-block (four of sixteen).
+  __device__ static __forceinline__ int row_place(int i, int g) { return place(i, D == 16 ? 4 * g : 8 * g); }
   // rows 16 r + i, channels of k-block kb: the order of the state's accumulator tiles
-  __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int i, int g) const {
-    const __bf16* at = x + p * kPlane + 16 * r * D;
-    if constexpr (D == 16) {
-      return join(*reinterpret_cast<const bhalf4*>(at + place(i, 4 * g)), bhalf4{});
-    } else {
-      return *reinterpret_cast<const bhalf8*>(at + place(i, 32 * kb + 8 * g));
-    }
+  __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int at) const {
+    const __bf16* from = x + p * kPlane + 16 * r * D + (at ^ 32 * kb);
+    if constexpr (D == 16) return join(*reinterpret_cast<const bhalf4*>(from), bhalf4{});
+    else return *reinterpret_cast<const bhalf8*>(from);
   }
-  // positions 32 kb + 8 g + e of channel `column` + (i / 4) step + i % 4, read transposed
-  __device__ __forceinline__ bhalf8 columns(int p, int kb, int column, int step, int i, int g) const {
-    const __bf16* at = x + p * kPlane + 32 * kb * D;
-    const int row = 8 * g + i / 4, col = column + (i % 4) * step;
-    return join(read_tr(at + place(row, col)), read_tr(at + place(row + 4, col)));
+  // A lane's place for columns(): of the positions 8 g + e of a k-block, it reads the four
+  // channels at `column` + (i % 4) step of position i / 4 (and of i / 4 + 4).
+  __device__ static __forceinline__ int column_place(int column, int step, int i, int g) {
+    return place(8 * g + i / 4, column + (i % 4) * step);
+  }
+  // positions 32 kb + 8 g + e of channel column + (i / 4) step + i % 4, read transposed;
+  // `block` moves the column by 32 channels, `half` by four
+  __device__ __forceinline__ bhalf8 columns(int p, int kb, int at, int block, int half) const {
+    const __bf16* from = x + p * kPlane + 32 * kb * D + 4 * half;
+    const int near = at ^ 32 * block, far = kSlots == 2 ? near : near ^ 16;  // four rows on, turn() differs by 2
+    return join(read_tr(from + near), read_tr(from + 4 * D + far));
   }
   __device__ __forceinline__ void put4(int p, int row, int col, bhalf4 v) {
     *reinterpret_cast<bhalf4*>(x + p * kPlane + place(row, col)) = v;
@@ -164,8 +169,8 @@ template <int C, int PARTS> struct Scores {
     if (C == 64 && row >= 32) second.put4(p, row - 32, col, v);
     else first.put4(p, row, col, v);
   }
-  __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int i, int g) const {
-    return r < 2 ? first.row(p, r, kb, i, g) : second.row(p, r - 2, kb, i, g);
+  __device__ __forceinline__ bhalf8 row(int p, int r, int kb, int at_first, int at_second) const {
+    return r < 2 ? first.row(p, r, kb, at_first) : second.row(p, r - 2, kb, at_second);
   }
 };
 
@@ -177,34 +182,46 @@ template <int C, int PARTS> struct Scores {
 // wave's base + 16 l, so the tile's slots are chosen by where a lane loads from). The
 // loads are written as assembly, which has no registers to guard and leaves the waiting to
 // wait_loads(); the compiler's own counts only ever wait for more.
-template <int C, int D, int NT, bool REV>
-__device__ __forceinline__ void load_direct(Tile<C, D, 1>& t, const __bf16* base, uint32_t step, int rows) {
-  typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-  constexpr int kSlots = D / 8, kAll = C * kSlots;
-  const uint64_t from = reinterpret_cast<uintptr_t>(base);
-  auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
-  const uint4v range = {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(uint32_t(rows - 1) * step + 2 * D), 0x00020000u};
-  const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) __bf16*)(t.x)));
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-#pragma unroll
-  for (int n = 0; n < (kAll + NT - 1) / NT; ++n) {
-    const int first = n * NT + 64 * wave;
-    if (kAll % NT != 0 && first >= kAll) break;
-    const uint32_t at = first + threadIdx.x % 64, row = at / kSlots, slot = at % kSlots ^ t.turn(row);
-    const uint32_t offset = (REV ? uint32_t(rows - 1) - row : row) * step + slot * 16;
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "{m0}"(uniform(lds + 16 * first)), "v"(offset), "s"(range) : "memory");
+template <int C, int D, int NT, bool REV> struct Direct {
+  static constexpr int kSlots = D / 8, kAll = C * kSlots;
+  static constexpr int kRows = NT / kSlots;        // rows a step of the workgroup covers
+  static constexpr bool kSame = kRows % 16 == 0;   // so that turn() is the same in each
+  uint32_t step;    // bytes from row to row
+  uint32_t offset;  // of the thread's slot of its first row
+  __device__ __forceinline__ uint32_t offset_of(uint32_t at) const {
+    const uint32_t row = at / kSlots, to = (at % kSlots ^ Tile<C, D, 1>::turn(row)) * 16;
+    return REV ? to - row * step : to + row * step;
   }
-}
+  __device__ __forceinline__ Direct(int64_t ld) : step(uint32_t(ld * 2)), offset(offset_of(threadIdx.x)) {}
+  __device__ __forceinline__ void load(Tile<C, D, 1>& t, const __bf16* base, int rows) const {
+    typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+    auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
+    const uint64_t from = reinterpret_cast<uintptr_t>(base);
+    const uint32_t top = uint32_t(rows - 1) * step;
+    const uint4v range = {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(top + 2 * D), 0x00020000u};
+    const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) __bf16*)(t.x)));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+#pragma unroll
+    for (int n = 0; n < (kAll + NT - 1) / NT; ++n) {
+      const int first = n * NT + 64 * wave;
+      if (kAll % NT != 0 && first >= kAll) break;
+      const uint32_t here = kSame ? offset + (REV ? 0u - uint32_t(n * kRows) * step : uint32_t(n * kRows) * step)
+                                  : offset_of(n * NT + threadIdx.x);
+      asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :: "{m0}"(uniform(lds + 16 * first)), "v"(REV ? here + top : here), "s"(range) : "memory");
+    }
+  }
+};
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // float32 rows pass through registers, where they become three bf16 planes.
-template <int C, int D, int NT> struct Staged {
+template <int C, int D, int NT, bool REV> struct Staged {
   static constexpr int kPerRow = D / 4;
   static constexpr int kCount = (C * kPerRow + NT - 1) / NT;
   uint4 v[kCount];
-  template <bool REV>
-  __device__ __forceinline__ void load(const float* base, uint32_t step, int rows) {
+  uint32_t step;
+  __device__ __forceinline__ Staged(int64_t ld) : step(uint32_t(ld * 4)) {}
+  __device__ __forceinline__ void load(const float* base, int rows) {
     const auto range = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), 0, uint32_t(rows - 1) * step + 4 * D, 0x00020000);
 #pragma unroll
     for (int n = 0; n < kCount; ++n) {
@@ -296,34 +313,33 @@ template <typename E, int DA, int DC, bool REV> struct Segment {
   }
 };
 
-// c of a k-block of positions for the wave's columns, and c times its positions' weights in
-// three parts.
+// c of a k-block of positions for the wave's columns, and c times its positions' weights.
 template <typename E, int DC, typename T>
-__device__ __forceinline__ void weighted(const T& tile, const float* weight, int kb, int wave, int i, int g, bhalf8* cv, bhalf8* wv) {
+__device__ __forceinline__ void weighted(const T& tile, const float* weight, int kb, int at, int g, bhalf8* cv, float* x) {
   constexpr int P = PassShape<E>::kParts;
-  float x[8];
 #pragma unroll
   for (int q = 0; q < P; ++q) {
-    cv[q] = tile.columns(q, kb, 16 * wave, 4, i, g);
+    cv[q] = tile.columns(q, kb, at, 0, 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = q == 0 ? float(cv[q][e]) : x[e] + float(cv[q][e]);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= weight[32 * kb + 8 * g + e];
-  split_parts<3, 8>(x, wv);
 }
 
-// X += b^T (weighted c) of a k-block of positions.
-template <typename E, int DA, typename T>
-__device__ __forceinline__ void add_outer(float4v (&X)[DA / 16], const T& tile, int kb, int i, int g, const bhalf8* wv) {
+// X += b^T (weighted c) of a k-block of positions, c in W parts.
+template <typename E, int DA, int W, typename T>
+__device__ __forceinline__ void add_outer(float4v (&X)[DA / 16], const T& tile, int kb, int at, const float* x) {
   constexpr int P = PassShape<E>::kParts, KT = DA / 16;
+  bhalf8 wv[W];
+  split_parts<W, 8>(x, wv);
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     bhalf8 bv[P];
 #pragma unroll
     for (int q = 0; q < P; ++q)
-      bv[q] = tile.columns(q, kb, KT == 1 ? 0 : 32 * (kt / 2) + 4 * (kt % 2), KT == 1 ? 4 : 8, i, g);
-    X[kt] = mma_parts<P, 3, 2>(bv, wv, X[kt]);
+      bv[q] = tile.columns(q, kb, at, kt / 2, kt % 2);
+    X[kt] = mma_parts<P, W, W - 1>(bv, wv, X[kt]);
   }
 }
 
@@ -355,18 +371,15 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 #pragma unroll
   for (int kt = 0; kt < DA / 16; ++kt) X[kt] *= whole;
 
-  [[maybe_unused]] Staged<C, DA, NT> rb;
-  [[maybe_unused]] Staged<C, DC, NT> rc;
+  std::conditional_t<kDirect, Direct<C, DA, NT, REV>, Staged<C, DA, NT, REV>> rb(s.ldb);
+  std::conditional_t<kDirect, Direct<C, DC, NT, REV>, Staged<C, DC, NT, REV>> rc(s.ldc);
   auto fetch = [&](int64_t p, int buf) {
     const E *fb = me.rows(s.b, s.ldb, s.group_b, DA, p), *fc = me.rows(s.c, s.ldc, s.group_c, DC, p);
-    if constexpr (kDirect) {
-      load_direct<C, DA, NT, REV>(sh.b[buf], fb, uint32_t(s.ldb * 2), me.size(p));
-      load_direct<C, DC, NT, REV>(sh.c[buf], fc, uint32_t(s.ldc * 2), me.size(p));
-    } else {
-      rb.template load<REV>(fb, uint32_t(s.ldb * 4), me.size(p));
-      rc.template load<REV>(fc, uint32_t(s.ldc * 4), me.size(p));
-    }
+    if constexpr (kDirect) rb.load(sh.b[buf], fb, me.size(p)), rc.load(sh.c[buf], fc, me.size(p));
+    else rb.load(fb, me.size(p)), rc.load(fc, me.size(p));
   };
+  const int at_b = Tile<C, DA, P>::column_place(0, DA == 16 ? 4 : 8, me.i, me.g);
+  const int at_c = Tile<C, DC, P>::column_place(16 * me.wave, 4, me.i, me.g);
   int64_t p = end > begin ? begin + (end - 1 - begin) / C * C : begin - C;
   if (p >= begin) fetch(p, 0);
   for (int buf = 0; p >= begin; p -= C, buf ^= 1) {
@@ -382,9 +395,10 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     const int at = kDirect ? buf : 0;
 #pragma unroll
     for (int kb = 0; kb < C / 32; ++kb) {
-      bhalf8 cv[P], wv[3];
-      weighted<E, DC>(sh.c[at], sh.weight[buf], kb, me.wave, me.i, me.g, cv, wv);
-      add_outer<E, DA>(X, sh.b[at], kb, me.i, me.g, wv);
+      bhalf8 cv[P];
+      float x[8];
+      weighted<E, DC>(sh.c[at], sh.weight[buf], kb, at_c, me.g, cv, x);
+      add_outer<E, DA, 3>(X, sh.b[at], kb, at_b, x);
     }
     if (!more) break;
     if constexpr (!kDirect) __syncthreads();
@@ -421,23 +435,34 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   else
     me.load_state(X, me.seg == 0 && s.x0 == nullptr ? nullptr : s.states + (me.bh * s.nseg + me.seg) * (DA * DC), s.st_sa, s.st_sc);
 
-  [[maybe_unused]] Staged<C, DA, NT> ra, rb;
-  [[maybe_unused]] Staged<C, DC, NT> rc;
+  std::conditional_t<kDirect, Direct<C, DA, NT, REV>, Staged<C, DA, NT, REV>> ra(s.lda), rb(s.ldb);
+  std::conditional_t<kDirect, Direct<C, DC, NT, REV>, Staged<C, DC, NT, REV>> rc(s.ldc);
   auto fetch_a = [&](int64_t p) {
     const E* from = me.rows(s.a, s.lda, s.group_a, DA, p);
-    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.a, from, uint32_t(s.lda * 2), me.size(p));
-    else ra.template load<REV>(from, uint32_t(s.lda * 4), me.size(p));
+    if constexpr (kDirect) ra.load(sh.a, from, me.size(p));
+    else ra.load(from, me.size(p));
   };
   auto fetch_b = [&](int64_t p, int buf) {
     const E* from = me.rows(s.b, s.ldb, s.group_b, DA, p);
-    if constexpr (kDirect) load_direct<C, DA, NT, REV>(sh.b[buf], from, uint32_t(s.ldb * 2), me.size(p));
-    else rb.template load<REV>(from, uint32_t(s.ldb * 4), me.size(p));
+    if constexpr (kDirect) rb.load(sh.b[buf], from, me.size(p));
+    else rb.load(from, me.size(p));
   };
   auto fetch_c = [&](int64_t p) {
     const E* from = me.rows(s.c, s.ldc, s.group_c, DC, p);
-    if constexpr (kDirect) load_direct<C, DC, NT, REV>(sh.c, from, uint32_t(s.ldc * 2), me.size(p));
-    else rc.template load<REV>(from, uint32_t(s.ldc * 4), me.size(p));
+    if constexpr (kDirect) rc.load(sh.c, from, me.size(p));
+    else rc.load(from, me.size(p));
   };
+  // A lane's places in the tiles, and the offset of its part of an output row. Opaque in
+  // every chunk, as what is formed from them would be held in registers otherwise.
+  int at_row = Tile<C, DA, P>::row_place(me.i, me.g);
+  int at_b = Tile<C, DA, P>::column_place(0, DA == 16 ? 4 : 8, me.i, me.g);
+  int at_c = Tile<C, DC, P>::column_place(16 * wave, 4, me.i, me.g);
+  int at_first = Tile<32, 32, PS>::row_place(me.i, me.g), at_second = Tile<32, 64, PS>::row_place(me.i, me.g);
+  const uint32_t out_step = uint32_t(s.H) * DC * uint32_t(sizeof(O));  // at most 2^25: a chunk's offsets fit in 31 bits
+  uint32_t at_out = (16 * wave + 4 * me.g) * uint32_t(sizeof(O)) + (REV ? 0u - me.i * out_step : me.i * out_step);
+  // The third part of the weighted c is for the state that is a result (wanted or not, so
+  // that outputs do not depend on that).
+  const bool exact = me.seg == s.nseg - 1;
   // Order of a chunk's loads and barriers. bf16: `a` and `b` are there at the start of a
   // chunk; `c` arrives while scores and a X are formed, the next `a` (its tile is read no
   // more) and `b` (the other buffer) while the chunk's own rows are summed: two workgroups
@@ -457,8 +482,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   for (int64_t p = begin; p < end; p += C, buf ^= 1) {
     const int m = me.size(p);
     const bool more = p + C < end;
-    // opaque in every chunk: powers and LDS addresses are formed where they are used, not held
-    asm volatile("" : "+v"(me.lg), "+v"(me.i), "+v"(me.g));
+    asm volatile("" : "+v"(me.lg), "+v"(me.i), "+v"(me.g), "+v"(at_row), "+v"(at_b), "+v"(at_c), "+v"(at_first), "+v"(at_second), "+v"(at_out));
     const int i = me.i, g = me.g;
     if constexpr (kDirect) {
       fetch_c(p);
@@ -491,7 +515,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
         for (int kb = 0; kb < KB; ++kb) {
           bhalf8 av[P], bv[P];
 #pragma unroll
-          for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g), bv[q] = tb.row(q, jt, kb, i, g);
+          for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, at_row), bv[q] = tb.row(q, jt, kb, at_row);
           d = mma_parts<P, P, P - 1>(bv, av, d);
         }
 #pragma unroll
@@ -525,7 +549,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       for (int r = 0; r < RT; ++r) {
         bhalf8 av[P];
 #pragma unroll
-        for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, i, g);
+        for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, at_row);
         acc[r] = mma_parts<PS, P, PS - 1>(xv, av, acc[r]);
       }
     }
@@ -544,8 +568,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     for (int kt = 0; kt < KT; ++kt) X[kt] *= whole;
 #pragma unroll
     for (int kb = 0; kb < PB; ++kb) {
-      bhalf8 cv[P], wv[3];
-      weighted<E, DC>(sh.c, sh.weight[buf], kb, wave, i, g, cv, wv);
+      bhalf8 cv[P];
+      float x[8];
+      weighted<E, DC>(sh.c, sh.weight[buf], kb, at_c, g, cv, x);
       // A masked score is 0, but 0 times Inf is not: such values leave the product, and the
       // rows from theirs on become NaN.
       if (__builtin_expect(__any(any_bad(cv[0])), 0)) {
@@ -564,27 +589,32 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       for (int r = 2 * kb; r < RT; ++r) {
         bhalf8 sv[PS];
 #pragma unroll
-        for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, i, g);
+        for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, at_first, at_second);
         acc[r] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r]);
       }
-      add_outer<E, DA>(X, tb, kb, i, g, wv);
+      if (!S::kHalf || exact) add_outer<E, DA, 3>(X, tb, kb, at_b, x);
+      else add_outer<E, DA, 2>(X, tb, kb, at_b, x);
     }
 
     if constexpr (kDirect) wait_loads();
+    // rows 16 r + i; stores behind the chunk's end fall out of the range
+    const uint32_t top = uint32_t(m - 1) * out_step;
+    O* to = static_cast<O*>(s.out) + ((me.b * s.T + (REV ? me.n - p - m : p)) * s.H + me.h) * DC;
+    const auto range = __builtin_amdgcn_make_buffer_rsrc(to, 0, top + DC * uint32_t(sizeof(O)), 0x00020000);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int at = 16 * r + i;
-      if (at < m) {
-        const int64_t token = me.b * s.T + (REV ? me.n - 1 - p - at : p + at);
-        const int ch = 16 * wave + 4 * g;
-        float x[4] = {acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
-        if (__builtin_expect(bad, 0)) {
+      float x4[4] = {acc[r][0], acc[r][1], acc[r][2], acc[r][3]};
+      if (__builtin_expect(bad, 0)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (at >= sh.bad_from[ch + e]) x[e] = __builtin_nanf("");
-        }
-        store4(static_cast<O*>(s.out) + (token * s.H + me.h) * DC + ch, x);
+        for (int e = 0; e < 4; ++e)
+          if (16 * r + i >= sh.bad_from[16 * wave + 4 * g + e]) x4[e] = __builtin_nanf("");
       }
+      vec<O, 4> o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = O(x4[e]);
+      const uint32_t at = REV ? at_out + (top - 16u * r * out_step) : at_out + 16u * r * out_step;
+      if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vec<uint32_t, 2>, o), range, at, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vec<uint32_t, 4>, o), range, at, 0, 0);
     }
     __syncthreads();
   }
