@@ -119,7 +119,8 @@ namespace {
 
 // slot[s] += l^{positions of segment s - 1} slot[s - 1] along the segments of a (b, h): the
 // workgroup's slice of 1024 floats of its state, in the order the passes left it.
-__global__ __launch_bounds__(256) void scan_states_kernel(LinearPass s, int per_state) {
+__global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int per_state) {
+  const LinearPass s = all.pass[blockIdx.y];
   const int parts = (per_state + 1023) / 1024;
   const int64_t bh = blockIdx.x / parts;
   const int at = int(blockIdx.x % parts) * 1024 + 4 * threadIdx.x;
@@ -147,12 +148,6 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPass s, int per_
   }
 }
 
-int launch_scan(const LinearPass& s, int64_t B, int per_state, hipStream_t stream) {
-  if (s.nseg <= 2) return 0;
-  scan_states_kernel<<<unsigned(B * s.H * ((per_state + 1023) / 1024)), 256, 0, stream>>>(s, per_state);
-  return int(hipGetLastError());
-}
-
 // Segments: enough workgroups for two on each of the 256 CUs, of at least four chunks.
 void choose_segments(const LinearProblem& p, int64_t* seg, int64_t* nseg) {
   const int64_t C = p.dtype == GDN_DTYPE_BF16 ? 64 : 32;
@@ -163,19 +158,21 @@ void choose_segments(const LinearProblem& p, int64_t* seg, int64_t* nseg) {
   *nseg = std::max<int64_t>(1, (chunks + each - 1) / each);
 }
 
-// A pass from its start states to its outputs: the segments' own states, their joining, and
-// the outputs (one launch where there is one segment).
-int run_pass(const LinearPass& s, const LinearProblem& p, int da, int dc, bool rev, bool wide_out, void* stream) {
-  auto launch = [&](bool out) {
-    return p.dtype == GDN_DTYPE_BF16 ? launch_pass_bf16(s, p.B, da, dc, rev, out, wide_out, stream)
-                                     : launch_pass_f32(s, p.B, da, dc, rev, out, stream);
-  };
-  int rc = 0;
-  if (s.nseg > 1) {
-    if ((rc = launch(false)) != 0) return rc;
-    if ((rc = launch_scan(s, p.B, da * dc, static_cast<hipStream_t>(stream))) != 0) return rc;
-  }
-  return launch(true);
+int launch_pass(const LinearPasses& s, int count, const LinearProblem& p, int da, int dc, bool out, bool wide_out, void* stream) {
+  return p.dtype == GDN_DTYPE_BF16 ? launch_pass_bf16(s, count, p.B, da, dc, out, wide_out, stream)
+                                   : launch_pass_f32(s, count, p.B, da, dc, out, stream);
+}
+
+// The states before every segment of `count` passes (nothing to do for one segment): the
+// segments' own, then their joining.
+int launch_states(const LinearPasses& s, int count, const LinearProblem& p, int da, int dc, void* stream) {
+  const LinearPass& first = s.pass[0];
+  if (first.nseg == 1) return 0;
+  const int rc = launch_pass(s, count, p, da, dc, false, false, stream);
+  if (rc != 0 || first.nseg == 2) return rc;
+  const dim3 grid(unsigned(p.B * p.H * ((da * dc + 1023) / 1024)), unsigned(count));
+  scan_states_kernel<<<grid, 256, 0, static_cast<hipStream_t>(stream)>>>(s, da * dc);
+  return int(hipGetLastError());
 }
 
 LinearPass base_pass(const LinearProblem& p) {
@@ -188,7 +185,7 @@ LinearPass base_pass(const LinearProblem& p) {
   return s;
 }
 
-size_t states_bytes(const LinearProblem& p) {
+size_t states_bytes(const LinearProblem& p) {  // of one pass, a multiple of 256
   int64_t seg, nseg;
   choose_segments(p, &seg, &nseg);
   return nseg > 1 ? size_t(p.B) * size_t(p.H) * size_t(nseg) * size_t(p.dk) * size_t(p.dv) * sizeof(float) : 256;
@@ -199,20 +196,25 @@ size_t states_bytes(const LinearProblem& p) {
 size_t linear_fwd_workspace(const LinearProblem& p) { return states_bytes(p); }
 
 int launch_linear_fwd(const LinearProblem& p, void* ws, void* stream) {
-  LinearPass s = base_pass(p);
+  LinearPasses all{};
+  LinearPass& s = all.pass[0];
+  s = base_pass(p);
   s.a = p.q, s.b = p.k, s.c = p.v, s.out = p.o;
   s.lda = p.ldq, s.ldb = p.ldk, s.ldc = p.ldv;
   s.group_a = s.group_b = int(p.group), s.group_c = 1;
   s.x0 = p.s0, s.x1 = p.s_final, s.x0_sa = p.dv, s.x0_sc = 1;
   s.states = static_cast<float*>(ws), s.st_sa = 1, s.st_sc = p.dk;
-  return run_pass(s, p, int(p.dk), int(p.dv), false, false, stream);
+  const int rc = launch_states(all, 1, p, int(p.dk), int(p.dv), stream);
+  return rc != 0 ? rc : launch_pass(all, 1, p, int(p.dk), int(p.dv), true, false, stream);
 }
 
 namespace {
 
 // out[row] = the sum of `group` rows of in, for rows of d channels, rounded once.
 template <typename E>
-__global__ __launch_bounds__(256) void group_sum_kernel(const float* in, E* out, int64_t n, int d, int group) {
+__global__ __launch_bounds__(256) void group_sum_kernel(const float* in0, const float* in1, E* out0, E* out1, int64_t n, int d, int group) {
+  const float* in = blockIdx.y == 0 ? in0 : in1;
+  E* out = blockIdx.y == 0 ? out0 : out1;
   const int64_t at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= n) return;
   const int64_t row = at / d;
@@ -227,57 +229,68 @@ __global__ __launch_bounds__(256) void group_sum_kernel(const float* in, E* out,
   store4(out + at, x);
 }
 
+// Where key heads are shared, dq and dk of every value head come first, in float32.
 size_t per_head_bytes(const LinearProblem& p) {
   return p.group > 1 ? size_t(p.B) * size_t(p.T) * size_t(p.H) * size_t(p.dk) * sizeof(float) : 0;
 }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t linear_bwd_workspace(const LinearProblem& p) { return round256(states_bytes(p)) + per_head_bytes(p); }
+size_t linear_bwd_workspace(const LinearProblem& p) { return 2 * (states_bytes(p) + per_head_bytes(p)); }
 
+// Gradients: the states S before every segment and, backwards, G behind it, both transposed
+// ([dv] rows, as dq and dk take them); then the outputs of dq, dk and dv, in one launch
+// where their dimensions and types are the same.
 int launch_linear_bwd(const LinearProblem& p, const LinearGrads& g, void* ws, void* stream) {
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const int dk = int(p.dk), dv = int(p.dv), group = int(p.group);
   const bool shared = group > 1;
-  float* per_head = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(states_bytes(p)));
+  char* mem = static_cast<char*>(ws);
+  float* per_head[2] = {reinterpret_cast<float*>(mem + 2 * states_bytes(p)),
+                        reinterpret_cast<float*>(mem + 2 * states_bytes(p) + per_head_bytes(p))};
   const int64_t ldo = p.H * p.dv;
-  auto sum_groups = [&](void* out) {
-    const int64_t n = p.B * p.T * p.Hk * p.dk;
-    if (!shared || n == 0) return 0;
-    const unsigned grid = unsigned((n + 1023) / 1024);
-    if (p.dtype == GDN_DTYPE_BF16)
-      group_sum_kernel<<<grid, 256, 0, hs>>>(per_head, static_cast<__bf16*>(out), n, dk, group);
-    else
-      group_sum_kernel<<<grid, 256, 0, hs>>>(per_head, static_cast<float*>(out), n, dk, group);
-    return int(hipGetLastError());
-  };
-  LinearPass s = base_pass(p);
-  s.states = static_cast<float*>(ws);
-  s.zero_tail = p.seq_lens != nullptr;
-  int rc;
-  // dq = S do: rows (do, v, k) with the transposed state
-  s.a = g.d_o, s.b = p.v, s.c = p.k, s.out = shared ? per_head : g.dq;
-  s.lda = ldo, s.ldb = p.ldv, s.ldc = p.ldk;
-  s.group_a = s.group_b = 1, s.group_c = group;
-  s.x0 = p.s0, s.x0_sa = 1, s.x0_sc = p.dv;
-  s.st_sa = 1, s.st_sc = p.dv;
-  if ((rc = run_pass(s, p, dv, dk, false, shared, stream)) != 0) return rc;
-  if ((rc = sum_groups(g.dq)) != 0) return rc;
-  // dk = G v backwards: rows (v, do, q), G transposed
-  s.shift = 1;
-  s.a = p.v, s.b = g.d_o, s.c = p.q, s.out = shared ? per_head : g.dk;
-  s.lda = p.ldv, s.ldb = ldo, s.ldc = p.ldq;
-  s.x0 = g.d_s_final;
-  if ((rc = run_pass(s, p, dv, dk, true, shared, stream)) != 0) return rc;
-  if ((rc = sum_groups(g.dk)) != 0) return rc;
-  // dv = G^T k backwards: rows (k, q, do); its last state is ds0
-  s.a = p.k, s.b = p.q, s.c = g.d_o, s.out = g.dv;
-  s.lda = p.ldk, s.ldb = p.ldq, s.ldc = ldo;
-  s.group_a = s.group_b = group, s.group_c = 1;
-  s.x1 = g.ds0, s.x0_sa = p.dv, s.x0_sc = 1;
-  s.st_sa = 1, s.st_sc = p.dk;
-  return run_pass(s, p, dk, dv, true, false, stream);
+  LinearPasses all{};
+  LinearPass &q = all.pass[0], &k = all.pass[1], &v = all.pass[2];
+  q = base_pass(p);
+  q.zero_tail = p.seq_lens != nullptr;
+  k = v = q;
+  k.back = v.back = k.shift = v.shift = 1;
+  // dq = S do: rows (do, v, k)
+  q.a = g.d_o, q.b = p.v, q.c = p.k, q.out = shared ? per_head[0] : g.dq;
+  q.lda = ldo, q.ldb = p.ldv, q.ldc = p.ldk;
+  q.group_a = q.group_b = 1, q.group_c = group;
+  q.x0 = p.s0, q.states = reinterpret_cast<float*>(mem);
+  // dk = G v: rows (v, do, q)
+  k.a = p.v, k.b = g.d_o, k.c = p.q, k.out = shared ? per_head[1] : g.dk;
+  k.lda = p.ldv, k.ldb = ldo, k.ldc = p.ldq;
+  k.group_a = k.group_b = 1, k.group_c = group;
+  k.x0 = g.d_s_final, k.states = reinterpret_cast<float*>(mem + states_bytes(p));
+  q.x0_sa = k.x0_sa = 1, q.x0_sc = k.x0_sc = p.dv;
+  q.st_sa = k.st_sa = 1, q.st_sc = k.st_sc = p.dv;
+  // dv = G^T k: rows (k, q, do), G as dk's states have it; its last state is ds0
+  v.a = p.k, v.b = p.q, v.c = g.d_o, v.out = g.dv;
+  v.lda = p.ldk, v.ldb = p.ldq, v.ldc = ldo;
+  v.group_a = v.group_b = group, v.group_c = 1;
+  v.x0 = g.d_s_final, v.x1 = g.ds0, v.x0_sa = p.dv, v.x0_sc = 1;
+  v.states = k.states, v.st_sa = p.dv, v.st_sc = 1;
+
+  int rc = launch_states(all, 2, p, dv, dk, stream);
+  if (rc != 0) return rc;
+  const bool one = dk == dv && !shared;
+  if ((rc = launch_pass(all, one ? 3 : 2, p, dv, dk, true, shared, stream)) != 0) return rc;
+  if (!one) {
+    LinearPasses last{};
+    last.pass[0] = v;
+    if ((rc = launch_pass(last, 1, p, dk, dv, true, false, stream)) != 0) return rc;
+  }
+  const int64_t n = p.B * p.T * p.Hk * p.dk;
+  if (!shared || n == 0) return 0;
+  const dim3 grid(unsigned((n + 1023) / 1024), 2);
+  if (p.dtype == GDN_DTYPE_BF16)
+    group_sum_kernel<<<grid, 256, 0, hs>>>(per_head[0], per_head[1], static_cast<__bf16*>(g.dq), static_cast<__bf16*>(g.dk), n, dk, group);
+  else
+    group_sum_kernel<<<grid, 256, 0, hs>>>(per_head[0], per_head[1], static_cast<float*>(g.dq), static_cast<float*>(g.dk), n, dk, group);
+  return int(hipGetLastError());
 }
 
 }  // namespace gdn

@@ -3,10 +3,10 @@
 
 namespace gdn {
 
-int launch_pass_bf16(const LinearPass& s, int64_t B, int da, int dc, bool rev, bool out, bool wide_out, void* stream) {
+int launch_pass_bf16(const LinearPasses& s, int count, int64_t B, int da, int dc, bool out, bool wide_out, void* stream) {
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  return wide_out ? launch_pass_any<__bf16, float>(s, B, da, dc, rev, out, hs)
-                  : launch_pass_any<__bf16, __bf16>(s, B, da, dc, rev, out, hs);
+  return wide_out ? launch_pass_any<__bf16, float>(s, count, B, da, dc, out, hs)
+                  : launch_pass_any<__bf16, __bf16>(s, count, B, da, dc, out, hs);
 }
 
 }  // namespace gdn

@@ -3,8 +3,8 @@
 
 namespace gdn {
 
-int launch_pass_f32(const LinearPass& s, int64_t B, int da, int dc, bool rev, bool out, void* stream) {
-  return launch_pass_any<float, float>(s, B, da, dc, rev, out, static_cast<hipStream_t>(stream));
+int launch_pass_f32(const LinearPasses& s, int count, int64_t B, int da, int dc, bool out, void* stream) {
+  return launch_pass_any<float, float>(s, count, B, da, dc, out, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace gdn

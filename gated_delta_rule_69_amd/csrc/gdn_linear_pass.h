@@ -51,6 +51,13 @@ struct LinearPass {
   int nseg;
   int shift;
   int zero_tail;               // write zeros to rows behind the sequence
+  int back;                    // from the last token to the first
+};
+
+// Passes of one launch, all of the same dimensions: blockIdx.y tells which.
+constexpr int kMostPasses = 3;
+struct LinearPasses {
+  LinearPass pass[kMostPasses];
 };
 
 // log of a head's decay; everything below e^-128 is taken as 0, -Inf included.
@@ -182,22 +189,23 @@ template <int C, int PARTS> struct Scores {
 // wave's base + 16 l, so the tile's slots are chosen by where a lane loads from). The
 // loads are written as assembly, which has no registers to guard and leaves the waiting to
 // wait_loads(); the compiler's own counts only ever wait for more.
-template <int C, int D, int NT, bool REV> struct Direct {
+template <int C, int D, int NT> struct Direct {
   static constexpr int kSlots = D / 8, kAll = C * kSlots;
   static constexpr int kRows = NT / kSlots;        // rows a step of the workgroup covers
   static constexpr bool kSame = kRows % 16 == 0;   // so that turn() is the same in each
+  bool back;
   uint32_t step;    // bytes from row to row
   uint32_t offset;  // of the thread's slot of its first row
   __device__ __forceinline__ uint32_t offset_of(uint32_t at) const {
     const uint32_t row = at / kSlots, to = (at % kSlots ^ Tile<C, D, 1>::turn(row)) * 16;
-    return REV ? to - row * step : to + row * step;
+    return back ? to - row * step : to + row * step;
   }
-  __device__ __forceinline__ Direct(int64_t ld) : step(uint32_t(ld * 2)), offset(offset_of(threadIdx.x)) {}
+  __device__ __forceinline__ Direct(int64_t ld, bool back_) : back(back_), step(uint32_t(ld * 2)), offset(offset_of(threadIdx.x)) {}
   __device__ __forceinline__ void load(Tile<C, D, 1>& t, const __bf16* base, int rows) const {
     typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
     auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
     const uint64_t from = reinterpret_cast<uintptr_t>(base);
-    const uint32_t top = uint32_t(rows - 1) * step;
+    const uint32_t top = uint32_t(rows - 1) * step, from_end = back ? top : 0;
     const uint4v range = {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(top + 2 * D), 0x00020000u};
     const uint32_t lds = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) __bf16*)(t.x)));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -205,28 +213,29 @@ template <int C, int D, int NT, bool REV> struct Direct {
     for (int n = 0; n < (kAll + NT - 1) / NT; ++n) {
       const int first = n * NT + 64 * wave;
       if (kAll % NT != 0 && first >= kAll) break;
-      const uint32_t here = kSame ? offset + (REV ? 0u - uint32_t(n * kRows) * step : uint32_t(n * kRows) * step)
-                                  : offset_of(n * NT + threadIdx.x);
+      const uint32_t here = kSame ? offset + (back ? 0u - uint32_t(n * kRows) * step : uint32_t(n * kRows) * step) + from_end
+                                  : offset_of(n * NT + threadIdx.x) + from_end;
       asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :: "{m0}"(uniform(lds + 16 * first)), "v"(REV ? here + top : here), "s"(range) : "memory");
+                   :: "{m0}"(uniform(lds + 16 * first)), "v"(here), "s"(range) : "memory");
     }
   }
 };
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // float32 rows pass through registers, where they become three bf16 planes.
-template <int C, int D, int NT, bool REV> struct Staged {
+template <int C, int D, int NT> struct Staged {
   static constexpr int kPerRow = D / 4;
   static constexpr int kCount = (C * kPerRow + NT - 1) / NT;
   uint4 v[kCount];
+  bool back;
   uint32_t step;
-  __device__ __forceinline__ Staged(int64_t ld) : step(uint32_t(ld * 4)) {}
+  __device__ __forceinline__ Staged(int64_t ld, bool back_) : back(back_), step(uint32_t(ld * 4)) {}
   __device__ __forceinline__ void load(const float* base, int rows) {
     const auto range = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), 0, uint32_t(rows - 1) * step + 4 * D, 0x00020000);
 #pragma unroll
     for (int n = 0; n < kCount; ++n) {
       const uint32_t at = threadIdx.x + n * NT, row = at / kPerRow, col = at % kPerRow;
-      v[n] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(range, (REV ? uint32_t(rows - 1) - row : row) * step + col * 16, 0, 0));
+      v[n] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(range, (back ? uint32_t(rows - 1) - row : row) * step + col * 16, 0, 0));
     }
   }
   template <int PARTS>
@@ -254,7 +263,7 @@ __device__ __forceinline__ bool is_bad(__bf16 x) { return (__builtin_bit_cast(ui
 
 // What both kernels of a pass know of their workgroup's segment, and the state of a wave's
 // sixteen columns in accumulators.
-template <typename E, int DA, int DC, bool REV> struct Segment {
+template <typename E, int DA, int DC> struct Segment {
   static constexpr int C = PassShape<E>::kChunk, NT = 64 * pass_waves(DC), KT = DA / 16;
   const LinearPass& s;
   int wave, i, g, h, seg;
@@ -280,7 +289,7 @@ template <typename E, int DA, int DC, bool REV> struct Segment {
   __device__ __forceinline__ int size(int64_t p) const { return int(end - p < C ? end - p : C); }  // positions of the chunk at p
   // first token in memory of positions p .. p + m - 1: token p, or n - m - p backwards
   __device__ __forceinline__ const E* rows(const void* x, int64_t ld, int group, int d, int64_t p) const {
-    return static_cast<const E*>(x) + (b * s.T + (REV ? n - size(p) - p : p)) * ld + int64_t(h / group) * d;
+    return static_cast<const E*>(x) + (b * s.T + (s.back ? n - size(p) - p : p)) * ld + int64_t(h / group) * d;
   }
   // a lane's first channel in state tile kt (four rows), and its column
   __device__ __forceinline__ int row_channel(int kt) const { return KT == 1 ? 4 * g : 32 * (kt / 2) + 8 * g + 4 * (kt % 2); }
@@ -347,8 +356,9 @@ __device__ __forceinline__ void add_outer(float4v (&X)[DA / 16], const T& tile, 
 // l^{end-1-p} b_p c_p^T, for scan_states to join. A segment is walked from its end, so that
 // nothing is scaled on the way, the positions whose weight is under 2^-127 (0 in float32)
 // are never read, and what the outputs' kernel reads first was read here last.
-template <typename E, int DA, int DC, bool REV>
-__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_states_kernel(LinearPass s) {
+template <typename E, int DA, int DC>
+__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_states_kernel(LinearPasses all) {
+  const LinearPass s = all.pass[blockIdx.y];
   using S = PassShape<E>;
   constexpr int C = S::kChunk, NT = 64 * pass_waves(DC), P = S::kParts;
   constexpr bool kDirect = S::kHalf;
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     float weight[2][C];
   };
   __shared__ Shared sh;
-  const Segment<E, DA, DC, REV> me(s, s.nseg - 1);
+  const Segment<E, DA, DC> me(s, s.nseg - 1);
   float4v X[DA / 16];
   float* slots = s.states + me.bh * s.nseg * (DA * DC);
   const int64_t begin = me.begin, end = me.end;
@@ -371,8 +381,8 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 #pragma unroll
   for (int kt = 0; kt < DA / 16; ++kt) X[kt] *= whole;
 
-  std::conditional_t<kDirect, Direct<C, DA, NT, REV>, Staged<C, DA, NT, REV>> rb(s.ldb);
-  std::conditional_t<kDirect, Direct<C, DC, NT, REV>, Staged<C, DC, NT, REV>> rc(s.ldc);
+  std::conditional_t<kDirect, Direct<C, DA, NT>, Staged<C, DA, NT>> rb(s.ldb, s.back);
+  std::conditional_t<kDirect, Direct<C, DC, NT>, Staged<C, DC, NT>> rc(s.ldc, s.back);
   auto fetch = [&](int64_t p, int buf) {
     const E *fb = me.rows(s.b, s.ldb, s.group_b, DA, p), *fc = me.rows(s.c, s.ldc, s.group_c, DC, p);
     if constexpr (kDirect) rb.load(sh.b[buf], fb, me.size(p)), rc.load(sh.c[buf], fc, me.size(p));
@@ -408,8 +418,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 
 // The outputs of a segment, chunk by chunk from the state before it; the last segment's
 // workgroup also has the pass's last state.
-template <typename E, typename O, int DA, int DC, bool REV>
-__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_outputs_kernel(LinearPass s) {
+template <typename E, typename O, int DA, int DC>
+__global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) void linear_outputs_kernel(LinearPasses all) {
+  const LinearPass s = all.pass[blockIdx.y];
   using S = PassShape<E>;
   constexpr int C = S::kChunk, NW = pass_waves(DC), NT = 64 * NW;
   constexpr int P = S::kParts, PS = S::kScoreParts;
@@ -426,7 +437,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
   };
   __shared__ Shared sh;
-  Segment<E, DA, DC, REV> me(s, s.nseg);
+  Segment<E, DA, DC> me(s, s.nseg);
   const int wave = me.wave;
   const int64_t begin = me.begin, end = me.end;
   float4v X[KT];
@@ -435,8 +446,8 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   else
     me.load_state(X, me.seg == 0 && s.x0 == nullptr ? nullptr : s.states + (me.bh * s.nseg + me.seg) * (DA * DC), s.st_sa, s.st_sc);
 
-  std::conditional_t<kDirect, Direct<C, DA, NT, REV>, Staged<C, DA, NT, REV>> ra(s.lda), rb(s.ldb);
-  std::conditional_t<kDirect, Direct<C, DC, NT, REV>, Staged<C, DC, NT, REV>> rc(s.ldc);
+  std::conditional_t<kDirect, Direct<C, DA, NT>, Staged<C, DA, NT>> ra(s.lda, s.back), rb(s.ldb, s.back);
+  std::conditional_t<kDirect, Direct<C, DC, NT>, Staged<C, DC, NT>> rc(s.ldc, s.back);
   auto fetch_a = [&](int64_t p) {
     const E* from = me.rows(s.a, s.lda, s.group_a, DA, p);
     if constexpr (kDirect) ra.load(sh.a, from, me.size(p));
@@ -459,7 +470,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   int at_c = Tile<C, DC, P>::column_place(16 * wave, 4, me.i, me.g);
   int at_first = Tile<32, 32, PS>::row_place(me.i, me.g), at_second = Tile<32, 64, PS>::row_place(me.i, me.g);
   const uint32_t out_step = uint32_t(s.H) * DC * uint32_t(sizeof(O));  // at most 2^25: a chunk's offsets fit in 31 bits
-  uint32_t at_out = (16 * wave + 4 * me.g) * uint32_t(sizeof(O)) + (REV ? 0u - me.i * out_step : me.i * out_step);
+  uint32_t at_out = (16 * wave + 4 * me.g) * uint32_t(sizeof(O)) + (s.back ? 0u - me.i * out_step : me.i * out_step);
   // The third part of the weighted c is for the state that is a result (wanted or not, so
   // that outputs do not depend on that).
   const bool exact = me.seg == s.nseg - 1;
@@ -599,7 +610,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     if constexpr (kDirect) wait_loads();
     // rows 16 r + i; stores behind the chunk's end fall out of the range
     const uint32_t top = uint32_t(m - 1) * out_step;
-    O* to = static_cast<O*>(s.out) + ((me.b * s.T + (REV ? me.n - p - m : p)) * s.H + me.h) * DC;
+    O* to = static_cast<O*>(s.out) + ((me.b * s.T + (s.back ? me.n - p - m : p)) * s.H + me.h) * DC;
     const auto range = __builtin_amdgcn_make_buffer_rsrc(to, 0, top + DC * uint32_t(sizeof(O)), 0x00020000);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -612,7 +623,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       vec<O, 4> o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = O(x4[e]);
-      const uint32_t at = REV ? at_out + (top - 16u * r * out_step) : at_out + 16u * r * out_step;
+      const uint32_t at = at_out + (s.back ? top - 16u * r * out_step : 16u * r * out_step);
       if constexpr (sizeof(O) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vec<uint32_t, 2>, o), range, at, 0, 0);
       else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vec<uint32_t, 4>, o), range, at, 0, 0);
     }
@@ -631,28 +642,25 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     me.store_state(X, s.x1 == nullptr ? nullptr : s.x1 + me.bh * (DA * DC), s.x0_sa, s.x0_sc);
 }
 
-// Launches of one direction and type, in the translation units of each element type.
-int launch_pass_bf16(const LinearPass& s, int64_t B, int da, int dc, bool rev, bool out, bool wide_out, void* stream);
-int launch_pass_f32(const LinearPass& s, int64_t B, int da, int dc, bool rev, bool out, void* stream);
+// Launches of `count` passes of B sequences of either type, in their own translation units:
+// the segments' states, or the outputs (float32 where wide_out).
+int launch_pass_bf16(const LinearPasses& s, int count, int64_t B, int da, int dc, bool out, bool wide_out, void* stream);
+int launch_pass_f32(const LinearPasses& s, int count, int64_t B, int da, int dc, bool out, void* stream);
 
 template <typename E, typename O, int DA, int DC>
-int launch_pass_dims(const LinearPass& s, int64_t B, bool rev, bool out, hipStream_t stream) {
+int launch_pass_dims(const LinearPasses& s, int count, int64_t B, bool out, hipStream_t stream) {
   constexpr int kThreads = 64 * pass_waves(DC);
-  const unsigned grid = unsigned(B * s.H * (out ? s.nseg : s.nseg - 1));
-  if (!out) {
-    if (rev) linear_states_kernel<E, DA, DC, true><<<grid, kThreads, 0, stream>>>(s);
-    else linear_states_kernel<E, DA, DC, false><<<grid, kThreads, 0, stream>>>(s);
-  } else {
-    if (rev) linear_outputs_kernel<E, O, DA, DC, true><<<grid, kThreads, 0, stream>>>(s);
-    else linear_outputs_kernel<E, O, DA, DC, false><<<grid, kThreads, 0, stream>>>(s);
-  }
+  const LinearPass& p = s.pass[0];
+  const dim3 grid(unsigned(B * p.H * (out ? p.nseg : p.nseg - 1)), unsigned(count));
+  if (out) linear_outputs_kernel<E, O, DA, DC><<<grid, kThreads, 0, stream>>>(s);
+  else linear_states_kernel<E, DA, DC><<<grid, kThreads, 0, stream>>>(s);
   return int(hipGetLastError());
 }
 
 template <typename E, typename O>
-int launch_pass_any(const LinearPass& s, int64_t B, int da, int dc, bool rev, bool out, hipStream_t stream) {
+int launch_pass_any(const LinearPasses& s, int count, int64_t B, int da, int dc, bool out, hipStream_t stream) {
   switch (da * 1000 + dc) {
-#define GDN_PASS(DA, DC) case DA * 1000 + DC: return launch_pass_dims<E, O, DA, DC>(s, B, rev, out, stream);
+#define GDN_PASS(DA, DC) case DA * 1000 + DC: return launch_pass_dims<E, O, DA, DC>(s, count, B, out, stream);
     GDN_PASS(16, 16) GDN_PASS(16, 32) GDN_PASS(16, 64) GDN_PASS(16, 128)
     GDN_PASS(32, 16) GDN_PASS(32, 32) GDN_PASS(32, 64) GDN_PASS(32, 128)
     GDN_PASS(64, 16) GDN_PASS(64, 32) GDN_PASS(64, 64) GDN_PASS(64, 128)
