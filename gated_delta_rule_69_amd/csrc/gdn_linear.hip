@@ -148,14 +148,31 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int 
   }
 }
 
-// Segments: enough workgroups for two on each of the 256 CUs, of at least four chunks.
-void choose_segments(const LinearProblem& p, int64_t* seg, int64_t* nseg) {
-  const int64_t C = p.dtype == GDN_DTYPE_BF16 ? 64 : 32;
+// Segments of `passes` passes that share a launch: as many workgroups as the 256 CUs hold at
+// once (by LDS, and by registers 16 waves a CU in bf16 and 12 in float32), a third more of a
+// padded batch, where some find nothing to do; each at least four chunks (three of float32).
+// Measured at bf16 d 128: B2 T32768 H16 forward with 256 / 512 / 768 / 1024 workgroups 417 /
+// 378 / 435 / 408 us; B2 T4096 gradients with 170 / 256 / 512 a pass 135 / 152 / 170 us; B1
+// T4096 forward with 2 / 4 / 8 chunks at least 54 / 47 / 63 us. Padded float32 B8 T2047 H32
+// d64 with 768 / 1024 / 1536: 145 / 130 / 141 us.
+struct Segments {
+  int64_t tokens, count;
+};
+Segments choose_segments(const LinearProblem& p, int da, int dc, int passes) {
+  const bool half = p.dtype == GDN_DTYPE_BF16;
+  const int64_t C = half ? 64 : 32;
+  const int64_t lds = half ? 2 * C * (3 * da + dc) + 13312 : 6 * C * (2 * da + dc) + 7168;
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((160 << 10) / lds, (half ? 16 : 12) / pass_waves(dc)));
+  const int64_t wanted = 256 * resident * (p.seq_lens != nullptr ? 4 : 3) / 3;
   const int64_t chunks = (p.T + C - 1) / C;
-  const int64_t want = std::max<int64_t>(1, 512 / (p.B * p.H));
-  const int64_t each = std::max<int64_t>(4, (chunks + want - 1) / want);
-  *seg = each * C;
-  *nseg = std::max<int64_t>(1, (chunks + each - 1) / each);
+  const int64_t want = std::max<int64_t>(1, wanted / (p.B * p.H * passes));
+  const int64_t each = std::max<int64_t>(half ? 4 : 3, (chunks + want - 1) / want);
+  return {each * C, std::max<int64_t>(1, (chunks + each - 1) / each)};
+}
+Segments forward_segments(const LinearProblem& p) { return choose_segments(p, int(p.dk), int(p.dv), 1); }
+// dq, dk and dv in one launch where they can be, else dq and dk
+Segments backward_segments(const LinearProblem& p) {
+  return choose_segments(p, int(p.dv), int(p.dk), p.dk == p.dv && p.group == 1 ? 3 : 2);
 }
 
 int launch_pass(const LinearPasses& s, int count, const LinearProblem& p, int da, int dc, bool out, bool wide_out, void* stream) {
@@ -175,30 +192,28 @@ int launch_states(const LinearPasses& s, int count, const LinearProblem& p, int 
   return int(hipGetLastError());
 }
 
-LinearPass base_pass(const LinearProblem& p) {
+LinearPass base_pass(const LinearProblem& p, const Segments& segments) {
   LinearPass s{};
   s.H = int(p.H), s.T = p.T;
   s.log_decay = p.log_decay, s.seq_lens = p.seq_lens;
-  int64_t nseg;
-  choose_segments(p, &s.seg, &nseg);
-  s.nseg = int(nseg);
+  s.seg = segments.tokens, s.nseg = int(segments.count);
   return s;
 }
 
-size_t states_bytes(const LinearProblem& p) {  // of one pass, a multiple of 256
-  int64_t seg, nseg;
-  choose_segments(p, &seg, &nseg);
-  return nseg > 1 ? size_t(p.B) * size_t(p.H) * size_t(nseg) * size_t(p.dk) * size_t(p.dv) * sizeof(float) : 256;
+// Bytes of a pass's states, a multiple of 256.
+size_t states_bytes(const LinearProblem& p, const Segments& segments) {
+  if (segments.count == 1) return 256;
+  return size_t(p.B) * size_t(p.H) * size_t(segments.count) * size_t(p.dk) * size_t(p.dv) * sizeof(float);
 }
 
 }  // namespace
 
-size_t linear_fwd_workspace(const LinearProblem& p) { return states_bytes(p); }
+size_t linear_fwd_workspace(const LinearProblem& p) { return states_bytes(p, forward_segments(p)); }
 
 int launch_linear_fwd(const LinearProblem& p, void* ws, void* stream) {
   LinearPasses all{};
   LinearPass& s = all.pass[0];
-  s = base_pass(p);
+  s = base_pass(p, forward_segments(p));
   s.a = p.q, s.b = p.k, s.c = p.v, s.out = p.o;
   s.lda = p.ldq, s.ldb = p.ldk, s.ldc = p.ldv;
   s.group_a = s.group_b = int(p.group), s.group_c = 1;
@@ -236,7 +251,9 @@ size_t per_head_bytes(const LinearProblem& p) {
 
 }  // namespace
 
-size_t linear_bwd_workspace(const LinearProblem& p) { return 2 * (states_bytes(p) + per_head_bytes(p)); }
+size_t linear_bwd_workspace(const LinearProblem& p) {
+  return 2 * (states_bytes(p, backward_segments(p)) + per_head_bytes(p));
+}
 
 // Gradients: the states S before every segment and, backwards, G behind it, both transposed
 // ([dv] rows, as dq and dk take them); then the outputs of dq, dk and dv, in one launch
@@ -246,12 +263,14 @@ int launch_linear_bwd(const LinearProblem& p, const LinearGrads& g, void* ws, vo
   const int dk = int(p.dk), dv = int(p.dv), group = int(p.group);
   const bool shared = group > 1;
   char* mem = static_cast<char*>(ws);
-  float* per_head[2] = {reinterpret_cast<float*>(mem + 2 * states_bytes(p)),
-                        reinterpret_cast<float*>(mem + 2 * states_bytes(p) + per_head_bytes(p))};
+  const Segments segments = backward_segments(p);
+  const size_t states = states_bytes(p, segments);
+  float* per_head[2] = {reinterpret_cast<float*>(mem + 2 * states),
+                        reinterpret_cast<float*>(mem + 2 * states + per_head_bytes(p))};
   const int64_t ldo = p.H * p.dv;
   LinearPasses all{};
   LinearPass &q = all.pass[0], &k = all.pass[1], &v = all.pass[2];
-  q = base_pass(p);
+  q = base_pass(p, segments);
   q.zero_tail = p.seq_lens != nullptr;
   k = v = q;
   k.back = v.back = k.shift = v.shift = 1;
@@ -264,7 +283,7 @@ int launch_linear_bwd(const LinearProblem& p, const LinearGrads& g, void* ws, vo
   k.a = p.v, k.b = g.d_o, k.c = p.q, k.out = shared ? per_head[1] : g.dk;
   k.lda = p.ldv, k.ldb = ldo, k.ldc = p.ldq;
   k.group_a = k.group_b = 1, k.group_c = group;
-  k.x0 = g.d_s_final, k.states = reinterpret_cast<float*>(mem + states_bytes(p));
+  k.x0 = g.d_s_final, k.states = reinterpret_cast<float*>(mem + states);
   q.x0_sa = k.x0_sa = 1, q.x0_sc = k.x0_sc = p.dv;
   q.st_sa = k.st_sa = 1, q.st_sc = k.st_sc = p.dv;
   // dv = G^T k: rows (k, q, do), G as dk's states have it; its last state is ds0
