@@ -9,6 +9,7 @@ belongs to that stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -54,6 +55,19 @@ class GdnGatedNormGrads(ctypes.Structure):
     _fields_ = [("dy", _ptr), ("dx", _ptr), ("dgate", _ptr), ("dweight", _ptr)]
 
 
+def _packer(structure):
+    """A function that packs a structure's fields, in order, into bytes: a few times faster
+    than filling the ctypes structure, which counts for one decoded token."""
+    codes = {_i32: "i", _i64: "q", _ptr: "P", _f32: "f"}
+    fmt = struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_))
+    assert fmt.size == ctypes.sizeof(structure)
+    return fmt.pack
+
+
+_linear_pack, _linear_grads_pack = _packer(GdnLinearArgs), _packer(GdnLinearGrads)
+_qk_pack, _qk_grads_pack = _packer(GdnQkNormArgs), _packer(GdnQkNormGrads)
+_gated_pack, _gated_grads_pack = _packer(GdnGatedNormArgs), _packer(GdnGatedNormGrads)
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _lib = None
 
 
@@ -61,20 +75,19 @@ def _library():
     global _lib
     if _lib is None:
         lib = load_library()
-        size, P = ctypes.c_size_t, ctypes.POINTER
-        la, qa, ga = P(GdnLinearArgs), P(GdnQkNormArgs), P(GdnGatedNormArgs)
+        size, status = ctypes.c_size_t, ctypes.c_int   # every pointer is untyped: structures come as bytes
         for name, args, res in (
-                ("gdn_linear_workspace_bytes", [la], size),
-                ("gdn_linear_chunk_fwd", [la, _ptr, size, _ptr], ctypes.c_int),
-                ("gdn_linear_recurrent_step", [la, _ptr, _ptr], ctypes.c_int),
-                ("gdn_linear_bwd_workspace_bytes", [la], size),
-                ("gdn_linear_chunk_bwd", [la, _ptr, _ptr, P(GdnLinearGrads), _ptr, size, _ptr], ctypes.c_int),
-                ("gdn_qk_norm_fwd", [qa, _ptr], ctypes.c_int),
-                ("gdn_qk_norm_bwd_workspace_bytes", [qa], size),
-                ("gdn_qk_norm_bwd", [qa, P(GdnQkNormGrads), _ptr, size, _ptr], ctypes.c_int),
-                ("gdn_gated_norm_fwd", [ga, _ptr], ctypes.c_int),
-                ("gdn_gated_norm_bwd_workspace_bytes", [ga], size),
-                ("gdn_gated_norm_bwd", [ga, P(GdnGatedNormGrads), _ptr, size, _ptr], ctypes.c_int)):
+                ("gdn_linear_workspace_bytes", [_ptr], size),
+                ("gdn_linear_chunk_fwd", [_ptr, _ptr, size, _ptr], status),
+                ("gdn_linear_recurrent_step", [_ptr, _ptr, _ptr], status),
+                ("gdn_linear_bwd_workspace_bytes", [_ptr], size),
+                ("gdn_linear_chunk_bwd", [_ptr, _ptr, _ptr, _ptr, _ptr, size, _ptr], status),
+                ("gdn_qk_norm_fwd", [_ptr, _ptr], status),
+                ("gdn_qk_norm_bwd_workspace_bytes", [_ptr], size),
+                ("gdn_qk_norm_bwd", [_ptr, _ptr, _ptr, size, _ptr], status),
+                ("gdn_gated_norm_fwd", [_ptr, _ptr], status),
+                ("gdn_gated_norm_bwd_workspace_bytes", [_ptr], size),
+                ("gdn_gated_norm_bwd", [_ptr, _ptr, _ptr, size, _ptr], status)):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         _lib = lib
@@ -85,13 +98,14 @@ def _library():
 
 def _elsewhere(t, name, stream):
     """Whether the call has to switch device or stream first; refuses host tensors."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, {name} on {t.device}")
         return True
-    return t.get_device() != torch.cuda.current_device()
+    return dev != _current_device()
 
 
 def _on(t, stream):
@@ -105,18 +119,24 @@ def _io(t, name):
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}") from None
 
 
-def _rows(t, name, shape, dtype, dev):
-    """Checks a [B, T, h, d] tensor that may be a view of a wider one; its token stride."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be a device tensor on {dev}")
-    if t.dtype != dtype:
+def _refuse(t, name, shape, dtype, dev):
+    """Says what is wrong with a tensor of another device, type or shape."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on cuda:{dev}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name, shape, dtype, dev):
+    """Checks a [B, T, h, d] tensor that may be a view of a wider one; its token stride (0:
+    contiguous)."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
+    if t.is_contiguous():
+        return 0
     B, T, h, d = shape
     sb, st, sh, sd = t.stride()
-    if B * T == 0:
-        return 0
     ld = st if T > 1 else sb if B > 1 else h * d
     if sd != 1 or (h > 1 and sh != d) or ld < h * d or (B > 1 and sb != T * ld):
         raise ValueError(f"{name} must have contiguous heads and sequences T tokens apart, got strides {t.stride()}")
@@ -124,38 +144,31 @@ def _rows(t, name, shape, dtype, dev):
 
 
 def _whole(t, name, shape, dtype, dev):
-    """Checks a contiguous tensor; its address (None for no tensor)."""
+    """Checks a contiguous tensor; its address (0 for no tensor)."""
     if t is None:
-        return None
-    if t.device != dev:
-        raise ValueError(f"{name} must be a device tensor on {dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return 0
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _heads(t, name):
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, T, heads, d], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be [B, T, heads, d], got {tuple(shape)}")
+    return shape
 
 
-def _stream():
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-
-
-def _workspace(ws, need, where, dev):
-    """The workspace's address and size; the tensor is returned to be kept alive."""
+def _workspace(ws, need, where, like):
+    """The workspace, its address and its size."""
     if need == 0:
         raise GdnError(-2, where)
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous device tensor on {dev}")
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous device tensor on {like.device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -167,19 +180,17 @@ def _done(status, where):
 # ---- linear attention -------------------------------------------------------------------
 
 def _linear_args(q, k, v, log_decay, seq_lens, s0, s_final, o):
-    dtype, dev = v.dtype, v.device
+    dtype, dev = v.dtype, v.get_device()
     io = _io(v, "v")
-    B, T, H, dv = _heads(v, "v")
+    B, T, H, dv = rows = _heads(v, "v")
     Hk, dk = _heads(k, "k")[2:]
-    key = (B, T, Hk, dk)
-    state = (B, H, dk, dv)
-    f32 = torch.float32
-    return GdnLinearArgs(
+    key, state, f32 = (B, T, Hk, dk), (B, H, dk, dv), torch.float32
+    return _linear_pack(
         io, 0, B, T, H, Hk, dk, dv, _rows(q, "q", key, dtype, dev), _rows(k, "k", key, dtype, dev),
-        _rows(v, "v", (B, T, H, dv), dtype, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _rows(v, "v", rows, dtype, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
         _whole(log_decay, "log_decay", (H,), f32, dev), _whole(seq_lens, "seq_lens", (B,), torch.int32, dev),
         _whole(s0, "s0", state, f32, dev), _whole(s_final, "s_final", state, f32, dev),
-        _whole(o, "o", (B, T, H, dv), dtype, dev))
+        _whole(o, "o", rows, dtype, dev))
 
 
 def gdn_linear_chunk_fwd(q, k, v, log_decay, *, s0=None, s_final=None, o=None, seq_lens=None, workspace=None,
@@ -195,13 +206,13 @@ def gdn_linear_chunk_fwd(q, k, v, log_decay, *, s0=None, s_final=None, o=None, s
                                         workspace=workspace, want_state=want_state)
     lib = _library()
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = v.new_empty(v.shape)
     if s_final is None and want_state:
         B, _, H, dv = _heads(v, "v")
-        s_final = torch.empty((B, H, k.shape[-1], dv), dtype=torch.float32, device=v.device)
-    a = ctypes.byref(_linear_args(q, k, v, log_decay, seq_lens, s0, s_final, o))
-    ws, at, size = _workspace(workspace, lib.gdn_linear_workspace_bytes(a), "gdn_linear_workspace_bytes", v.device)
-    _done(lib.gdn_linear_chunk_fwd(a, at, size, _stream()), "gdn_linear_chunk_fwd")
+        s_final = v.new_empty((B, H, k.shape[-1], dv), dtype=torch.float32)
+    a = _linear_args(q, k, v, log_decay, seq_lens, s0, s_final, o)
+    ws, at, size = _workspace(workspace, lib.gdn_linear_workspace_bytes(a), "gdn_linear_workspace_bytes", v)
+    _done(lib.gdn_linear_chunk_fwd(a, at, size, _current_stream(v.get_device())), "gdn_linear_chunk_fwd")
     return o, s_final
 
 
@@ -212,9 +223,10 @@ def gdn_linear_recurrent_step(q, k, v, log_decay, *, state, o=None, seq_lens=Non
         with _on(v, stream):
             return gdn_linear_recurrent_step(q, k, v, log_decay, state=state, o=o, seq_lens=seq_lens)
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = v.new_empty(v.shape)
     a = _linear_args(q, k, v, log_decay, seq_lens, state, None, o)
-    _done(_library().gdn_linear_recurrent_step(ctypes.byref(a), a.s0, _stream()), "gdn_linear_recurrent_step")
+    _done(_library().gdn_linear_recurrent_step(a, state.data_ptr(), _current_stream(v.get_device())),
+          "gdn_linear_recurrent_step")
     return o
 
 
@@ -228,24 +240,22 @@ def gdn_linear_chunk_bwd(q, k, v, log_decay, *, d_o, s0=None, ds_final=None, seq
             return gdn_linear_chunk_bwd(q, k, v, log_decay, d_o=d_o, s0=s0, ds_final=ds_final, seq_lens=seq_lens,
                                         workspace=workspace)
     lib = _library()
-    args = _linear_args(q, k, v, log_decay, seq_lens, s0, None, None)
-    dev, dtype = v.device, v.dtype
-    state = (args.B, args.H, args.dk, args.dv)
-    up = _whole(d_o, "d_o", v.shape, dtype, dev)
-    up_state = _whole(ds_final, "ds_final", state, torch.float32, dev)
-    out = {"dq": torch.empty(q.shape, dtype=dtype, device=dev), "dk": torch.empty(k.shape, dtype=dtype, device=dev),
-           "dv": torch.empty(v.shape, dtype=dtype, device=dev), "ds0": torch.empty(state, dtype=torch.float32, device=dev)}
-    g = GdnLinearGrads(*(t.data_ptr() for t in out.values()))
-    a = ctypes.byref(args)
-    ws, at, size = _workspace(workspace, lib.gdn_linear_bwd_workspace_bytes(a), "gdn_linear_bwd_workspace_bytes", dev)
-    _done(lib.gdn_linear_chunk_bwd(a, up, up_state, ctypes.byref(g), at, size, _stream()), "gdn_linear_chunk_bwd")
+    a = _linear_args(q, k, v, log_decay, seq_lens, s0, None, None)
+    dev, f32 = v.get_device(), torch.float32
+    state = (v.shape[0], v.shape[2], k.shape[3], v.shape[3])
+    up, up_state = _whole(d_o, "d_o", v.shape, v.dtype, dev), _whole(ds_final, "ds_final", state, f32, dev)
+    out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape),
+           "ds0": v.new_empty(state, dtype=f32)}
+    g = _linear_grads_pack(*(t.data_ptr() for t in out.values()))
+    ws, at, size = _workspace(workspace, lib.gdn_linear_bwd_workspace_bytes(a), "gdn_linear_bwd_workspace_bytes", v)
+    _done(lib.gdn_linear_chunk_bwd(a, up, up_state, g, at, size, _current_stream(dev)), "gdn_linear_chunk_bwd")
     return out
 
 
 # ---- norms of queries and keys -----------------------------------------------------------
 
 def _qk_args(q, k, wq, wk, norm, eps, q_scale, cos, sin, positions, interleaved, q_out, k_out):
-    dtype, dev = q.dtype, q.device
+    dtype, dev = q.dtype, q.get_device()
     io = _io(q, "q")
     B, T, Hq, d = _heads(q, "q")
     Hk = _heads(k, "k")[2]
@@ -263,7 +273,7 @@ def _qk_args(q, k, wq, wk, norm, eps, q_scale, cos, sin, positions, interleaved,
     elif positions is not None:
         raise ValueError("positions need cos and sin")
     f32, table, qs, ks = torch.float32, (n_pos, rot // 2), (B, T, Hq, d), (B, T, Hk, d)
-    return GdnQkNormArgs(
+    return _qk_pack(
         io, NORMS[norm], B, T, Hq, Hk, d, _rows(q, "q", qs, dtype, dev), _rows(k, "k", ks, dtype, dev), rot, n_pos,
         1 if interleaved else 0, eps, q_scale, 0, q.data_ptr(), k.data_ptr(), _whole(wq, "wq", (d,), f32, dev),
         _whole(wk, "wk", (d,), f32, dev), _whole(cos, "cos", table, f32, dev), _whole(sin, "sin", table, f32, dev),
@@ -283,11 +293,11 @@ def gdn_qk_norm_fwd(q, k, wq=None, wk=None, *, norm="rms", eps=1e-6, q_scale=1.0
             return gdn_qk_norm_fwd(q, k, wq, wk, norm=norm, eps=eps, q_scale=q_scale, cos=cos, sin=sin,
                                    positions=positions, interleaved=interleaved, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q.shape)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        k_out = q.new_empty(k.shape)
     a = _qk_args(q, k, wq, wk, norm, eps, q_scale, cos, sin, positions, interleaved, q_out, k_out)
-    _done(_library().gdn_qk_norm_fwd(ctypes.byref(a), _stream()), "gdn_qk_norm_fwd")
+    _done(_library().gdn_qk_norm_fwd(a, _current_stream(q.get_device())), "gdn_qk_norm_fwd")
     return q_out, k_out
 
 
@@ -301,31 +311,30 @@ def gdn_qk_norm_bwd(q, k, wq=None, wk=None, *, dq_out, dk_out, norm="rms", eps=1
             return gdn_qk_norm_bwd(q, k, wq, wk, dq_out=dq_out, dk_out=dk_out, norm=norm, eps=eps, q_scale=q_scale,
                                    cos=cos, sin=sin, positions=positions, interleaved=interleaved, workspace=workspace)
     lib = _library()
-    args = _qk_args(q, k, wq, wk, norm, eps, q_scale, cos, sin, positions, interleaved, None, None)
-    dev, dtype = q.device, q.dtype
-    up = dq_out.dtype if dq_out.dtype == torch.float32 else dtype
+    a = _qk_args(q, k, wq, wk, norm, eps, q_scale, cos, sin, positions, interleaved, None, None)
+    dev = q.get_device()
+    up = dq_out.dtype if dq_out.dtype is torch.float32 else q.dtype
     uq, uk = _whole(dq_out, "dq_out", q.shape, up, dev), _whole(dk_out, "dk_out", k.shape, up, dev)
-    out = {"dq": torch.empty(q.shape, dtype=dtype, device=dev), "dk": torch.empty(k.shape, dtype=dtype, device=dev)}
+    out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape)}
     for name, w in (("dwq", wq), ("dwk", wk)):
         if w is not None:
-            out[name] = torch.empty(w.shape, dtype=torch.float32, device=dev)
+            out[name] = w.new_empty(w.shape)
     at = {n: t.data_ptr() for n, t in out.items()}
-    g = GdnQkNormGrads(_DTYPES[up], 0, uq, uk, at["dq"], at["dk"], at.get("dwq"), at.get("dwk"))
-    a = ctypes.byref(args)
-    ws, wp, size = _workspace(workspace, lib.gdn_qk_norm_bwd_workspace_bytes(a), "gdn_qk_norm_bwd_workspace_bytes", dev)
-    _done(lib.gdn_qk_norm_bwd(a, ctypes.byref(g), wp, size, _stream()), "gdn_qk_norm_bwd")
+    g = _qk_grads_pack(_DTYPES[up], 0, uq, uk, at["dq"], at["dk"], at.get("dwq", 0), at.get("dwk", 0))
+    ws, wp, size = _workspace(workspace, lib.gdn_qk_norm_bwd_workspace_bytes(a), "gdn_qk_norm_bwd_workspace_bytes", q)
+    _done(lib.gdn_qk_norm_bwd(a, g, wp, size, _current_stream(dev)), "gdn_qk_norm_bwd")
     return out
 
 
 # ---- gated norm ----------------------------------------------------------------------------
 
 def _gated_args(x, gate, weight, eps, activation, out):
-    dtype, dev = x.dtype, x.device
+    dtype, dev = x.dtype, x.get_device()
     io = _io(x, "x")
     B, T, H, d = shape = _heads(x, "x")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
-    return GdnGatedNormArgs(
+    return _gated_pack(
         io, ACTIVATIONS[activation], B, T, H, d, _rows(x, "x", shape, dtype, dev),
         _rows(gate, "gate", shape, dtype, dev), eps, 0, x.data_ptr(), gate.data_ptr(),
         _whole(weight, "weight", (d,), torch.float32, dev), _whole(out, "out", shape, dtype, dev))
@@ -339,9 +348,9 @@ def gdn_gated_norm_fwd(x, gate, weight=None, *, eps=1e-6, activation="silu", out
         with _on(x, stream):
             return gdn_gated_norm_fwd(x, gate, weight, eps=eps, activation=activation, out=out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     a = _gated_args(x, gate, weight, eps, activation, out)
-    _done(_library().gdn_gated_norm_fwd(ctypes.byref(a), _stream()), "gdn_gated_norm_fwd")
+    _done(_library().gdn_gated_norm_fwd(a, _current_stream(x.get_device())), "gdn_gated_norm_fwd")
     return out
 
 
@@ -352,14 +361,13 @@ def gdn_gated_norm_bwd(x, gate, weight=None, *, d_out, eps=1e-6, activation="sil
         with _on(x, stream):
             return gdn_gated_norm_bwd(x, gate, weight, d_out=d_out, eps=eps, activation=activation, workspace=workspace)
     lib = _library()
-    args = _gated_args(x, gate, weight, eps, activation, None)
-    dev, dtype = x.device, x.dtype
-    up = _whole(d_out, "d_out", x.shape, dtype, dev)
-    out = {"dx": torch.empty(x.shape, dtype=dtype, device=dev), "dgate": torch.empty(x.shape, dtype=dtype, device=dev)}
+    a = _gated_args(x, gate, weight, eps, activation, None)
+    dev = x.get_device()
+    up = _whole(d_out, "d_out", x.shape, x.dtype, dev)
+    out = {"dx": x.new_empty(x.shape), "dgate": x.new_empty(x.shape)}
     if weight is not None:
-        out["dw"] = torch.empty(weight.shape, dtype=torch.float32, device=dev)
-    g = GdnGatedNormGrads(up, *(t.data_ptr() for t in out.values()))
-    a = ctypes.byref(args)
-    ws, at, size = _workspace(workspace, lib.gdn_gated_norm_bwd_workspace_bytes(a), "gdn_gated_norm_bwd_workspace_bytes", dev)
-    _done(lib.gdn_gated_norm_bwd(a, ctypes.byref(g), at, size, _stream()), "gdn_gated_norm_bwd")
+        out["dw"] = weight.new_empty(weight.shape)
+    g = _gated_grads_pack(up, out["dx"].data_ptr(), out["dgate"].data_ptr(), 0 if weight is None else out["dw"].data_ptr())
+    ws, at, size = _workspace(workspace, lib.gdn_gated_norm_bwd_workspace_bytes(a), "gdn_gated_norm_bwd_workspace_bytes", x)
+    _done(lib.gdn_gated_norm_bwd(a, g, at, size, _current_stream(dev)), "gdn_gated_norm_bwd")
     return out

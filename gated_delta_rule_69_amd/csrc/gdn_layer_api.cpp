@@ -39,6 +39,7 @@ int linear_shapes(const gdn_linear_args* a, LinearProblem* p) {
   int st = sizes(a->B, a->T, a->H);
   if (st != GDN_OK) return st;
   if (a->Hk < 1 || a->Hk > a->H || a->H % a->Hk != 0) return GDN_ERR_ARG;
+  if (a->T > (int64_t(1) << 31) - (1 << 16)) return GDN_ERR_UNSUPPORTED;  // positions are ints, a chunk's end included
   if (!head_dim_ok(a->dk) || !head_dim_ok(a->dv)) return GDN_ERR_UNSUPPORTED;
   *p = LinearProblem{};
   if ((st = stride(a->q_stride, a->Hk, a->dk, a->dtype, &p->ldq)) != GDN_OK) return st;

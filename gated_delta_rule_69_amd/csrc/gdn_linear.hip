@@ -130,14 +130,15 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int 
   float* slot = s.states + bh * s.nseg * per_state + at;
   float x[4];
   load4(slot + per_state, x);
-  // eight segments' loads at a time: the chain itself is one multiplication and addition each
-  for (int seg = 2; seg < s.nseg; seg += 8) {
-    float y[8][4];
+  // sixteen segments' loads at a time: the chain itself is one multiplication and addition each
+  constexpr int N = 16;
+  for (int seg = 2; seg < s.nseg; seg += N) {
+    float y[N][4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < N; ++k)
       if (seg + k < s.nseg) load4(slot + int64_t(seg + k) * per_state, y[k]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < N; ++k) {
       if (seg + k >= s.nseg) break;
       const int64_t left = n - (seg + k - 1) * s.seg;
       const float w = expf(lg * float(left < 0 ? 0 : left > s.seg ? s.seg : left));

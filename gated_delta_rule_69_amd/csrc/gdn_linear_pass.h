@@ -103,15 +103,19 @@ __device__ __forceinline__ void split_parts(const float* x, vec<__bf16, N>* part
 
 __device__ __forceinline__ float4v mma(bhalf8 a, bhalf8 b, float4v acc) { return mma_pair_bf16(a, b, acc); }
 
-// Sum of the products of parts, the smallest first; those of order above MOST are left out.
-template <int PA, int PB, int MOST>
-__device__ __forceinline__ float4v mma_parts(const bhalf8* a, const bhalf8* b, float4v acc) {
+// acc[t] += the products of the parts of a[t] and b[t], the smallest first; those of order
+// above MOST are left out. Each product goes round the N tiles, so that neighbouring
+// instructions do not wait for one another.
+template <int N, int PA, int PB, int MOST, typename A, typename B>
+__device__ __forceinline__ void mma_parts(A a, B b, float4v* acc) {
 #pragma unroll
   for (int order = MOST; order >= 0; --order)
 #pragma unroll
     for (int p = 0; p < PA; ++p)
-      if (order - p >= 0 && order - p < PB) acc = mma(a[p], b[order - p], acc);
-  return acc;
+      if (order - p >= 0 && order - p < PB) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) acc[t] = mma(a(t, p), b(t, order - p), acc[t]);
+      }
 }
 
 typedef __attribute__((address_space(3))) bhalf4 lds_bhalf4;
@@ -267,29 +271,31 @@ template <typename E, int DA, int DC> struct Segment {
   static constexpr int C = PassShape<E>::kChunk, NT = 64 * pass_waves(DC), KT = DA / 16;
   const LinearPass& s;
   int wave, i, g, h, seg;
-  int64_t b, bh, n, begin, last, end;  // end: the segment's last real position + 1; last: of any
+  int n, begin, last, end;  // end: the segment's last real position + 1; last: of any
+  int64_t b, bh;
   float lg;                            // log2 of the decay
 
   __device__ __forceinline__ Segment(const LinearPass& s_, int segs) : s(s_) {
     wave = threadIdx.x / 64;
     const int lane = threadIdx.x % 64;
     i = lane % 16, g = lane / 16;
-    h = int(blockIdx.x) % s.H;
-    const int64_t bs = int64_t(blockIdx.x) / s.H;
-    seg = int(bs % segs);
-    b = bs / segs;
+    const unsigned bs = blockIdx.x / unsigned(s.H);
+    h = int(blockIdx.x - bs * unsigned(s.H));
+    const unsigned bq = bs / unsigned(segs);
+    seg = int(bs - bq * unsigned(segs));
+    b = bq;
     bh = b * s.H + h;
-    n = length_of(s.seq_lens, b, s.T);
+    n = __builtin_amdgcn_readfirstlane(int(length_of(s.seq_lens, b, s.T)));
     lg = head_log_decay(s.log_decay, h) * 1.44269504088896341f;
-    begin = seg * s.seg;
-    last = begin + s.seg < s.T ? begin + s.seg : s.T;
+    begin = int(seg * s.seg);
+    last = int(begin + s.seg < s.T ? begin + s.seg : s.T);
     end = last < n ? last : n;
   }
-  __device__ __forceinline__ float power(int64_t m) const { return __builtin_amdgcn_exp2f(lg * float(m)); }
-  __device__ __forceinline__ int size(int64_t p) const { return int(end - p < C ? end - p : C); }  // positions of the chunk at p
+  __device__ __forceinline__ float power(int m) const { return __builtin_amdgcn_exp2f(lg * float(m)); }
+  __device__ __forceinline__ int size(int p) const { return end - p < C ? end - p : C; }  // positions of the chunk at p
   // first token in memory of positions p .. p + m - 1: token p, or n - m - p backwards
-  __device__ __forceinline__ const E* rows(const void* x, int64_t ld, int group, int d, int64_t p) const {
-    return static_cast<const E*>(x) + (b * s.T + (s.back ? n - size(p) - p : p)) * ld + int64_t(h / group) * d;
+  __device__ __forceinline__ const E* rows(const void* x, int64_t ld, int group, int d, int p) const {
+    return static_cast<const E*>(x) + (b * s.T + int64_t(s.back ? n - size(p) - p : p)) * ld + int64_t(h / group) * d;
   }
   // a lane's first channel in state tile kt (four rows), and its column
   __device__ __forceinline__ int row_channel(int kt) const { return KT == 1 ? 4 * g : 32 * (kt / 2) + 8 * g + 4 * (kt % 2); }
@@ -336,19 +342,20 @@ __device__ __forceinline__ void weighted(const T& tile, const float* weight, int
   for (int e = 0; e < 8; ++e) x[e] *= weight[32 * kb + 8 * g + e];
 }
 
-// X += b^T (weighted c) of a k-block of positions, c in W parts.
-template <typename E, int DA, int W, typename T>
-__device__ __forceinline__ void add_outer(float4v (&X)[DA / 16], const T& tile, int kb, int at, const float* x) {
-  constexpr int P = PassShape<E>::kParts, KT = DA / 16;
+// X += b^T (weighted c) of a k-block of positions: parts FIRST .. W-1 of c.
+template <typename E, int DA, int FIRST, int W, typename T>
+__device__ __forceinline__ void add_outer(float4v* X, const T& tile, int kb, int at, const float* x) {
+  constexpr int P = PassShape<E>::kParts, KT = DA / 16, N = KT < 2 ? KT : 2;
   bhalf8 wv[W];
   split_parts<W, 8>(x, wv);
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    bhalf8 bv[P];
+  for (int kt = 0; kt < KT; kt += N) {
+    bhalf8 bv[N][P];
 #pragma unroll
-    for (int q = 0; q < P; ++q)
-      bv[q] = tile.columns(q, kb, at, kt / 2, kt % 2);
-    X[kt] = mma_parts<P, W, W - 1>(bv, wv, X[kt]);
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int q = 0; q < P; ++q) bv[t][q] = tile.columns(q, kb, at, (kt + t) / 2, (kt + t) % 2);
+    mma_parts<N, P, W - FIRST, W - 1 - FIRST>([&](int t, int p) { return bv[t][p]; }, [&](int, int p) { return wv[FIRST + p]; }, X + kt);
   }
 }
 
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   const Segment<E, DA, DC> me(s, s.nseg - 1);
   float4v X[DA / 16];
   float* slots = s.states + me.bh * s.nseg * (DA * DC);
-  const int64_t begin = me.begin, end = me.end;
+  const int begin = me.begin, end = me.end;
   const bool first = me.seg == 0 && s.x0 != nullptr;
   me.load_state(X, first ? s.x0 + me.bh * (DA * DC) : nullptr, s.x0_sa, s.x0_sc);
   // x0 may be overwritten by the last segment's state while the first segment's outputs are
@@ -383,21 +390,21 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 
   std::conditional_t<kDirect, Direct<C, DA, NT>, Staged<C, DA, NT>> rb(s.ldb, s.back);
   std::conditional_t<kDirect, Direct<C, DC, NT>, Staged<C, DC, NT>> rc(s.ldc, s.back);
-  auto fetch = [&](int64_t p, int buf) {
+  auto fetch = [&](int p, int buf) {
     const E *fb = me.rows(s.b, s.ldb, s.group_b, DA, p), *fc = me.rows(s.c, s.ldc, s.group_c, DC, p);
     if constexpr (kDirect) rb.load(sh.b[buf], fb, me.size(p)), rc.load(sh.c[buf], fc, me.size(p));
     else rb.load(fb, me.size(p)), rc.load(fc, me.size(p));
   };
   const int at_b = Tile<C, DA, P>::column_place(0, DA == 16 ? 4 : 8, me.i, me.g);
   const int at_c = Tile<C, DC, P>::column_place(16 * me.wave, 4, me.i, me.g);
-  int64_t p = end > begin ? begin + (end - 1 - begin) / C * C : begin - C;
+  int p = end > begin ? begin + (end - 1 - begin) / C * C : begin - C;
   if (p >= begin) fetch(p, 0);
   for (int buf = 0; p >= begin; p -= C, buf ^= 1) {
     const bool more = p - C >= begin && me.lg * float(end - p + s.shift) > -127.0f;
     if constexpr (kDirect) wait_loads();
     else rb.store(sh.b[0]), rc.store(sh.c[0]);
     if (threadIdx.x < C) {
-      const int64_t left = end - 1 - p - int(threadIdx.x);
+      const int left = end - 1 - p - int(threadIdx.x);
       sh.weight[buf][threadIdx.x] = left >= 0 ? me.power(left + s.shift) : 0.0f;
     }
     __syncthreads();
@@ -408,7 +415,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       bhalf8 cv[P];
       float x[8];
       weighted<E, DC>(sh.c[at], sh.weight[buf], kb, at_c, me.g, cv, x);
-      add_outer<E, DA, 3>(X, sh.b[at], kb, at_b, x);
+      add_outer<E, DA, 0, 3>(X, sh.b[at], kb, at_b, x);
     }
     if (!more) break;
     if constexpr (!kDirect) __syncthreads();
@@ -434,12 +441,13 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     Tile<C, DC, P> c;
     Scores<C, PS> scores;
     float weight[2][C];  // l^{n-1-j+shift}
+    float decay[C + 1];  // powers of l
     int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
   };
   __shared__ Shared sh;
   Segment<E, DA, DC> me(s, s.nseg);
   const int wave = me.wave;
-  const int64_t begin = me.begin, end = me.end;
+  const int begin = me.begin, end = me.end;
   float4v X[KT];
   if (s.nseg == 1)
     me.load_state(X, s.x0 == nullptr ? nullptr : s.x0 + me.bh * (DA * DC), s.x0_sa, s.x0_sc);
@@ -448,17 +456,17 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 
   std::conditional_t<kDirect, Direct<C, DA, NT>, Staged<C, DA, NT>> ra(s.lda, s.back), rb(s.ldb, s.back);
   std::conditional_t<kDirect, Direct<C, DC, NT>, Staged<C, DC, NT>> rc(s.ldc, s.back);
-  auto fetch_a = [&](int64_t p) {
+  auto fetch_a = [&](int p) {
     const E* from = me.rows(s.a, s.lda, s.group_a, DA, p);
     if constexpr (kDirect) ra.load(sh.a, from, me.size(p));
     else ra.load(from, me.size(p));
   };
-  auto fetch_b = [&](int64_t p, int buf) {
+  auto fetch_b = [&](int p, int buf) {
     const E* from = me.rows(s.b, s.ldb, s.group_b, DA, p);
     if constexpr (kDirect) rb.load(sh.b[buf], from, me.size(p));
     else rb.load(from, me.size(p));
   };
-  auto fetch_c = [&](int64_t p) {
+  auto fetch_c = [&](int p) {
     const E* from = me.rows(s.c, s.ldc, s.group_c, DC, p);
     if constexpr (kDirect) rc.load(sh.c, from, me.size(p));
     else rc.load(from, me.size(p));
@@ -481,16 +489,14 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   if (begin < end) {
     fetch_a(begin);
     fetch_b(begin, 0);
-    if constexpr (kDirect) {
-      wait_loads();
-      __syncthreads();
-    } else {
-      fetch_c(begin);
-    }
+    if constexpr (kDirect) wait_loads();
+    else fetch_c(begin);
   }
 
+  for (int at = threadIdx.x; at <= C; at += NT) sh.decay[at] = me.power(at);
+  __syncthreads();
   int buf = 0;
-  for (int64_t p = begin; p < end; p += C, buf ^= 1) {
+  for (int p = begin; p < end; p += C, buf ^= 1) {
     const int m = me.size(p);
     const bool more = p + C < end;
     asm volatile("" : "+v"(me.lg), "+v"(me.i), "+v"(me.g), "+v"(at_row), "+v"(at_b), "+v"(at_c), "+v"(at_first), "+v"(at_second), "+v"(at_out));
@@ -527,12 +533,12 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
           bhalf8 av[P], bv[P];
 #pragma unroll
           for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, at_row), bv[q] = tb.row(q, jt, kb, at_row);
-          d = mma_parts<P, P, P - 1>(bv, av, d);
+          mma_parts<1, P, P, P - 1>([&](int, int p) { return bv[p]; }, [&](int, int p) { return av[p]; }, &d);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int ahead = 16 * r + i - (16 * jt + 4 * g + e);
-          x[e] = ahead >= 0 ? d[e] * me.power(ahead) : 0.0f;
+          x[e] = ahead >= 0 ? d[e] * sh.decay[ahead] : 0.0f;
         }
       } else {
         r = 2 * (t - kLower), jt = r + 1;
@@ -556,16 +562,15 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       }
       bhalf8 xv[PS];
       split_parts<PS, 8>(x, xv);
+      bhalf8 av[RT][P];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        bhalf8 av[P];
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int q = 0; q < P; ++q) av[q] = sh.a.row(q, r, kb, at_row);
-        acc[r] = mma_parts<PS, P, PS - 1>(xv, av, acc[r]);
-      }
+        for (int q = 0; q < P; ++q) av[r][q] = sh.a.row(q, r, kb, at_row);
+      mma_parts<RT, PS, P, PS - 1>([&](int, int p) { return xv[p]; }, [&](int t, int p) { return av[t][p]; }, acc);
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] *= me.power(16 * r + i + 1 - s.shift);
+    for (int r = 0; r < RT; ++r) acc[r] *= sh.decay[16 * r + i + 1 - s.shift];
     if constexpr (kDirect) wait_loads();
     __syncthreads();
     if constexpr (kDirect) {
@@ -596,21 +601,31 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
           for (int q = 0; q < P; ++q) cv[q][e] = __bf16(0.0f);
         }
       }
+      // rows before the block see none of it
+      auto own_rows = [&](auto from) {
+        constexpr int R = decltype(from)::value;
+        bhalf8 sv[RT - R][PS];
 #pragma unroll
-      for (int r = 2 * kb; r < RT; ++r) {
-        bhalf8 sv[PS];
+        for (int r = R; r < RT; ++r)
 #pragma unroll
-        for (int q = 0; q < PS; ++q) sv[q] = sh.scores.row(q, r, kb, at_first, at_second);
-        acc[r] = mma_parts<P, PS, PS - 1>(cv, sv, acc[r]);
+          for (int q = 0; q < PS; ++q) sv[r - R][q] = sh.scores.row(q, r, kb, at_first, at_second);
+        mma_parts<RT - R, P, PS, PS - 1>([&](int, int p) { return cv[p]; }, [&](int t, int p) { return sv[t][p]; }, acc + R);
+      };
+      if (kb == 0) own_rows(std::integral_constant<int, 0>{});
+      else own_rows(std::integral_constant<int, PB == 2 ? 2 : 0>{});
+      add_outer<E, DA, 0, S::kHalf ? 2 : 3>(X, tb, kb, at_b, x);
+      if constexpr (S::kHalf) {
+        if (exact) {  // the third part, from a second look at c: it holds no registers meanwhile
+          weighted<E, DC>(sh.c, sh.weight[buf], kb, at_c, g, cv, x);
+          add_outer<E, DA, 2, 3>(X, tb, kb, at_b, x);
+        }
       }
-      if (!S::kHalf || exact) add_outer<E, DA, 3>(X, tb, kb, at_b, x);
-      else add_outer<E, DA, 2>(X, tb, kb, at_b, x);
     }
 
     if constexpr (kDirect) wait_loads();
     // rows 16 r + i; stores behind the chunk's end fall out of the range
     const uint32_t top = uint32_t(m - 1) * out_step;
-    O* to = static_cast<O*>(s.out) + ((me.b * s.T + (s.back ? me.n - p - m : p)) * s.H + me.h) * DC;
+    O* to = static_cast<O*>(s.out) + ((me.b * s.T + int64_t(s.back ? me.n - p - m : p)) * s.H + me.h) * DC;
     const auto range = __builtin_amdgcn_make_buffer_rsrc(to, 0, top + DC * uint32_t(sizeof(O)), 0x00020000);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -631,9 +646,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   }
 
   if (s.zero_tail) {
-    const int64_t first = begin > me.n ? begin : me.n;
+    const int first = begin > me.n ? begin : me.n;
     constexpr int V = DC / 4;
-    for (int64_t at = threadIdx.x; at < (me.last - first) * V; at += NT) {
+    for (int64_t at = threadIdx.x; at < int64_t(me.last - first) * V; at += NT) {
       const float zero[4] = {};
       store4(static_cast<O*>(s.out) + ((me.b * s.T + first + at / V) * s.H + me.h) * DC + at % V * 4, zero);
     }

@@ -169,15 +169,15 @@ def test_binding_refuses_host_tensors():
 def test_binding_reads_strides_and_refuses_what_it_cannot():
     """The view checks need no GPU: token strides of a wider tensor pass, others are refused."""
     from gated_delta_rule_69_amd._layer import _rows
-    cpu = torch.device("cpu")
+    cpu = -1  # the device number of host tensors
     wide = torch.zeros(2, 6, 96)
     view = wide[..., 32:64].unflatten(-1, (2, 16))
     rows = lambda t: _rows(t, "x", tuple(t.shape), torch.float32, cpu)  # noqa: E731
     assert rows(view) == 96
-    assert rows(view.contiguous()) == 32
+    assert rows(view.contiguous()) == 0                          # contiguous
     assert rows(wide[:1, :4, 32:64].unflatten(-1, (2, 16))) == 96
     assert rows(view[:, :1]) == 6 * 96                           # one token: the stride between sequences
-    assert rows(view[:1, :1]) == 32
+    assert rows(view[:1, :1]) == 0
     assert rows(view[:, :0]) == 0
     assert rows(view[:, ::2]) == 192                             # every second token
     same = wide[:, :1, :32].unflatten(-1, (2, 16)).expand(2, 6, 2, 16)
