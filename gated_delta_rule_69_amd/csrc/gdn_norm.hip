@@ -114,21 +114,44 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkNorm a) {
   const int64_t end = begin + a.rows_per_block < a.rows ? begin + a.rows_per_block : a.rows;
   int64_t row = begin + threadIdx.x / L;
   RowWalk at(row, a.hq + a.hk, R);
-  for (; row < end; row += R, at.next()) {
+  // A row's loads run one step ahead of its use.
+  struct Loaded {
+    vec<E, 4> x[2];
+    vec<G, 4> dy[2];
+    float cs[4], sn[4];
+    bool in;
+  };
+  auto fetch = [&](Loaded& f) {
     const bool key = at.hh >= a.hq;
     const unsigned h = key ? at.hh - a.hq : at.hh;
-    const E* x_row = static_cast<const E*>(key ? a.k : a.q) + at.token * (key ? a.ldk : a.ldq) + int64_t(h) * D;
-    const int64_t out_row = (at.token * (key ? a.hk : a.hq) + h) * D;
-    float x[8], y[8], cs[4], sn[4];
-    load4(x_row + ch.c0, x);
-    load4(x_row + ch.c1, x + 4);
+    const E* x = static_cast<const E*>(key ? a.k : a.q) + at.token * (key ? a.ldk : a.ldq) + int64_t(h) * D;
+    f.x[0] = *reinterpret_cast<const vec<E, 4>*>(x + ch.c0);
+    f.x[1] = *reinterpret_cast<const vec<E, 4>*>(x + ch.c1);
     if constexpr (BWD) {
-      const G* dy = static_cast<const G*>(key ? a.dk_out : a.dq_out) + out_row;
-      load4(dy + ch.c0, y);
-      load4(dy + ch.c1, y + 4);
+      const G* dy = static_cast<const G*>(key ? a.dk_out : a.dq_out) + (at.token * (key ? a.hk : a.hq) + h) * D;
+      f.dy[0] = *reinterpret_cast<const vec<G, 4>*>(dy + ch.c0);
+      f.dy[1] = *reinterpret_cast<const vec<G, 4>*>(dy + ch.c1);
     }
-    bool in = true;
-    if (ch.turned) in = angles(a, at.token, ch, cs, sn);
+    f.in = !ch.turned || angles(a, at.token, ch, f.cs, f.sn);
+  };
+  Loaded next;
+  if (row < end) fetch(next);
+  while (row < end) {
+    const Loaded now = next;
+    const bool key = at.hh >= a.hq;
+    const unsigned h = key ? at.hh - a.hq : at.hh;
+    const int64_t out_row = (at.token * (key ? a.hk : a.hq) + h) * D;
+    row += R;
+    at.next();
+    if (row < end) fetch(next);
+    float x[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = float(now.x[i / 4][i % 4]);
+      if constexpr (BWD) y[i] = float(now.dy[i / 4][i % 4]);
+    }
+    const float *cs = now.cs, *sn = now.sn;
+    const bool in = now.in;
     const float scale = key ? 1.0f : a.q_scale;
     float sq = 0.0f;
 #pragma unroll
@@ -213,15 +236,27 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
   const int64_t end = begin + a.rows_per_block < a.rows ? begin + a.rows_per_block : a.rows;
   int64_t row = begin + threadIdx.x / L;
   RowWalk at(row, a.heads, R);
-  for (; row < end; row += R, at.next()) {
-    const E* xr = static_cast<const E*>(a.x) + at.token * a.ldx + int64_t(at.hh) * D + c;
-    const E* gr = static_cast<const E*>(a.gate) + at.token * a.ldg + int64_t(at.hh) * D + c;
+  struct Loaded {  // one step ahead of its use
+    vec<E, 8> x, z, dy;
+  };
+  auto fetch = [&](Loaded& f) {
+    f.x = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.x) + at.token * a.ldx + int64_t(at.hh) * D + c);
+    f.z = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.gate) + at.token * a.ldg + int64_t(at.hh) * D + c);
+    if constexpr (BWD) f.dy = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.dy) + row * D + c);
+  };
+  Loaded next;
+  if (row < end) fetch(next);
+  while (row < end) {
+    const Loaded now = next;
+    const int64_t here = row;
+    row += R;
+    at.next();
+    if (row < end) fetch(next);
     float x[8], z[8], dy[8];
-    load4(xr, x), load4(xr + 4, x + 4);
-    load4(gr, z), load4(gr + 4, z + 4);
-    if constexpr (BWD) {
-      const E* dr = static_cast<const E*>(a.dy) + row * D + c;
-      load4(dr, dy), load4(dr + 4, dy + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = float(now.x[i]), z[i] = float(now.z[i]);
+      if constexpr (BWD) dy[i] = float(now.dy[i]);
     }
     float sq = 0.0f;
 #pragma unroll
@@ -234,7 +269,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
         const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));  // 1 + e^-z >= 1: within 1 ulp
         x[i] = x[i] * r * w[i] * (SILU ? z[i] * s : s);
       }
-      E* out = static_cast<E*>(a.y) + row * D + c;
+      E* out = static_cast<E*>(a.y) + here * D + c;
       store4(out, x), store4(out + 4, x + 4);
     } else {
       float dot = 0.0f;
@@ -253,8 +288,8 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
       dot = row_sum<L>(dot) * (1.0f / D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = r * (dy[i] - x[i] * dot);
-      E* dx = static_cast<E*>(a.dx) + row * D + c;
-      E* dg = static_cast<E*>(a.dgate) + row * D + c;
+      E* dx = static_cast<E*>(a.dx) + here * D + c;
+      E* dg = static_cast<E*>(a.dgate) + here * D + c;
       store4(dx, x), store4(dx + 4, x + 4);
       store4(dg, z), store4(dg + 4, z + 4);
     }
