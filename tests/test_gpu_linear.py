@@ -10,6 +10,8 @@ pytestmark = pytest.mark.gpu
 # B, T, H, Hk, dk, dv
 SIZES = [
     (1, 1, 1, 1, 16, 16),
+    (3, 8, 2, 1, 128, 64),
+    (2, 9, 3, 3, 64, 16),
     (2, 15, 3, 3, 16, 32),
     (1, 64, 4, 2, 64, 64),
     (3, 65, 2, 1, 32, 128),
@@ -286,3 +288,27 @@ def test_another_stream_and_a_captured_graph():
         want_step = gdn.gdn_linear_recurrent_step(*step, on["g"], state=eager)
         assert torch.equal(out, want) and torch.equal(S, S_want)
         assert torch.equal(so, want_step) and torch.equal(state, eager)
+
+
+def test_rows_far_apart():
+    """Views with 256 KiB from token to token over more than 4 GiB equal contiguous rows."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    T, wide = 17000, 131072
+    gen = torch.Generator(device=dev()).manual_seed(40)
+    x = torch.empty((1, T, wide), dtype=torch.bfloat16, device=dev())
+    assert x.numel() * 2 > 1 << 32
+    views = []
+    for n, at in enumerate((0, 50000, wide - 64)):
+        x[..., at:at + 64] = torch.randn((1, T, 64), generator=gen, device=dev()).to(x)
+        views.append(x[..., at:at + 64].unflatten(-1, (2, 32)))
+    near = [v.contiguous() for v in views]
+    g = slopes(2).to(dev())
+    for got, want in zip(gdn.gdn_linear_chunk_fwd(*views, g), gdn.gdn_linear_chunk_fwd(*near, g)):
+        assert torch.equal(got, want)
+    do = near[0].flip(1).contiguous()
+    got, want = (gdn.gdn_linear_chunk_bwd(*t, g, d_o=do) for t in (views, near))
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    for got, want in zip(gdn.gdn_qk_norm_fwd(*views[:2]), gdn.gdn_qk_norm_fwd(*near[:2])):
+        assert torch.equal(got, want)
+    assert torch.equal(gdn.gdn_gated_norm_fwd(*views[1:]), gdn.gdn_gated_norm_fwd(*near[1:]))
