@@ -269,7 +269,9 @@ int gdn_recurrent_bwd(const gdn_args* args, const void* d_o, const float* d_s_fi
  * heads; the heads of a token are contiguous, and a sequence starts T strides after the
  * one before. o is contiguous and must not overlap an input.
  * Ownership, asynchrony, determinism and errors as above; the current device must be
- * the stream's. A NaN or Inf in token t reaches o from token t on, never an earlier row. */
+ * the stream's. A NaN or Inf in token t makes o NaN or Inf from token t on, until its decay
+ * leaves nothing of it (weights under 2^-127 are 0), and never reaches an earlier row; of
+ * float32 inputs, magnitudes above 3.3e38 count as Inf. */
 typedef struct gdn_linear_args {
   int32_t dtype;          /* enum gdn_dtype: q, k, v and o                    */
   int32_t reserved;       /* must be 0                                        */
@@ -293,7 +295,7 @@ size_t gdn_linear_workspace_bytes(const gdn_linear_args* args);
  * sequence is cut into segments that run in parallel: one pass adds up each segment's own
  * k v^T, a second carries the state over the segments, and a third computes the outputs
  * chunk by chunk from the state before each segment (one launch where a sequence is one
- * segment). ws must hold gdn_linear_workspace_bytes(args) bytes, 256-byte aligned. */
+ * segment; up to eight tokens go one by one). ws must hold gdn_linear_workspace_bytes(args) bytes, 256-byte aligned. */
 int gdn_linear_chunk_fwd(const gdn_linear_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* The recurrence token by token on state_inout ([B, H, dk, dv] float32, updated in
@@ -303,8 +305,8 @@ int gdn_linear_recurrent_step(const gdn_linear_args* args, float* state_inout, v
 
 /* Gradient outputs of gdn_linear_chunk_bwd, contiguous: dq, dk [B, T, Hk, dk] and dv
  * [B, T, H, dv] in args->dtype (dq and dk summed over the value heads of a key head);
- * ds0 [B, H, dk, dv] float32, NULL means not written. Rows behind a sequence's length
- * are written as zero. */
+ * ds0 [B, H, dk, dv] float32, NULL means not written; none may overlap an input or
+ * d_s_final. Rows behind a sequence's length are written as zero. */
 typedef struct gdn_linear_grads {
   void* dq;
   void* dk;
