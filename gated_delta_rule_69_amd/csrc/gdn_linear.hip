@@ -134,6 +134,8 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int 
   if (at >= per_state) return;
   const int64_t n = length_of(s.seq_lens, bh / s.H, s.T);
   const float lg = head_log_decay(s.log_decay, int(bh % s.H));
+  // a segment that leaves nothing of the one before: every state is its segment's own already
+  if (n > (s.nseg - 1) * s.seg && expf(lg * float(s.seg)) == 0.0f) return;
   float* slot = s.states + bh * s.nseg * per_state + at;
   float x[4];
   load4(slot + per_state, x);
