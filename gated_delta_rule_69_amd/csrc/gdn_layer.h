@@ -44,7 +44,9 @@ struct GatedNormProblem {
   int64_t tokens;
 };
 
-// Partial sums of weight gradients: at most this many blocks, one row of floats each.
+// Partial sums of weight gradients: at most this many blocks, one row of floats each (four
+// blocks a CU; q / k norm gradients at 8,192 x 24 rows of 128: 512, 768, 2048 blocks 46, 40,
+// 40 us against 38).
 constexpr int64_t kNormPartials = 1024;
 
 // Launchers (the .hip translation units); each returns a hipError_t as int.

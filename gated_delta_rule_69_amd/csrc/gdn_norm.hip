@@ -5,7 +5,12 @@
 // bounds them. A row lies in d / 8 neighbouring lanes, eight channels a lane, and its sum
 // of squares is a few DPP adds; nothing goes through LDS. A block walks the rows of a
 // range of its own and keeps (token, head) of its next row by addition, so there is no
-// division in the loop.
+// division in the loop, and a row's loads run one step ahead of its use.
+//
+// bf16, d 128: queries and keys of 65,536 tokens, 16 heads each, 217 to 227 us (1.11 GB,
+// 4.9 to 5.1 TB/s); the gated norm of 65,536 tokens x 16 heads 141 to 144 us (805 MB, 5.6
+// TB/s, a large copy's rate). Backward at 8,192 tokens: 33 us (153 MB) and 28 us (168 MB),
+// and 4 us for the weights' sums in a second kernel, whose order is fixed.
 #include <algorithm>
 
 #include "gdn_layer.h"

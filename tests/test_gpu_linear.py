@@ -84,12 +84,13 @@ def test_gradients_against_the_recurrence(case, states, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_gradients_of_a_padded_batch(dt):
-    """Rows behind a length get zero gradients, whatever d_o holds there."""
+@pytest.mark.parametrize("T,lens", [(150, [150, 0, 64, 97, -1]), (900, [900, 0, 256, 701, 31])])
+def test_gradients_of_a_padded_batch(T, lens, dt):
+    """Rows behind a length get zero gradients, whatever d_o holds there; one and several
+    segments, some of them empty."""
     import gated_delta_rule_69_amd as gdn
     from layer_util import check, dev, f64
-    host, on = make((5, 150, 4, 2, 64, 32), dt, 42)
-    lens = [150, 0, 64, 97, -1]
+    host, on = make((5, T, 4, 2, 64, 32), dt, 42)
     for t in (host, on):
         for b, n in enumerate(lens):
             t["do"][b, max(n, 0):] = float("nan")
@@ -102,7 +103,7 @@ def test_gradients_of_a_padded_batch(dt):
         if name != "ds0":
             for b, n in enumerate(lens):
                 assert (got[name][b, max(n, 0):] == 0).all(), name
-    assert torch.equal(got["ds0"][1], on["ds"][1]) and torch.equal(got["ds0"][4], on["ds"][4])
+    assert all(torch.equal(got["ds0"][b], on["ds"][b]) for b, n in enumerate(lens) if n <= 0)
 
 
 def test_gradients_at_extreme_decays_and_of_no_tokens():
@@ -138,23 +139,24 @@ def test_long_sequence_of_many_segments():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_padded_batch_leaves_what_lies_behind(dt):
+@pytest.mark.parametrize("T,lens", [(200, [200, 0, 64, 131, -5, 1000]),   # out of range: taken as 0 and as T
+                                    (900, [900, 0, 256, 701, 31, 512])])
+def test_padded_batch_leaves_what_lies_behind(T, lens, dt):
     import gated_delta_rule_69_amd as gdn
     from layer_util import check, dev, f64
-    host, on = make((6, 200, 4, 2, 64, 64), dt, 32)
-    lens = [200, 0, 64, 131, -5, 1000]          # out of range: taken as 0 and as T
+    host, on = make((6, T, 4, 2, 64, 64), dt, 32)
     ld = torch.tensor(lens, dtype=torch.int32, device=dev())
     keep = torch.full_like(on["v"], 3.0)
     o_ref, S_ref = ref(host, s0=f64(host["s0"]), lens=lens, o=f64(keep))
     o, S = gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], seq_lens=ld, o=keep.clone())
     check(o, o_ref, "o")
     check(S, S_ref, "s_final")
-    assert torch.equal(S[1], on["s0"][1]) and torch.equal(S[4], on["s0"][4])
+    assert all(torch.equal(S[b], on["s0"][b]) for b, n in enumerate(lens) if n <= 0)
     state = on["s0"].clone()
     o2 = gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=state, seq_lens=ld, o=keep.clone())
     check(o2, o_ref, "o of the step")
     assert torch.equal(state[1], on["s0"][1])
-    for b, n in enumerate([200, 0, 64, 131, 0, 200]):
+    for b, n in enumerate(min(max(n, 0), T) for n in lens):
         assert (o[b, n:] == 3.0).all() and (o2[b, n:] == 3.0).all()
 
 
