@@ -275,12 +275,21 @@ template <typename E, int DA, int DC> struct Segment {
   int64_t b, bh;
   float lg;                            // log2 of the decay
 
-  __device__ __forceinline__ Segment(const LinearPass& s_, int segs) : s(s_) {
+  // Workgroups go over heads, segments and sequences, the heads first or last: last for the
+  // states, whose work goes by the head's decay, so that a CU gets heads of different ones
+  // (98 -> 90 us at the long prompt); first for the outputs, whose work goes by the sequence's
+  // length (a padded float32 batch 126 against 160 us a call).
+  __device__ __forceinline__ Segment(const LinearPass& s_, int segs, bool heads_last) : s(s_) {
     wave = threadIdx.x / 64;
     const int lane = threadIdx.x % 64;
     i = lane % 16, g = lane / 16;
-    const unsigned bs = blockIdx.x / unsigned(s.H);
-    h = int(blockIdx.x - bs * unsigned(s.H));
+    const unsigned per = heads_last ? gridDim.x / unsigned(s.H) : unsigned(s.H);
+    unsigned bs = blockIdx.x / per;
+    h = int(blockIdx.x - bs * per);
+    if (heads_last) {
+      const unsigned rest = unsigned(h);
+      h = int(bs), bs = rest;
+    }
     const unsigned bq = bs / unsigned(segs);
     seg = int(bs - bq * unsigned(segs));
     b = bq;
@@ -364,7 +373,7 @@ __device__ __forceinline__ void add_outer(float4v* X, const T& tile, int kb, int
 // nothing is scaled on the way, the positions whose weight is under 2^-127 (0 in float32)
 // are never read, and what the outputs' kernel reads first was read here last.
 //
-// Barriers and instructions bound it: at B2 T32768 H16 d128 bf16 98 us, 80 with its loads left
+// Barriers and instructions bound it: at B2 T32768 H16 d128 bf16 90 us, 80 with its loads left
 // out and 116 with its arithmetic left out before it passed over what counts nothing (332 of
 // 503 MB are read). Float32 B8 T2047 H32 d64, padded: 39 us.
 template <typename E, int DA, int DC>
@@ -379,7 +388,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     float weight[2][C];
   };
   __shared__ Shared sh;
-  const Segment<E, DA, DC> me(s, s.nseg - 1);
+  const Segment<E, DA, DC> me(s, s.nseg - 1, true);
   float4v X[DA / 16];
   float* slots = s.states + me.bh * s.nseg * (DA * DC);
   const int begin = me.begin, end = me.end;
@@ -455,7 +464,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
   };
   __shared__ Shared sh;
-  Segment<E, DA, DC> me(s, s.nseg);
+  Segment<E, DA, DC> me(s, s.nseg, false);
   const int wave = me.wave;
   const int begin = me.begin, end = me.end;
   float4v X[KT];
