@@ -41,6 +41,8 @@ int linear_shapes(const gdn_linear_args* a, LinearProblem* p) {
   if (a->Hk < 1 || a->Hk > a->H || a->H % a->Hk != 0) return GDN_ERR_ARG;
   if (a->T > (int64_t(1) << 31) - (1 << 16)) return GDN_ERR_UNSUPPORTED;  // positions are ints, a chunk's end included
   if (!head_dim_ok(a->dk) || !head_dim_ok(a->dv)) return GDN_ERR_UNSUPPORTED;
+  // a launch has fewer than 2^32 threads: four for each of a head's channels
+  if (a->B * a->H * (a->dk > a->dv ? a->dk : a->dv) >= int64_t(1) << 30) return GDN_ERR_UNSUPPORTED;
   *p = LinearProblem{};
   if ((st = stride(a->q_stride, a->Hk, a->dk, a->dtype, &p->ldq)) != GDN_OK) return st;
   if ((st = stride(a->k_stride, a->Hk, a->dk, a->dtype, &p->ldk)) != GDN_OK) return st;

@@ -79,6 +79,19 @@ def test_linear_workspace_and_state_checks(lib):
     assert lib.gdn_linear_recurrent_step(linear(**none), FAKE, None) == 0
 
 
+@pytest.mark.parametrize("shape", [dict(dk=128, dv=16), dict(dk=16, dv=128), dict(dk=128, dv=128)])
+def test_linear_refuses_more_threads_than_a_launch_has(lib, shape):
+    # 2^23 heads of 128 channels would be 2^32 threads; one sequence less is accepted
+    a = linear(B=1 << 17, H=64, Hk=64, T=9, **shape)
+    grads = (ctypes.c_void_p * 4)(FAKE, FAKE, FAKE, FAKE)
+    assert lib.gdn_linear_workspace_bytes(a) == 0 and lib.gdn_linear_bwd_workspace_bytes(a) == 0
+    assert lib.gdn_linear_chunk_fwd(a, FAKE, BIG, None) == -2
+    assert lib.gdn_linear_recurrent_step(a, FAKE, None) == -2
+    assert lib.gdn_linear_chunk_bwd(a, FAKE, None, grads, FAKE, BIG, None) == -2
+    a = linear(B=(1 << 17) - 1, H=64, Hk=64, T=9, **shape)
+    assert lib.gdn_linear_workspace_bytes(a) > 0 and lib.gdn_linear_bwd_workspace_bytes(a) > 0
+
+
 def test_linear_backward_checks(lib):
     from gated_delta_rule_69_amd._layer import GdnLinearGrads
     full = dict(dq=FAKE, dk=FAKE, dv=FAKE, ds0=FAKE)
