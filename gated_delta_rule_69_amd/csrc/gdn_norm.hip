@@ -340,10 +340,11 @@ int64_t split_rows(int64_t rows, int64_t per_step, int64_t most, int64_t* per_bl
   return (steps + each - 1) / each;
 }
 
-// Blocks of a forward launch: each takes at least four steps where there are enough.
+// Blocks of a forward launch: each takes at least four steps where there are enough, and a
+// launch has fewer than 2^32 threads.
 int64_t forward_blocks(int64_t rows, int64_t per_step) {
   const int64_t steps = (rows + per_step - 1) / per_step;
-  return steps < 4096 ? std::max<int64_t>(steps, 1) : std::min<int64_t>((steps + 3) / 4, int64_t(1) << 30);
+  return steps < 4096 ? std::max<int64_t>(steps, 1) : std::min<int64_t>((steps + 3) / 4, int64_t(1) << 23);
 }
 
 template <typename F>
