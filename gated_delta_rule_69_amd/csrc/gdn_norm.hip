@@ -229,6 +229,14 @@ struct GatedNorm {
   float* partial;  // [blocks][d]
 };
 
+// 1 / (1 + e^-z), the reciprocal (of at least 1) within 1 ulp. __expf rounds z log2 e first,
+// which puts it off by |z| 2^-24: nothing for a gate of bf16, 30 steps for a float32 one at
+// -60, which takes expf.
+template <typename E>
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + (sizeof(E) == 2 ? __expf(-z) : expf(-z)));
+}
+
 template <typename E, int D, bool SILU, bool BWD>
 __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
   constexpr int L = D / 8;
@@ -271,7 +279,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
     if constexpr (!BWD) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));  // 1 + e^-z >= 1: within 1 ulp
+        const float s = sigmoid<E>(z[i]);
         x[i] = x[i] * r * w[i] * (SILU ? z[i] * s : s);
       }
       E* out = static_cast<E*>(a.y) + here * D + c;
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));  // 1 + e^-z >= 1: within 1 ulp
+        const float s = sigmoid<E>(z[i]);
         const float act = SILU ? z[i] * s : s;
         const float slope = SILU ? s * (1.0f + z[i] * (1.0f - s)) : s * (1.0f - s);
         x[i] *= r;

@@ -173,6 +173,20 @@ def test_gated_norm_extremes_in_place_and_no_weight():
     assert sorted(g) == ["dgate", "dx"] and all(torch.isfinite(t).all() for t in g.values())
 
 
+@pytest.mark.parametrize("activation", ["silu", "sigmoid"])
+def test_gated_norm_float32_gate_far_out(activation):
+    """Every output to a few float32 steps, nearly closed gates too: rows of +-1 have r = 1, so
+    y is +-act(z). e^-z and the reciprocal are within a step of 2^-23 each, 1 + e^-z, z times
+    the sigmoid and the three products within half of one, r within a step: 5.5 steps."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev, f64
+    z = torch.linspace(-80, 30, 8 * 128).reshape(1, 8, 1, 128)
+    x = torch.where(torch.arange(128) % 3 == 0, -1.0, 1.0).expand(z.shape).contiguous()
+    y = f64(gdn.gdn_gated_norm_fwd(x.to(dev()), z.to(dev()), eps=0.0, activation=activation))
+    want = layer.gated_norm(f64(x), f64(z), eps=0.0, activation=activation)
+    assert (abs(y - want) <= 5.5 * 2.0 ** -23 * abs(want)).all(), float((abs(y - want) / abs(want)).max() * 2 ** 23)
+
+
 def test_norms_of_no_tokens():
     import gated_delta_rule_69_amd as gdn
     from layer_util import dev
