@@ -193,3 +193,44 @@ def test_norms_in_a_captured_graph():
         again = calls()
         for w, g, a in zip(want, got, again):
             assert torch.equal(w, g) and torch.equal(w, a)
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    """Other types, shapes, strides and devices are refused before anything is launched."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    from gated_delta_rule_69_amd import GdnError
+    x = torch.zeros((2, 10, 4, 32), device=dev())
+    k, g, state = x[:, :, :2].contiguous(), torch.zeros(4, device=dev()), torch.zeros((2, 4, 32, 32), device=dev())
+    lens, w, half = torch.ones(2, dtype=torch.int32, device=dev()), torch.ones(32, device=dev()), x.half()
+    off = torch.zeros(x.numel() + 1, device=dev())[1:].view(x.shape)   # 4 bytes off a 16-byte border
+    table = torch.zeros((10, 16), device=dev())
+    linear = [("q", x), ("q", k.bfloat16()), ("k", k[:, :5]), ("k", k[0]), ("k", k.cpu()), ("v", half), ("v", x[0]),
+              ("v", off), ("v", x.transpose(1, 2)), ("log_decay", g[:2]), ("log_decay", g.double()),
+              ("log_decay", g.cpu()), ("seq_lens", lens.long()), ("seq_lens", lens[:1])]
+    chunk = [("o", x.bfloat16()), ("o", k), ("o", x.transpose(2, 3)), ("o", off), ("s0", state[:1]),
+             ("s0", state.bfloat16()), ("s_final", state.transpose(2, 3)), ("s_final", state.cpu()),
+             ("workspace", torch.empty(16, dtype=torch.uint8, device=dev()))]
+    step = [("o", k), ("o", x.cpu()), ("state", state[:1]), ("state", state.bfloat16())]
+    back = [("d_o", x.bfloat16()), ("d_o", k), ("ds_final", state[:1]), ("s0", state.double())]
+    norm = [("q", half), ("k", k[:1]), ("wq", w[:16]), ("wk", w.bfloat16()), ("cos", table[:9]), ("cos", None),
+            ("sin", table[:, :8]), ("positions", torch.zeros((2, 10), dtype=torch.int64, device=dev())),
+            ("norm", "max"), ("eps", -1.0), ("q_out", k), ("k_out", k.bfloat16()), ("q", off)]
+    gate = [("x", half), ("gate", k), ("gate", x.bfloat16()), ("weight", w[:8]), ("activation", "tanh"), ("out", k),
+            ("eps", float("nan")), ("gate", off)]
+    base = dict(q=k, k=k, v=x, log_decay=g, seq_lens=lens)
+    rope = dict(q=x, k=k, wq=w, wk=w, cos=table, sin=table)
+    gated = dict(x=x, gate=x, weight=w)
+    for fn, args, bad in ((gdn.gdn_linear_chunk_fwd, base, linear + chunk),
+                          (gdn.gdn_linear_recurrent_step, dict(base, state=state), linear + step),
+                          (gdn.gdn_linear_chunk_bwd, dict(base, d_o=x), linear + back),
+                          (gdn.gdn_qk_norm_fwd, rope, norm),
+                          (gdn.gdn_qk_norm_bwd, dict(rope, dq_out=x, dk_out=k),
+                           norm[:-4] + [("dq_out", k), ("dk_out", k.bfloat16())]),
+                          (gdn.gdn_gated_norm_fwd, gated, gate),
+                          (gdn.gdn_gated_norm_bwd, dict(gated, d_out=x), gate[:5] + [("d_out", k), ("d_out", half)])):
+        fn(**args)  # as they are they fit
+        for name, value in bad:
+            with pytest.raises((ValueError, GdnError)):
+                fn(**{**args, name: value})
+                print(fn.__name__, name, "was taken", flush=True)
