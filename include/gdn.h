@@ -268,8 +268,9 @@ int gdn_recurrent_bwd(const gdn_args* args, const void* d_o, const float* d_s_fi
  * one token to the next (0: contiguous), a multiple of 16 bytes and at least one token's
  * heads; the heads of a token are contiguous, and a sequence starts T strides after the
  * one before. o is contiguous and must not overlap an input.
- * GDN_ERR_UNSUPPORTED above B = 2^20, H = 2^16, B * T = 2^36, T = 2^31 - 2^16 or a stride
- * of 2^24, and from B * H * max(dk, dv) = 2^30 on.
+ * GDN_ERR_UNSUPPORTED above B = 2^20, H = 2^16, B * H = 2^24, B * T = 2^36, T = 2^31 - 2^16
+ * or a stride of 2^24, and from B * H * max(dk, dv) = 2^30 on (the norms below: the same
+ * without the last and with T = 2^31).
  * Ownership, asynchrony, determinism and errors as above; the current device must be
  * the stream's. A NaN or Inf in token t makes o NaN or Inf from token t on, until its decay
  * leaves nothing of it (weights under 2^-127 are 0), and never reaches an earlier row; of
