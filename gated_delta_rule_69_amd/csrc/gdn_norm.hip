@@ -93,14 +93,16 @@ __device__ __forceinline__ void ones_or(const float* w, int c, float* out) {
   }
 }
 
-// cos and sin of a lane's pairs at its token's position; false for a position outside
-// the table (the row becomes NaN).
+// cos and sin of a lane's pairs, if it has any, at its token's position; false, in every
+// lane of the row, for a position outside the table (the row becomes NaN).
 __device__ __forceinline__ bool angles(const QkNorm& a, int64_t token, const Channels& ch, float* cs, float* sn) {
   const int64_t pos = a.positions != nullptr ? int64_t(a.positions[token]) : token % a.T;
   const bool in = pos >= 0 && pos < a.n_pos;
   const int64_t at = (in ? pos : 0) * (a.rot / 2) + ch.pair;
-  load4(a.cos + at, cs);
-  load4(a.sin + at, sn);
+  if (ch.turned) {
+    load4(a.cos + at, cs);
+    load4(a.sin + at, sn);
+  }
   return in;
 }
 
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkNorm a) {
       f.dy[0] = *reinterpret_cast<const vec<G, 4>*>(dy + ch.c0);
       f.dy[1] = *reinterpret_cast<const vec<G, 4>*>(dy + ch.c1);
     }
-    f.in = !ch.turned || angles(a, at.token, ch, f.cs, f.sn);
+    f.in = a.rot == 0 || angles(a, at.token, ch, f.cs, f.sn);
   };
   Loaded next;
   if (row < end) fetch(next);

@@ -112,6 +112,33 @@ def test_qk_norm_positions_outside_the_table_give_nan_rows():
     assert torch.equal(qo[:, keep], good[:, keep])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,interleaved", [(32, 16, False), (64, 8, True), (128, 64, False), (128, 128, True)])
+def test_qk_norm_positions_outside_the_table_are_nan_in_every_channel(d, rot, interleaved, dt):
+    """Rotated channels or not: the whole row of the output and of its gradient, and the sums
+    for the weights, which take every row in. Other rows keep their bits."""
+    import gated_delta_rule_69_amd as gdn
+    host, on = _qk_case((2, 7, 3, 2, d, rot), dt, 17, fuse=True)
+    P = on["cos"].shape[0]
+    kw = _kw(on, "l2", interleaved)
+    run = lambda: gdn.gdn_qk_norm_fwd(on["q"], on["k"], on["wq"], on["wk"], **kw) + tuple(  # noqa: E731
+        gdn.gdn_qk_norm_bwd(on["q"], on["k"], on["wq"], on["wk"], dq_out=on["dq"], dk_out=on["dk"], **kw)[n]
+        for n in ("dq", "dk", "dwq", "dwk"))
+    good = run()
+    assert all(torch.isfinite(x).all() for x in good)
+    bad = on["pos"].clone()
+    bad[0, 1], bad[0, 6], bad[1, 3] = -1, P, 2 ** 31 - 1
+    kw["positions"] = bad
+    got = run()
+    out = torch.zeros((2, 7), dtype=torch.bool)
+    out[0, 1] = out[0, 6] = out[1, 3] = True
+    for x, y in zip(got[:4], good[:4]):
+        assert torch.isnan(x.cpu()[out]).all()
+        assert torch.equal(x.cpu()[~out], y.cpu()[~out])
+    for x in got[4:]:
+        assert torch.isnan(x).all()
+
+
 def test_qk_norm_zero_rows_and_many_rows():
     """Rows of zeros stay zero under eps; a launch of many blocks touches every row."""
     import gated_delta_rule_69_amd as gdn
