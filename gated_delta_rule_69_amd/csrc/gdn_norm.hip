@@ -239,6 +239,17 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + (sizeof(E) == 2 ? __expf(-z) : expf(-z)));
 }
 
+// The sigmoid s and 1 - s, both from e = e^-|z|: 1 / (1 + e) and e / (1 + e) are within a few
+// steps wherever they lie, where the difference 1 - s would hold nothing of a gate far open
+// (e^-z is under a step of 1 from z = 17 on, and 1 % of it is lost at 12).
+template <typename E>
+__device__ __forceinline__ void sigmoid_both(float z, float* s, float* rest) {
+  const float e = sizeof(E) == 2 ? __expf(-fabsf(z)) : expf(-fabsf(z));
+  const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+  *s = z < 0.0f ? small : big;
+  *rest = z < 0.0f ? big : small;
+}
+
 template <typename E, int D, bool SILU, bool BWD>
 __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
   constexpr int L = D / 8;
@@ -290,9 +301,10 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNorm a) {
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = sigmoid<E>(z[i]);
+        float s, rest;
+        sigmoid_both<E>(z[i], &s, &rest);
         const float act = SILU ? z[i] * s : s;
-        const float slope = SILU ? s * (1.0f + z[i] * (1.0f - s)) : s * (1.0f - s);
+        const float slope = SILU ? s * (1.0f + z[i] * rest) : s * rest;
         x[i] *= r;
         const float dn = dy[i] * x[i];   // gradient of w act, but for its factors
         z[i] = dn * w[i] * slope;

@@ -214,6 +214,32 @@ def test_gated_norm_float32_gate_far_out(activation):
     assert (abs(y - want) <= 5.5 * 2.0 ** -23 * abs(want)).all(), float((abs(y - want) / abs(want)).max() * 2 ** 23)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("activation", ["silu", "sigmoid"])
+def test_gated_norm_gradient_of_a_gate_far_out(activation, dt):
+    """Every element of dgate, gates wide open too, where 1 - sigmoid is far under a step of 1.
+    Rows of +-1 with upstream 1 have r = 1, so dgate is +-act'(z). In steps of 2^-23, with n
+    those of e = e^-|z| (1 for float32; 1 + |z| / 2 for bf16, whose exponent is rounded first):
+    1 / (1 + e) takes n / 2 + 1.5 (half a step of the sum, one of the reciprocal), e / (1 + e)
+    n + 2. Sigmoid: their product and its half step, 1.5 n + 4. SiLU, s (1 + z rest): n + 2.5
+    of z rest, half a step of the sum, n + 2.5 of the product with s. Then the output's own half
+    step, 2^-8 or 2^-24 of the value."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import DTYPES, dev, f64
+    z = torch.linspace(-80, 80, 16 * 128).reshape(1, 16, 1, 128).to(DTYPES[dt])
+    x = torch.where(torch.arange(128) % 3 == 0, -1.0, 1.0).expand(z.shape).to(z.dtype).contiguous()
+    got = gdn.gdn_gated_norm_bwd(x.to(dev()), z.to(dev()), d_out=torch.ones_like(x).to(dev()), eps=0.0, activation=activation)
+    zz = f64(z)
+    s, rest = 1 / (1 + np.exp(-zz)), 1 / (1 + np.exp(zz))
+    # written out: the oracle's 1 - s is 0 in 64 bits from z = 37 on
+    want = np.sign(f64(x)) * (s * rest if activation == "sigmoid" else s * (1 + zz * rest))
+    n = 1.0 if dt == "f32" else 1 + abs(zz) / 2
+    steps = (1.5 * n + 4) * abs(want) if activation == "sigmoid" else s * abs(zz) * rest * (n + 2.5) + (n + 3) * abs(want)
+    bound = steps * 2.0 ** -23 + abs(want) * (2.0 ** -8 if dt == "bf16" else 2.0 ** -24)
+    off = abs(f64(got["dgate"]) - want)
+    assert (off <= bound).all(), (float(zz.flatten()[(off / bound).argmax()]), float((off / bound).max()))
+
+
 def test_norms_of_no_tokens():
     import gated_delta_rule_69_amd as gdn
     from layer_util import dev
