@@ -194,6 +194,51 @@ def test_extreme_decays():
     check(state, S_ref, "state of the step")
 
 
+@pytest.mark.parametrize("g", [-0.03, -1e-3, -1e-4, -1.3e-5, 1e-5])
+def test_slow_heads_over_many_tokens(g):
+    """A state that keeps thousands of tokens, token by token and in chunks: the decay's own
+    rounding must not add up. A token's rounding of the state is 2^-24 of it at most, N tokens'
+    (those the state keeps) add up as their root at random; five times that."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev, f64
+    T, d = 20000, 16
+    gen = torch.Generator().manual_seed(45)
+    q, k, v = (torch.randn((1, T, 1, d), generator=gen) for _ in range(3))
+    log_decay = torch.tensor([g])
+    w = np.exp(f64(log_decay) * np.arange(T - 1, -1, -1))
+    want = np.matmul((f64(k)[0, :, 0] * w[:, None]).T, f64(v)[0, :, 0])
+    last = np.matmul(f64(q)[0, -1, 0], want)
+    state = torch.zeros((1, 1, d, d), device=dev())
+    on = [x.to(dev()) for x in (q, k, v, log_decay)]
+    step = gdn.gdn_linear_recurrent_step(*on, state=state)
+    o, S = gdn.gdn_linear_chunk_fwd(*on)
+    most = 5 * 2.0 ** -24 * min(T, 1 / abs(g)) ** 0.5
+    for x, y, name in ((state, step, "step"), (S, o, "chunk")):
+        off = [np.linalg.norm(f64(a) - b) / np.linalg.norm(b) for a, b in ((x[0, 0], want), (y[0, -1, 0], last))]
+        print(name, g, off, most, flush=True)
+        assert max(off) <= max(most, 1e-6), (name, off, most)
+
+
+@pytest.mark.parametrize("tokens", [1, 7])
+def test_a_slow_head_decoded_call_by_call(tokens):
+    """The same over calls of one and of a few tokens, by the same rule."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev, f64
+    T, d, g = 20000 // tokens * tokens, 16, -1e-4
+    gen = torch.Generator().manual_seed(46)
+    k, v = (torch.randn((1, T, 1, d), generator=gen) for _ in range(2))
+    log_decay = torch.tensor([g])
+    w = np.exp(f64(log_decay) * np.arange(T - 1, -1, -1))
+    want = np.matmul((f64(k)[0, :, 0] * w[:, None]).T, f64(v)[0, :, 0])
+    state, gd = torch.zeros((1, 1, d, d), device=dev()), log_decay.to(dev())
+    rows = [x.to(dev()).split(tokens, 1) for x in (k, v)]
+    for kt, vt in zip(*rows):
+        gdn.gdn_linear_recurrent_step(kt, kt, vt, gd, state=state)
+    off = np.linalg.norm(f64(state)[0, 0] - want) / np.linalg.norm(want)
+    # calls of several tokens take one more step on the state each
+    assert off <= 5 * 2.0 ** -24 * (1 / abs(g)) ** 0.5, off
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_nothing_reaches_an_earlier_row(dt, value):
