@@ -100,6 +100,13 @@ def _beside(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
+def _rows_beside(v, seq_lens):
+    """An output of v's shape. A call writes no rows behind a sequence's length, so those of a
+    padded batch are cleared here: whatever the memory held would go on into the next operator,
+    and a NaN among it into a weight's gradient."""
+    return _beside(v) if seq_lens is None else _beside(v).zero_()
+
+
 # ---- checks ---------------------------------------------------------------------------
 
 def _elsewhere(t, name, stream):
@@ -205,7 +212,7 @@ def gdn_linear_chunk_fwd(q, k, v, log_decay, *, s0=None, s_final=None, o=None, s
     constant g <= 0 a value head (``log_decay`` [H]). q, k [B, T, Hk, dk], v [B, T, H, dv], H a
     multiple of Hk. Returns (o, s_final), allocated when not given; s_final may be s0.
     ``seq_lens`` [B] int32 gives each sequence's tokens in a padded batch: rows of o behind
-    them are left as they are."""
+    them are left as they are in a given o, and zero in one allocated here."""
     if _elsewhere(v, "v", stream):
         with _on(v, stream):
             return gdn_linear_chunk_fwd(q, k, v, log_decay, s0=s0, s_final=s_final, o=o, seq_lens=seq_lens,
@@ -214,7 +221,7 @@ def gdn_linear_chunk_fwd(q, k, v, log_decay, *, s0=None, s_final=None, o=None, s
     B, _, H, dv = rows = _heads(v, "v")
     state, f32, dev = (B, H, _heads(k, "k")[3], dv), torch.float32, v.get_device()
     if o is None:
-        o = _beside(v)
+        o = _rows_beside(v, seq_lens)
         to = o.data_ptr()
     else:
         to = _whole(o, "o", rows, v.dtype, dev)
@@ -231,13 +238,14 @@ def gdn_linear_chunk_fwd(q, k, v, log_decay, *, s0=None, s_final=None, o=None, s
 
 def gdn_linear_recurrent_step(q, k, v, log_decay, *, state, o=None, seq_lens=None, stream=None):
     """The same recurrence token by token on ``state`` [B, H, dk, dv] (updated in place):
-    T = 1 is one decode step. Returns o. A sequence of length 0 keeps its state."""
+    T = 1 is one decode step. Returns o; ``seq_lens`` as above. A sequence of length 0 keeps its
+    state."""
     if _elsewhere(v, "v", stream):
         with _on(v, stream):
             return gdn_linear_recurrent_step(q, k, v, log_decay, state=state, o=o, seq_lens=seq_lens)
     dev = v.get_device()
     if o is None:
-        o = _beside(v)
+        o = _rows_beside(v, seq_lens)
         to = o.data_ptr()
     else:
         to = _whole(o, "o", v.shape, v.dtype, dev)

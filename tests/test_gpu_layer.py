@@ -148,6 +148,39 @@ def test_whole_layer_against_automatic_gradients():
         assert e <= 6e-5, (name, e)
 
 
+def test_padded_batch_through_the_layer():
+    """A padded batch, outputs allocated by the calls, from memory that holds NaN: what lies
+    behind the lengths reaches neither the rows nor a gradient of what lies before them."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    t = _inputs("f32")
+    B, T = t["v"].shape[:2]
+    lens = [T, 43]
+    seq_lens = torch.tensor(lens, dtype=torch.int32, device=dev())
+    shape, dy = t["v"].shape, t["dy"].clone()
+    dy[1, lens[1]:] = 0
+    q, k, v, gate = (t[n].contiguous() for n in ("q", "k", "v", "gate"))
+
+    def leave_nan():  # the allocator hands this block out again
+        torch.cuda.synchronize()
+        torch.full(shape, float("nan"), device=dev())
+
+    state = torch.zeros((B, shape[2], q.shape[3], shape[3]), device=dev())
+    leave_nan()
+    o, _ = gdn.gdn_linear_chunk_fwd(q, k, v, t["g"], seq_lens=seq_lens)
+    leave_nan()
+    o2 = gdn.gdn_linear_recurrent_step(q, k, v, t["g"], state=state, seq_lens=seq_lens)
+    want, _ = layer.linear_forward(f64(q), f64(k), f64(v), f64(t["g"]), lens=lens)
+    for x in (o, o2):
+        assert (x[1, lens[1]:] == 0).all()
+        check(x, want, "o")
+    y = gdn.gdn_gated_norm_fwd(o, gate, t["w"], eps=1e-5)
+    back = gdn.gdn_gated_norm_bwd(o, gate, t["w"], d_out=dy, eps=1e-5)
+    ref = layer.gated_norm(f64(o), f64(gate), f64(t["w"]), eps=EPS, dy=f64(dy))
+    for got, r, name in zip((y, back["dx"], back["dgate"], back["dw"]), ref, ("y", "do", "dgate", "dw")):
+        check(got, r, name)
+
+
 def test_results_do_not_depend_on_what_runs_beside_them():
     """Two calls at once on two streams, and twice the same call: equal bits."""
     import gated_delta_rule_69_amd as gdn
