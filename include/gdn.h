@@ -323,8 +323,9 @@ size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_args* args);
 /* Gradients of o and s_final with respect to q, k, v and s0 (log_decay is a constant of
  * the model): with d_o [B, T, H, dv] in args->dtype (contiguous) and d_s_final
  * [B, H, dk, dv] float32 (NULL: zero),
- *     G_t = e^{g} G_{t+1} + q_t do_t^T  (G after the last token: d_s_final),
- *     dq_t = S_t do_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds0 = e^{g} G_1.
+ *     G_n = d_s_final + q_n do_n^T,  G_t = e^{g} G_{t+1} + q_t do_t^T  (t < n),
+ *     dq_t = S_t do_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  ds0 = e^{g} G_1,
+ * n the sequence's tokens; ds0 = d_s_final where n = 0.
  * args->o and args->s_final are ignored. Rows of d_o behind a sequence's length are not
  * used. ws must hold gdn_linear_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
 int gdn_linear_chunk_bwd(const gdn_linear_args* args, const void* d_o, const float* d_s_final,

@@ -100,3 +100,20 @@ def test_gated_norm_against_differences(activation):
     loss = lambda: float((layer.gated_norm(x, z, w, **kw) * dy).sum())  # noqa: E731
     for got, leaf in ((dx, x), (dz, z), (dw, w)):
         np.testing.assert_allclose(got, _differences(loss, leaf), rtol=1e-6, atol=1e-8)
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 9])
+@pytest.mark.parametrize("log_decay", [-0.3, float("-inf")])
+def test_the_gradients_recurrence_as_the_header_states_it(log_decay, n):
+    """G_n = d_s_final + q_n do_n^T, undecayed, then G_t = e^g G_{t+1} + q_t do_t^T; ds0 = e^g G_1,
+    or d_s_final itself for a sequence of no tokens."""
+    rng = np.random.default_rng(n)
+    q, k, v, do = (rng.standard_normal((1, 9, 1, d)) for d in (4, 4, 3, 3))
+    ds = rng.standard_normal((1, 1, 4, 3))
+    got = layer.linear_backward(q, k, v, [log_decay], do, ds_final=ds, lens=[n])
+    G, gam = ds[0, 0], np.exp(log_decay)
+    for t in range(n - 1, -1, -1):
+        G = (G if t == n - 1 else gam * G) + np.outer(q[0, t, 0], do[0, t, 0])
+        np.testing.assert_allclose(got["dk"][0, t, 0], G @ v[0, t, 0], rtol=1e-12, atol=1e-12)
+        np.testing.assert_allclose(got["dv"][0, t, 0], G.T @ k[0, t, 0], rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(got["ds0"][0, 0], gam * G if n else ds[0, 0], rtol=1e-12, atol=1e-12)
