@@ -272,9 +272,16 @@ int gdn_recurrent_bwd(const gdn_args* args, const void* d_o, const float* d_s_fi
  * or a stride of 2^24, and from B * H * max(dk, dv) = 2^30 on (the norms below: the same
  * without the last and with T = 2^31).
  * Ownership, asynchrony, determinism and errors as above; the current device must be
- * the stream's. A NaN or Inf in token t makes o NaN or Inf from token t on, until its decay
- * leaves nothing of it (weights under 2^-127 are 0), and never reaches an earlier row; of
- * float32 inputs, magnitudes above 3.3e38 count as Inf. */
+ * the stream's.
+ * A NaN or Inf in row t of k or v makes the rows of o from t on NaN or Inf (v: in its
+ * column), at least as long as the row's weight e^{g (i - t)} is over 2^-127; one in q its
+ * own row of o. It never reaches an earlier row, another head or another sequence. Behind
+ * that weight nothing is promised: 0 times NaN is NaN where tokens go one by one and within
+ * a segment of the chunked pass, while a segment does not read rows that weigh nothing, and
+ * where segments begin goes by the sizes and by whether seq_lens is given. A finite s_final of a head that
+ * forgets is no sign of finite inputs. In the gradients below the same holds along each
+ * formula (in dk and dv from the row backwards). Of float32 inputs, magnitudes above
+ * 3.3e38 count as Inf. */
 typedef struct gdn_linear_args {
   int32_t dtype;          /* enum gdn_dtype: q, k, v and o                    */
   int32_t reserved;       /* must be 0                                        */

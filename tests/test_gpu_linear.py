@@ -261,6 +261,83 @@ def test_nothing_reaches_an_earlier_row(dt, value):
             assert not torch.isfinite(o[0, 70:, 1, 5]).any()
 
 
+T_BAD, AT = 1200, 10  # several segments where there are few heads, one where there are many
+
+
+def _paths(x, g, wide):
+    """(name, o, s_final) of one sequence: chunked, in a batch of many, and token by token."""
+    import gated_delta_rule_69_amd as gdn
+    o, S = gdn.gdn_linear_chunk_fwd(x["q"], x["k"], x["v"], g)
+    state = torch.zeros_like(S)
+    step = gdn.gdn_linear_recurrent_step(x["q"], x["k"], x["v"], g, state=state)
+    many = [x[n].expand(wide, *x[n].shape[1:]).contiguous() for n in "qkv"]
+    ob, Sb = gdn.gdn_linear_chunk_fwd(*many, g)
+    return ("chunk", o[0], S[0]), ("batch", ob[0], Sb[0]), ("step", step[0], state[0])
+
+
+def _reach(now, was, rows, least, name):
+    """``now`` is not finite in the rows of ``least``, and has the bits of ``was`` outside of
+    ``rows`` (both ranges)."""
+    bad = (~torch.isfinite(now)).any(-1).cpu()
+    assert bad[list(least)].all(), name
+    keep = [i for i in range(now.shape[0]) if i not in rows]
+    assert torch.equal(now[keep], was[keep]), name
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_how_far_a_bad_row_reaches_at_least(dt, value):
+    """Head 0 forgets within 88 tokens (weights from 2^-127 on), head 1 keeps it to the end: the
+    rows that are promised, whichever way the sequence is cut, and no other head."""
+    host, on = make((1, T_BAD, 3, 3, 32, 32), dt, 47)
+    g = torch.tensor([-1.0, -1e-3, -1e-2], device=on["q"].device)
+    clean = _paths(on, g, 256)
+    assert torch.isfinite(clean[0][1]).all()
+    for name in "qkv":
+        x = {n: on[n].clone() for n in "qkv"}
+        x[name][0, AT, :2, 5] = value
+        for (path, o, S), (_, o0, S0) in zip(_paths(x, g, 256), clean):
+            print(name, path, flush=True)
+            if name == "q":
+                _reach(o[:, 0], o0[:, 0], [AT], [AT], (name, path))
+                assert torch.equal(S, S0)
+                continue
+            _reach(o[:, 0], o0[:, 0], range(AT, T_BAD), range(AT, AT + 88), (name, path))
+            _reach(o[:, 1], o0[:, 1], range(AT, T_BAD), range(AT, T_BAD), (name, path))
+            assert torch.equal(o[:, 2], o0[:, 2]) and torch.equal(S[2], S0[2]), (name, path)
+            assert not torch.isfinite(S[1]).all(), (name, path)
+
+
+@pytest.mark.parametrize("wide", [1, 256])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_how_far_a_bad_row_reaches_in_the_gradients(dt, wide):
+    """Along each formula: dq from a row of k or v on, dk and dv from a row of q or do
+    backwards, else the row alone."""
+    import gated_delta_rule_69_amd as gdn
+    host, on = make((1, T_BAD, 3, 3, 32, 32), dt, 48)
+    g = torch.tensor([-1.0, -1e-3, -1e-2], device=on["q"].device)
+    names = ("q", "k", "v", "do")
+    on = {n: on[n].expand(wide, *on[n].shape[1:]).contiguous() for n in names}
+    run = lambda x: gdn.gdn_linear_chunk_bwd(x["q"], x["k"], x["v"], g, d_o=x["do"])  # noqa: E731
+    clean = run(on)
+    t = T_BAD - AT
+    row, after, before = (range(t, t + 1),) * 2, (range(t, T_BAD), range(t, T_BAD)), (range(0, t + 1), range(t - 87, t + 1))
+    reach = {"q": dict(dk=before, dv=before), "k": dict(dq=after, dv=row), "v": dict(dq=after, dk=row),
+             "do": dict(dq=row, dk=before, dv=before)}
+    for name in names:
+        x = {n: on[n].clone() for n in names}
+        x[name][0, t, :2, 5] = float("nan")
+        got = run(x)
+        for out in ("dq", "dk", "dv"):
+            rows, least = reach[name].get(out, ((), ()))
+            for h in (0, 1):
+                print(name, out, h, flush=True)
+                _reach(got[out][0, :, h], clean[out][0, :, h], rows, rows if h else least, (name, out, h))
+            assert torch.equal(got[out][:, :, 2], clean[out][:, :, 2]) and torch.equal(got[out][1:], clean[out][1:])
+        if name in ("q", "do"):
+            assert not torch.isfinite(got["ds0"][0, 1]).all() and torch.equal(got["ds0"][0, 2], clean["ds0"][0, 2])
+
+
 def test_agrees_with_the_asym_entry_without_its_erase():
     """The library's ASYM recurrence with j = 0, eta = 1 and one decay a head."""
     import gated_delta_rule_69_amd as gdn
