@@ -85,6 +85,24 @@ def test_qk_norm_without_weights_positions_or_upstream_in_bf16():
         check(g["d" + which], dx, "d" + which)
 
 
+@pytest.mark.parametrize("B,T,Hq,Hk,d", [(7, 1, 1, 1, 16), (300, 2, 1, 1, 16), (90, 3, 2, 1, 16), (50, 7, 1, 1, 32),
+                                          (3, 129, 1, 1, 16), (2, 130, 5, 2, 16), (2, 999, 16, 8, 64), (40, 300, 3, 1, 16)])
+def test_qk_norm_default_positions_are_those_of_each_sequence(B, T, Hq, Hk, d):
+    """No positions: 0 .. T-1 in every sequence, bit for bit, where a step of the walk over the
+    rows is many sequences, less than one, or a token's heads; several steps a block."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    _, on = _qk_case((B, T, Hq, Hk, d, 16), "f32", 18, fuse=False)
+    kw = _kw(on, "rms", False)
+    run = lambda: gdn.gdn_qk_norm_fwd(on["q"], on["k"], on["wq"], on["wk"], **kw) + tuple(  # noqa: E731
+        gdn.gdn_qk_norm_bwd(on["q"], on["k"], on["wq"], on["wk"], dq_out=on["dq"], dk_out=on["dk"], **kw).values())
+    kw["positions"] = torch.arange(T, dtype=torch.int32, device=dev()).expand(B, T).contiguous()
+    want = run()
+    kw["positions"] = None
+    for x, y in zip(run(), want):
+        assert torch.equal(x, y)
+
+
 def test_qk_norm_in_place_equals_out_of_place():
     import gated_delta_rule_69_amd as gdn
     _, on = _qk_case((2, 41, 3, 2, 128, 128), "bf16", 13, fuse=False)
