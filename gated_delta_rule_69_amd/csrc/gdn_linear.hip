@@ -205,8 +205,7 @@ struct Segments {
 Segments choose_segments(const LinearProblem& p, int da, int dc, int passes) {
   const bool half = p.dtype == GDN_DTYPE_BF16;
   const int64_t C = half ? 64 : 32;
-  const int64_t lds = half ? 2 * C * (3 * da + dc) + 13312 : 6 * C * (2 * da + dc) + 7168;
-  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((160 << 10) / lds, (half ? 16 : 12) / pass_waves(dc)));
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((160 << 10) / outputs_lds(half, da, dc), (half ? 16 : 12) / pass_waves(dc)));
   const int64_t wanted = 256 * resident * (p.seq_lens != nullptr ? 4 : 3) / 3;
   const int64_t chunks = (p.T + C - 1) / C;
   const int64_t want = std::max<int64_t>(1, wanted / (p.B * p.H * passes));

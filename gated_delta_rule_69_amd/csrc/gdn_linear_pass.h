@@ -80,6 +80,13 @@ template <typename E> struct PassShape {
   static constexpr int kChunk = kHalf ? 64 : 32;
 };
 constexpr int pass_waves(int DC) { return DC / 16; }  // sixteen columns of the state a wave
+// Bytes of LDS of a workgroup of the outputs' kernel (asserted there): tiles of a, b and c,
+// scores, weights, decays, and an int a column.
+constexpr int outputs_lds(bool half, int DA, int DC) {
+  const int C = half ? 64 : 32, parts = half ? 1 : 3;
+  const int tiles = 2 * parts * C * ((half ? 3 : 2) * DA + DC), scores = half ? 4 * 32 * (32 + 64) : 6 * (32 * 32 + 64);
+  return (tiles + scores + 4 * (2 * C + C + 1 + DC) + 15) / 16 * 16;
+}
 
 // x[0..N) as sums of PARTS bf16 values part[p][i], two at a time: one packed conversion,
 // and what is left by subtracting its halves, which are floats but for their position.
@@ -463,6 +470,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     float decay[C + 1];  // powers of l
     int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
   };
+  static_assert(sizeof(Shared) == outputs_lds(S::kHalf, DA, DC), "choose_segments goes by outputs_lds");
   __shared__ Shared sh;
   Segment<E, DA, DC> me(s, s.nseg, false);
   const int wave = me.wave;
