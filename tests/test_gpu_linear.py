@@ -84,6 +84,51 @@ def test_gradients_against_the_recurrence(case, states, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [(2, 130, 3, 3, 64, 64), (1, 1100, 2, 2, 64, 64), (2, 65, 2, 2, 128, 128),
+                                  (1, 1100, 3, 3, 128, 128)], ids=lambda c: "-".join(map(str, c)))
+def test_gradients_of_heads_of_their_own(case, dt):
+    """dk = dv and unshared key heads, whose dq, dk and dv are one launch: one and several
+    segments, whole and padded."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    host, on = make(case, dt, 49)
+    B, T = case[:2]
+    for lens in (None, [T - 1 - 40 * b for b in range(B)]):
+        want = layer.linear_backward(*(f64(host[n]) for n in ("q", "k", "v", "g", "do")), s0=f64(host["s0"]),
+                                     ds_final=f64(host["ds"]), lens=lens)
+        got = gdn.gdn_linear_chunk_bwd(on["q"], on["k"], on["v"], on["g"], d_o=on["do"], s0=on["s0"], ds_final=on["ds"],
+                                       seq_lens=None if lens is None else torch.tensor(lens, dtype=torch.int32, device=dev()))
+        for name in ("dq", "dk", "dv", "ds0"):
+            check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 7, 150, 900])
+def test_what_lies_behind_a_length_is_not_read(T, dt):
+    """NaN and Inf in every input's rows behind the lengths change no bit."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    _, on = make((4, T, 4, 2, 32, 64), dt, 50)
+    lens = [T, 0, T // 2, T - 1]
+    seq_lens = torch.tensor(lens, dtype=torch.int32, device=dev())
+    names = ("q", "k", "v", "do")
+    bad = {n: on[n].clone() for n in names}
+    for i, n in enumerate(names):
+        for b, m in enumerate(lens):
+            bad[n][b, m:] = float("nan") if (i + b) % 2 else float("inf")
+
+    def run(x):
+        o, S = gdn.gdn_linear_chunk_fwd(x["q"], x["k"], x["v"], on["g"], s0=on["s0"], seq_lens=seq_lens)
+        state = on["s0"].clone()
+        step = gdn.gdn_linear_recurrent_step(x["q"], x["k"], x["v"], on["g"], state=state, seq_lens=seq_lens)
+        back = gdn.gdn_linear_chunk_bwd(x["q"], x["k"], x["v"], on["g"], d_o=x["do"], s0=on["s0"], ds_final=on["ds"],
+                                        seq_lens=seq_lens)
+        return [o, S, step, state, *back.values()]
+    for x, y in zip(run(bad), run({n: on[n] for n in names})):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("T,lens", [(150, [150, 0, 64, 97, -1]), (900, [900, 0, 256, 701, 31])])
 def test_gradients_of_a_padded_batch(T, lens, dt):
     """Rows behind a length get zero gradients, whatever d_o holds there; one and several
@@ -412,6 +457,34 @@ def test_another_stream_and_a_captured_graph():
         want_step = gdn.gdn_linear_recurrent_step(*step, on["g"], state=eager)
         assert torch.equal(out, want) and torch.equal(S, S_want)
         assert torch.equal(so, want_step) and torch.equal(state, eager)
+
+
+@pytest.mark.parametrize("T", [1, 90])
+def test_a_padded_batch_in_a_captured_graph(T):
+    """Outputs allocated inside the capture, cleared and written at every replay, for lengths
+    that change between replays."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    _, on = make((3, T, 4, 2, 32, 32), "bf16", 51)
+    seq_lens, state = torch.full((3,), T, dtype=torch.int32, device=dev()), on["s0"].clone()
+    run = lambda st: (*gdn.gdn_linear_chunk_fwd(on["q"], on["k"], on["v"], on["g"], s0=on["s0"], seq_lens=seq_lens),  # noqa: E731
+                      gdn.gdn_linear_recurrent_step(on["q"], on["k"], on["v"], on["g"], state=st, seq_lens=seq_lens))
+    run(on["s0"].clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(state)
+    for lens in ([T, T, T], [T // 2, 0, T], [0, T, T - 1]):
+        seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        state.copy_(on["s0"])
+        for x in got:
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = on["s0"].clone()
+        for x, y in zip((*got, state), (*run(eager), eager)):
+            assert torch.equal(x, y)
+        for b, n in enumerate(lens):
+            assert (got[0][b, n:] == 0).all() and (got[2][b, n:] == 0).all()
 
 
 def test_rows_far_apart():
