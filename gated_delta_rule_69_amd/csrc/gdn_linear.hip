@@ -32,17 +32,6 @@ struct LinearSeq {
 };
 constexpr int kSeqWaves = 4;
 
-// e^g as hi + lo. Rounded to hi alone it is off by up to 2^-25, the same way at every token,
-// and a state that keeps some 1 / |g| tokens adds that up to 2^-25 / |g|: 1.3e-4 of the state
-// at g = -1e-4 in 20,000 tokens, where the state's own roundings come to 2e-6. From a factor
-// of e^-1/2 on it is gone before it adds up.
-__device__ __forceinline__ void head_decay(float g, float* hi, float* lo) {
-  const float less = expm1f(g);
-  const bool slow = fabsf(g) < 0.5f;
-  *hi = slow ? 1.0f + less : expf(g);
-  *lo = slow ? less - (*hi - 1.0f) : 0.0f;
-}
-
 // ONE: a call of one token, whose state takes hi and lo. In longer ones a token's factor is hi
 // and what those before left out, as soon as that is half a step, and the state takes the rest
 // in the end (hi and lo at every token: 33 us against 27 for 8 tokens of 1024 heads of 128).
@@ -61,7 +50,7 @@ __global__ __launch_bounds__(64 * kSeqWaves) void linear_seq_kernel(LinearSeq a)
   const int h = int(bh - b * a.H);
   const int64_t n = length_of(a.seq_lens, b, a.T);
   float decay, decay_lo;
-  head_decay(head_log_decay(a.log_decay, h), &decay, &decay_lo);
+  two_floats(head_log_decay(a.log_decay, h), &decay, &decay_lo);
   const int64_t at = (bh * DK + g * NR) * a.dv + col;
 
   float S[NR][4];
@@ -169,7 +158,9 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int 
   const int64_t n = length_of(s.seq_lens, bh / s.H, s.T);
   const float lg = head_log_decay(s.log_decay, int(bh % s.H));
   // a segment that leaves nothing of the one before: every state is its segment's own already
-  if (n > (s.nseg - 1) * s.seg && expf(lg * float(s.seg)) == 0.0f) return;
+  float whole, whole_lo;
+  two_floats(lg * float(s.seg), &whole, &whole_lo);
+  if (n > (s.nseg - 1) * s.seg && whole == 0.0f) return;
   float* slot = s.states + bh * s.nseg * per_state + at;
   float x[4];
   load4(slot + per_state, x);
@@ -184,9 +175,10 @@ __global__ __launch_bounds__(256) void scan_states_kernel(LinearPasses all, int 
     for (int k = 0; k < N; ++k) {
       if (seg + k >= s.nseg) break;
       const int64_t left = n - (seg + k - 1) * s.seg;
-      const float w = expf(lg * float(left < 0 ? 0 : left > s.seg ? s.seg : left));
+      float w = whole, w_lo = whole_lo;
+      if (left < s.seg) two_floats(lg * float(left < 0 ? 0 : left), &w, &w_lo);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = y[k][e] + w * x[e];
+      for (int e = 0; e < 4; ++e) x[e] = w * x[e] + (w_lo * x[e] + y[k][e]);
       store4(slot + int64_t(seg + k) * per_state, x);
     }
   }

@@ -66,6 +66,18 @@ __device__ __forceinline__ float head_log_decay(const float* g, int h) {
   return x < -128.0f ? -128.0f : x;
 }
 
+// e^g as hi + lo. Rounded to hi alone a token's decay is off by up to 2^-25, the same way at
+// every token, and a state that keeps some 1 / |g| tokens adds that up to 2^-25 / |g|: 1.3e-4 of
+// the state at g = -1e-4 in 20,000 tokens, where the state's own roundings come to 2e-6. A
+// chunk's or a segment's decay is applied less often and adds up to 4.5e-5 at g = -3e-6 in
+// 131,072 tokens. From a factor of e^-1/2 on it is gone before it adds up.
+__device__ __forceinline__ void two_floats(float g, float* hi, float* lo) {
+  const float less = expm1f(g);
+  const bool slow = fabsf(g) < 0.5f;
+  *hi = slow ? 1.0f + less : expf(g);
+  *lo = slow ? less - (*hi - 1.0f) : 0.0f;
+}
+
 // Tokens of sequence b.
 __device__ __forceinline__ int64_t length_of(const int32_t* lens, int64_t b, int64_t T) {
   if (lens == nullptr) return T;
@@ -81,11 +93,11 @@ template <typename E> struct PassShape {
 };
 constexpr int pass_waves(int DC) { return DC / 16; }  // sixteen columns of the state a wave
 // Bytes of LDS of a workgroup of the outputs' kernel (asserted there): tiles of a, b and c,
-// scores, weights, decays, and an int a column.
+// scores, weights, decays and what the last leaves out, and an int a column.
 constexpr int outputs_lds(bool half, int DA, int DC) {
   const int C = half ? 64 : 32, parts = half ? 1 : 3;
   const int tiles = 2 * parts * C * ((half ? 3 : 2) * DA + DC), scores = half ? 4 * 32 * (32 + 64) : 6 * (32 * 32 + 64);
-  return (tiles + scores + 4 * (2 * C + C + 1 + DC) + 15) / 16 * 16;
+  return (tiles + scores + 4 * (2 * C + C + 2 + DC) + 15) / 16 * 16;
 }
 
 // x[0..N) as sums of PARTS bf16 values part[p][i], two at a time: one packed conversion,
@@ -468,6 +480,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     Scores<C, PS> scores;
     float weight[2][C];  // l^{n-1-j+shift}
     float decay[C + 1];  // powers of l
+    float decay_lo;      // of l^C: what decay[C] leaves out
     int bad_from[DC];    // first position of the chunk whose c is not finite, a channel
   };
   static_assert(sizeof(Shared) == outputs_lds(S::kHalf, DA, DC), "choose_segments goes by outputs_lds");
@@ -520,7 +533,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     else fetch_c(begin);
   }
 
-  for (int at = threadIdx.x; at <= C; at += NT) sh.decay[at] = me.power(at);
+  for (int at = threadIdx.x; at < C; at += NT) sh.decay[at] = me.power(at);
+  if (threadIdx.x == 0) two_floats(head_log_decay(s.log_decay, me.h) * float(C), &sh.decay[C], &sh.decay_lo);
+  float left = 0.0f;  // of the chunks' decays, not in the state yet: into it as soon as it is half a step of the next
   __syncthreads();
   int buf = 0;
   for (int p = begin; p < end; p += C, buf ^= 1) {
@@ -610,7 +625,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
     // what the chunk's own rows give, and the state after it
     __builtin_amdgcn_s_setprio(2);
     bool bad = false;
-    const float whole = me.power(m);
+    left += sh.decay_lo;
+    const float once = m == C ? sh.decay[C] : me.power(m), whole = once + left;
+    left = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(left - (whole - once))));
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) X[kt] *= whole;
 #pragma unroll

@@ -264,6 +264,30 @@ def test_slow_heads_over_many_tokens(g):
         assert max(off) <= max(most, 1e-6), (name, off, most)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 1024])
+def test_slow_heads_over_many_chunks(H, dt):
+    """131,072 tokens as many segments and as one: the decays of chunks and of segments must not
+    add up either. By the rule above for the 32 tokens of a chunk, which takes eight roundings
+    (its scaling and the sums of its products): sqrt(8 tokens / 32) as many as tokens."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import DTYPES, dev
+    T, d = 131072, 16
+    gen = torch.Generator(device=dev()).manual_seed(52)
+    k, v = (torch.randn((1, T, 1, d), generator=gen, device=dev()).to(DTYPES[dt]) for _ in range(2))
+    many = v.expand(1, T, H, d).contiguous()
+    back = torch.arange(T - 1, -1, -1, dtype=torch.float64, device=dev())
+    for g in (-1e-3, -1e-4, -1e-5, -3e-6, -1e-6):
+        log_decay = torch.full((H,), g, device=dev())
+        _, S = gdn.gdn_linear_chunk_fwd(k, k, many, log_decay)
+        w = torch.exp(log_decay[0].double() * back)
+        want = torch.matmul((k[0, :, 0].double() * w[:, None]).T.contiguous(), v[0, :, 0].double())
+        off = float((S[0, H // 2].double() - want).norm() / want.norm())
+        most = 5 * 2.0 ** -24 * (min(T, 1 / abs(g)) * 8 / 32) ** 0.5
+        print(H, dt, g, off, most, flush=True)
+        assert off <= max(most, 1e-6), (g, off, most)
+
+
 @pytest.mark.parametrize("tokens", [1, 7])
 def test_a_slow_head_decoded_call_by_call(tokens):
     """The same over calls of one and of a few tokens, by the same rule."""
