@@ -12,11 +12,14 @@
 //     out = (mask(a b^T)) c + Diag(l^{i+1}) a X,   X' = l^n X + b^T Diag(l^{n-1-j}) c
 // with mask_ij = l^{i-j} for j <= i. All four products run on bf16 MFMA 16x16x32. Factors
 // that are not bf16 values enter as sums of bf16 parts x = x0 + x1 (+ x2), each the rounding
-// of what is left (8 bits a part, float32's range): bf16 inputs take the masked scores and
-// the state in two parts (2^-16, under the output's rounding) and the weighted c of the state
-// update in three (2^-24: the state is a float32 result); float32 inputs are three parts
-// themselves, and of the nine products of parts the six above 2^-24 are formed. By the
-// instructions' rates six bf16 products are 2.7 times as fast as the float32 MFMA.
+// of what is left (8 bits a part, float32's range). The weighted c of the state update is three
+// parts (2^-24), so that the state is a float32 sum on either type. Of bf16 inputs the masked
+// scores and the state as it enters a X are two (2^-17 at most, under the output's 2^-8): three of
+// the state take 382 us for 359 at the long prompt below and 145 for 133 for the 4K gradients,
+// three of the scores the LDS of a second workgroup, and the outputs are as far from float64
+// either way, 1.7e-3. Float32 inputs are three parts themselves, and of the nine products of
+// parts the six above 2^-24 are formed: results 2 to 3e-7 from float64. By the instructions'
+// rates six bf16 products are 2.7 times as fast as the float32 MFMA.
 //
 // One workgroup runs one segment of a head. Its waves share the chunk's tiles in LDS and
 // split the DC columns of the state, sixteen a wave, which it keeps in accumulators: an
@@ -370,10 +373,10 @@ __device__ __forceinline__ void weighted(const T& tile, const float* weight, int
   for (int e = 0; e < 8; ++e) x[e] *= weight[32 * kb + 8 * g + e];
 }
 
-// X += b^T (weighted c) of a k-block of positions: parts FIRST .. W-1 of c.
-template <typename E, int DA, int FIRST, int W, typename T>
+// X += b^T (weighted c) of a k-block of positions, three parts of c: a float32 sum.
+template <typename E, int DA, typename T>
 __device__ __forceinline__ void add_outer(float4v* X, const T& tile, int kb, int at, const float* x) {
-  constexpr int P = PassShape<E>::kParts, KT = DA / 16, N = KT < 2 ? KT : 2;
+  constexpr int P = PassShape<E>::kParts, W = 3, KT = DA / 16, N = KT < 2 ? KT : 2;
   bhalf8 wv[W];
   split_parts<W, 8>(x, wv);
 #pragma unroll
@@ -383,7 +386,7 @@ __device__ __forceinline__ void add_outer(float4v* X, const T& tile, int kb, int
     for (int t = 0; t < N; ++t)
 #pragma unroll
       for (int q = 0; q < P; ++q) bv[t][q] = tile.columns(q, kb, at, (kt + t) / 2, (kt + t) % 2);
-    mma_parts<N, P, W - FIRST, W - 1 - FIRST>([&](int t, int p) { return bv[t][p]; }, [&](int, int p) { return wv[FIRST + p]; }, X + kt);
+    mma_parts<N, P, W, W - 1>([&](int t, int p) { return bv[t][p]; }, [&](int, int p) { return wv[p]; }, X + kt);
   }
 }
 
@@ -447,7 +450,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       bhalf8 cv[P];
       float x[8];
       weighted<E, DC>(sh.c[at], sh.weight[buf], kb, at_c, me.g, cv, x);
-      add_outer<E, DA, 0, 3>(X, sh.b[at], kb, at_b, x);
+      add_outer<E, DA>(X, sh.b[at], kb, at_b, x);
     }
     if (!more) break;
     if constexpr (!kDirect) __syncthreads();
@@ -519,9 +522,6 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
   int at_first = Tile<32, 32, PS>::row_place(me.i, me.g), at_second = Tile<32, 64, PS>::row_place(me.i, me.g);
   const uint32_t out_step = uint32_t(s.H) * DC * uint32_t(sizeof(O));  // at most 2^25: a chunk's offsets fit in 31 bits
   uint32_t at_out = (16 * wave + 4 * me.g) * uint32_t(sizeof(O)) + (s.back ? 0u - me.i * out_step : me.i * out_step);
-  // The third part of the weighted c is for the state that is a result (wanted or not, so
-  // that outputs do not depend on that).
-  const bool exact = me.seg == s.nseg - 1;
   // Order of a chunk's loads and barriers. bf16: `a` and `b` are there at the start of a
   // chunk; `c` arrives while scores and a X are formed, the next `a` (its tile is read no
   // more) and `b` (the other buffer) while the chunk's own rows are summed: two workgroups
@@ -661,13 +661,7 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
       };
       if (kb == 0) own_rows(std::integral_constant<int, 0>{});
       else own_rows(std::integral_constant<int, PB == 2 ? 2 : 0>{});
-      add_outer<E, DA, 0, S::kHalf ? 2 : 3>(X, tb, kb, at_b, x);
-      if constexpr (S::kHalf) {
-        if (exact) {  // the third part, from a second look at c: it holds no registers meanwhile
-          weighted<E, DC>(sh.c, sh.weight[buf], kb, at_c, g, cv, x);
-          add_outer<E, DA, 2, 3>(X, tb, kb, at_b, x);
-        }
-      }
+      add_outer<E, DA>(X, tb, kb, at_b, x);
     }
 
     if constexpr (kDirect) wait_loads();
