@@ -14,7 +14,7 @@
 // that are not bf16 values enter as sums of bf16 parts x = x0 + x1 (+ x2), each the rounding
 // of what is left (8 bits a part, float32's range). The weighted c of the state update is three
 // parts (2^-24), so that the state is a float32 sum on either type. Of bf16 inputs the masked
-// scores and the state as it enters a X are two (2^-17 at most, under the output's 2^-8): three of
+// scores and the state as it enters a X are two (2^-16 at most, under the output's 2^-8): three of
 // the state take 382 us for 359 at the long prompt below and 145 for 133 for the 4K gradients,
 // three of the scores the LDS of a second workgroup, and the outputs are as far from float64
 // either way, 1.7e-3. Float32 inputs are three parts themselves, and of the nine products of
@@ -461,9 +461,9 @@ __global__ __launch_bounds__(64 * pass_waves(DC), PassShape<E>::kHalf ? 4 : 2) v
 // The outputs of a segment, chunk by chunk from the state before it; the last segment's
 // workgroup also has the pass's last state.
 //
-// At B2 T32768 H16 d128 bf16 it takes 250 us for 1.07 GB (4.3 TB/s); its loads and stores
-// alone take 220, its arithmetic alone 224: vector instructions (addresses, splits into parts,
-// scores) take 55 % of the issue slots and keep the MFMAs 32 % busy. Sixteen columns a wave
+// At B2 T32768 H16 d128 bf16 it takes 234 us at best for 1.07 GB (4.6 TB/s), 279 on average
+// under load; its loads and stores alone take 220: vector instructions (addresses, splits into
+// parts, scores) take 68 % of the issue slots, the MFMAs are busy 43 %. Sixteen columns a wave
 // and eight waves equal thirty-two and four there and are a tenth faster at T4096, where a
 // chunk's latency counts. Float32 B8 T2047 H32 d64, padded: 82 us.
 template <typename E, typename O, int DA, int DC>

@@ -7,10 +7,12 @@
 // range of its own and keeps (token, head) of its next row by addition, so there is no
 // division in the loop, and a row's loads run one step ahead of its use.
 //
-// bf16, d 128: queries and keys of 65,536 tokens, 16 heads each, 217 to 227 us (1.11 GB,
-// 4.9 to 5.1 TB/s); the gated norm of 65,536 tokens x 16 heads 141 to 144 us (805 MB, 5.6
-// TB/s, a large copy's rate). Backward at 8,192 tokens: 33 us (153 MB) and 28 us (168 MB),
-// and 4 us for the weights' sums in a second kernel, whose order is fixed.
+// bf16, d 128: queries and keys of 65,536 tokens, 16 heads each, 215 to 228 us (1.11 GB, 4.9
+// to 5.1 TB/s; a copy of 512 MiB reaches 5.39), float32 382 us (5.7); the gated norm of 65,536
+// tokens x 16 heads 142 to 145 us (805 MB, 5.6 TB/s), float32 277 us (5.8). Backward at 8,192
+// tokens: 34 to 35 us (153 MB) and 29 to 30 us (168 MB), and 4 us for the weights' sums in a
+// second kernel, whose order is fixed. Those sums are float32: at d 128 rows / 16,384 terms a
+// lane, then 16 of a block, 16 blocks and a tree of six, 6e-6 at worst for a million rows.
 #include <algorithm>
 
 #include "gdn_layer.h"

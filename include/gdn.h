@@ -272,7 +272,8 @@ int gdn_recurrent_bwd(const gdn_args* args, const void* d_o, const float* d_s_fi
  * or a stride of 2^24, and from B * H * max(dk, dv) = 2^30 on (the norms below: the same
  * without the last and with T = 2^31).
  * Ownership, asynchrony, determinism and errors as above; the current device must be
- * the stream's.
+ * the stream's. States are float32 sums on either type; of bf16 inputs the scores q k^T and
+ * the state as it meets q enter the chunked products to 2^-16, under the rounding of o.
  * A NaN or Inf in row t of k or v makes the rows of o from t on NaN or Inf (v: in its
  * column), at least as long as the row's weight e^{g (i - t)} is over 2^-127; one in q its
  * own row of o. It never reaches an earlier row, another head or another sequence. Behind
