@@ -1,0 +1,67 @@
+// Device helpers of the operators of a block: lengths, sigmoids, sums of columns.
+#pragma once
+
+#include "gdn_layer_device.h"
+
+namespace gdn {
+
+__device__ __forceinline__ int64_t tokens_of(const int32_t* lens, int64_t b, int64_t T) {
+  if (lens == nullptr) return T;
+  const int64_t n = lens[b];
+  return n < 0 ? 0 : n > T ? T : n;
+}
+
+// e^x. bf16 values take the one-instruction 2^x of x log2 e, off by |x| 2^-24; float32 expf.
+template <typename E>
+__device__ __forceinline__ float exp_of(float x) {
+  return sizeof(E) == 2 ? __expf(x) : expf(x);
+}
+
+// The sigmoid s of z and 1 - s, both from e^-|z|, so that neither is a difference.
+template <typename E>
+__device__ __forceinline__ void sigmoids(float z, float* s, float* rest) {
+  const float e = exp_of<E>(-fabsf(z));
+  const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+  *s = z < 0.0f ? small : big;
+  *rest = z < 0.0f ? big : small;
+}
+// The sigmoid alone: the reciprocal of at least 1, 0 where e^-z overflows.
+template <typename E>
+__device__ __forceinline__ float sigmoid_of(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_of<E>(-z));
+}
+
+// out[c] = sum over rows of partial[row][c] for c < cols, split over up to three arrays of n0,
+// n1 and the remaining columns (NULL: dropped). A block has 32 columns, 32 threads a column
+// add up every 32nd row, then a tree of fixed order.
+struct ColumnSum {
+  const float* partial;
+  int rows;
+  int64_t cols, n0, n1;
+  float *out0, *out1, *out2;
+};
+static __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSum a) {
+  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
+  float s = 0.0f;
+  if (c < a.cols) {
+#pragma unroll 4
+    for (int r = threadIdx.x / 32; r < a.rows; r += 32) s += a.partial[r * a.cols + c];
+  }
+  __shared__ float part[1024];
+  part[threadIdx.x] = s;
+#pragma unroll
+  for (int step = 512; step >= 32; step /= 2) {
+    __syncthreads();
+    if (threadIdx.x < step) part[threadIdx.x] += part[threadIdx.x + step];
+  }
+  if (threadIdx.x < 32 && c < a.cols) {
+    float* out = c < a.n0 ? a.out0 : c < a.n0 + a.n1 ? a.out1 : a.out2;
+    if (out != nullptr) out[c < a.n0 ? c : c < a.n0 + a.n1 ? c - a.n0 : c - a.n0 - a.n1] = part[threadIdx.x];
+  }
+}
+inline int launch_column_sum(const ColumnSum& a, hipStream_t s) {
+  column_sum_kernel<<<unsigned((a.cols + 31) / 32), 1024, 0, s>>>(a);
+  return int(hipGetLastError());
+}
+
+}  // namespace gdn

@@ -441,6 +441,192 @@ size_t gdn_gated_norm_bwd_workspace_bytes(const gdn_gated_norm_args* args);
 int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_grads* grads, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* ---- Gated recurrence a channel ----------------------------------------------------------
+ *
+ * A state of one number a channel instead of a matrix a head:
+ *
+ *     h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t,     elementwise over C channels
+ *
+ *   LOG      a = e^f (f <= 0; above 0 is not checked and grows the state), m = 1
+ *   SIGMOID  a = sigmoid(f), m = 1 - a
+ *   POWER    a = e^{-decay_c sigmoid(f)} (decay [C] >= 0), m = sqrt(1 - a^2)
+ * and without i its factor is 1. 1 - a is computed as it is, not as a difference, so that
+ * channels that keep many tokens keep their last bits.
+ *   x, f, i      [B, T, C], C a multiple of 8; views of a larger array by *_stride as for the
+ *                linear entry points (at least C elements from token to token)
+ *   h            [B, T, C], contiguous, in the inputs' type; must not overlap an input
+ *   seq_lens     as for the linear entry points: rows of h behind a length stay as they were
+ *   h0, h_final  [B, C] float32
+ *   checkpoints  [B, ceil(T / GDN_SCAN_SPAN), C] float32: the state before every span of
+ *                GDN_SCAN_SPAN tokens (spans behind a length: not written). The forward pass
+ *                writes them if given; the gradients read them if given, and otherwise run
+ *                over x, f and i once more to get them.
+ * GDN_ERR_UNSUPPORTED above C = 2^16, B * C = 2^24, and the limits of B, T, B * T and strides
+ * of the linear entry points. The state is float32; a sequence's tokens are joined in a
+ * fixed tree. A NaN or Inf in row t makes its channel of h NaN or Inf from t on, until a row
+ * of a = 0 or beyond (0 times NaN is NaN), and nothing else. */
+enum gdn_scan_gate { GDN_SCAN_LOG = 1, GDN_SCAN_SIGMOID = 2, GDN_SCAN_POWER = 3 };
+#define GDN_SCAN_SPAN 64
+
+typedef struct gdn_scan_args {
+  int32_t dtype;     /* enum gdn_dtype: x, f, i and h  */
+  int32_t gate;      /* enum gdn_scan_gate             */
+  int64_t B, T, C;   /* T >= 0                         */
+  int64_t x_stride, f_stride, i_stride;
+  const void* x;
+  const void* f;
+  const void* i;        /* NULL: no input gate         */
+  const float* decay;   /* [C], POWER only             */
+  const int32_t* seq_lens;
+  const float* h0;      /* NULL means zero; ignored by the step               */
+  float* h_final;       /* NULL: not written; may alias h0; ignored by the step */
+  float* checkpoints;   /* ignored by the step         */
+  void* h;
+} gdn_scan_args;
+
+/* Bytes of device workspace gdn_gated_scan_fwd needs (0 for an invalid set). */
+size_t gdn_gated_scan_workspace_bytes(const gdn_scan_args* args);
+
+/* h for every token and the state after the last one. ws must hold
+ * gdn_gated_scan_workspace_bytes(args) bytes, 256-byte aligned. */
+int gdn_gated_scan_fwd(const gdn_scan_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* The recurrence token by token on state_inout ([B, C] float32, in place): T = 1 is one
+ * decode step. A sequence of length 0 keeps its state and its row of h. No workspace. */
+int gdn_gated_scan_step(const gdn_scan_args* args, float* state_inout, void* stream);
+
+/* Gradient outputs of gdn_gated_scan_bwd: dx, df, di [B, T, C] contiguous in args->dtype
+ * (di NULL without i), zero behind a sequence's length; ddecay [C] float32 (POWER only;
+ * NULL: not written) and dh0 [B, C] float32 (NULL: not written). None may overlap an input. */
+typedef struct gdn_scan_grads {
+  void* dx;
+  void* df;
+  void* di;
+  float* ddecay;
+  float* dh0;
+} gdn_scan_grads;
+
+/* Bytes of device workspace gdn_gated_scan_bwd needs (0 for an invalid set). */
+size_t gdn_gated_scan_bwd_workspace_bytes(const gdn_scan_args* args);
+
+/* Gradients of h and h_final: with d_h [B, T, C] in args->dtype (contiguous; rows behind a
+ * length are not used) and d_h_final [B, C] float32 (NULL: zero),
+ *     l_n = d_h_n + d_h_final,  l_t = d_h_t + a_{t+1} l_{t+1},
+ *     d a_t = l_t h_{t-1},  d (m sigmoid(i) x)_t = l_t,  dh0 = a_1 l_1,
+ * h recomputed in float32. args->h and args->h_final are ignored. In POWER, m has no slope
+ * at a = 1 (decay or sigmoid(f) 0): its part is taken as 0 there, the limit for f. The sums
+ * for ddecay run in a fixed order. */
+int gdn_gated_scan_bwd(const gdn_scan_args* args, const void* d_h, const float* d_h_final, const gdn_scan_grads* grads,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Short causal convolution a channel ----------------------------------------------------
+ *
+ *     z_t = bias + sum_{j < W} w[c][j] x_{t - W + 1 + j},     y_t = z_t / (1 + e^{-z_t}) or z_t
+ *
+ * what mixes a few neighbouring tokens before a recurrence's inputs. The rows before the
+ * first token are those of a state, the last W - 1 inputs so far, oldest first.
+ *   x, y             [B, T, C], C a multiple of 8; x a view by x_stride, y contiguous and not
+ *                    overlapping x
+ *   w                [C, W] float32, bias [C] float32 (NULL: zero)
+ *   seq_lens         as above: rows of y behind a length stay as they were
+ *   s0, s_final      [B, W - 1, C] in the inputs' type
+ * Limits as for the gated recurrence. A NaN or Inf in a row reaches the W rows that read it. */
+typedef struct gdn_conv_args {
+  int32_t dtype;       /* enum gdn_dtype: x, y and the states  */
+  int32_t activation;  /* 0: none, or GDN_ACT_SILU             */
+  int64_t B, T, C;
+  int64_t W;           /* 2, 3 or 4                            */
+  int64_t x_stride;
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* seq_lens;
+  const void* s0;      /* NULL means zero; ignored by the step                 */
+  void* s_final;       /* NULL: not written; may alias s0; ignored by the step */
+  void* y;
+} gdn_conv_args;
+
+/* y for every token, and the state after the last one. No workspace. */
+int gdn_short_conv_fwd(const gdn_conv_args* args, void* stream);
+
+/* The same with one state, read and then replaced ([B, W - 1, C] in args->dtype). */
+int gdn_short_conv_step(const gdn_conv_args* args, void* state_inout, void* stream);
+
+/* Gradient outputs of gdn_short_conv_bwd: dx [B, T, C] contiguous and ds0 [B, W - 1, C]
+ * (NULL: not written) in args->dtype, zero behind a sequence's length; dw [C, W] and dbias
+ * [C] float32 (NULL: not written). None may overlap an input. */
+typedef struct gdn_conv_grads {
+  void* dx;
+  float* dw;
+  float* dbias;
+  void* ds0;
+} gdn_conv_grads;
+
+/* Bytes of device workspace gdn_short_conv_bwd needs (0 for an invalid set). */
+size_t gdn_short_conv_bwd_workspace_bytes(const gdn_conv_args* args);
+
+/* Gradients of y and s_final: d_y [B, T, C] in args->dtype (contiguous; rows behind a length
+ * are not used), d_s_final [B, W - 1, C] in args->dtype (NULL: zero). args->y and
+ * args->s_final are ignored. The sums for dw and dbias run in a fixed order. */
+int gdn_short_conv_bwd(const gdn_conv_args* args, const void* d_y, const void* d_s_final, const gdn_conv_grads* grads,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Norms around a block, with its gate and residual scale ---------------------------------
+ *
+ * What stands between one block's output y and the next block's input, in one pass:
+ *     u  = y (sum y^2 / C + eps)^{-1/2} post_weight   (post_norm), or y
+ *     r' = residual_scale r + scale act(gate) u
+ *     n  = r' (sum r'^2 / C + eps)^{-1/2} weight
+ * with r the residual stream; the sums and n are of r' before it is rounded.
+ *   r, residual_out   [B, T, C] in residual_dtype; C a multiple of 8 up to 16,384
+ *   y, gate, out      [B, T, C] in dtype. gate NULL: act(gate) is 1. y NULL (then gate, scale and
+ *                     post_weight are NULL and post_norm 0): u = 0, the norm before a first block
+ *   scale, post_weight, weight   [C] float32, NULL means ones
+ * r, y and gate may be views by their strides; residual_out and out are contiguous, at least
+ * one is given, and each may be r, y or gate itself where that is contiguous and of its type.
+ * Other limits as for the gated recurrence. */
+typedef struct gdn_block_norm_args {
+  int32_t dtype;           /* enum gdn_dtype: y, gate, out                            */
+  int32_t residual_dtype;  /* GDN_DTYPE_F32 or dtype: r, residual_out                 */
+  int32_t activation;      /* enum gdn_activation (of the gate)                       */
+  int32_t post_norm;       /* 0 or 1                                                  */
+  int64_t B, T, C;
+  int64_t r_stride, y_stride, gate_stride;
+  float eps;               /* >= 0 */
+  float residual_scale;
+  const void* r;
+  const void* y;
+  const void* gate;
+  const float* scale;
+  const float* post_weight;
+  const float* weight;
+  void* residual_out;
+  void* out;
+} gdn_block_norm_args;
+
+int gdn_block_norm_fwd(const gdn_block_norm_args* args, void* stream);
+
+/* Gradients: d_residual_out (residual_dtype) and d_out (dtype), contiguous, at least one of
+ * them given (NULL: zero), in; dr (residual_dtype), dy and dgate (dtype), contiguous, NULL:
+ * not written, and dscale, dpost_weight, dweight [C] float32 (NULL: not written) out. What an
+ * absent input would have as a gradient must be NULL. args->residual_out and out are ignored;
+ * dr may be d_residual_out. The weight sums run in a fixed order. */
+typedef struct gdn_block_norm_grads {
+  const void* d_residual_out;
+  const void* d_out;
+  void* dr;
+  void* dy;
+  void* dgate;
+  float* dscale;
+  float* dpost_weight;
+  float* dweight;
+} gdn_block_norm_grads;
+
+/* Bytes of device workspace gdn_block_norm_bwd needs (0 for an invalid set). */
+size_t gdn_block_norm_bwd_workspace_bytes(const gdn_block_norm_args* args);
+int gdn_block_norm_bwd(const gdn_block_norm_args* args, const gdn_block_norm_grads* grads, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* Static text for a status code. */
 const char* gdn_status_str(int status);
 
