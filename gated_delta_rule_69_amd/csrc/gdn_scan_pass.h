@@ -27,8 +27,8 @@ constexpr int kSpan = GDN_SCAN_SPAN;
 constexpr int kLanes = 8;              // lanes across a slice's channels
 constexpr int kRuns = 64 / kLanes;     // lane groups, a run of tokens each
 constexpr int kRun = kSpan / kRuns;    // tokens a run
-constexpr int kWaves = 4;              // waves a workgroup: spans a tile
-constexpr int kTile = kWaves * kSpan;
+constexpr int kWaves = 16;             // waves a workgroup of the forward pass: spans a tile
+constexpr int kBackWaves = 8;          // and of the gradients
 
 template <typename E> struct Shape {
   static constexpr int V = 4 / sizeof(E);   // channels a lane
@@ -113,7 +113,7 @@ struct Pass {
   float *h_final, *marks;
   void* h;
   int64_t ldx, ldf, ldi, T, C;
-  int64_t seg;          // tokens a segment, a multiple of kTile
+  int64_t seg;          // tokens a segment, a multiple of a tile
   unsigned slices, segs, blocks;
   float* start;         // [B][C]: h0, where segments run side by side
   Run* totals;          // [B][segs - 1][C]
@@ -124,18 +124,19 @@ struct Pass {
   float *dh0, *ddecay;  // ddecay: [B * segs][C] partial sums
 };
 
-// Rows base + r ld of a run of tokens, four bytes a lane: from a span's first row at a lane's
-// channel, `left` (>= 1) tokens of it present; those behind them repeat the last.
-__device__ __forceinline__ void load_run(uint32_t* out, const char* base, int64_t ld, int run, int64_t left) {
+// Rows of a run of tokens, four bytes a lane: `base` is a span's first row at a slice's first
+// channel, `at` the lane's channel in bytes. `left` (>= 1) tokens of the span are present; those
+// behind them repeat the last.
+__device__ __forceinline__ void load_run(uint32_t* out, const char* base, int64_t ld, int run, uint32_t at, int64_t left) {
   if (left >= kSpan) {
-    const uint32_t off = uint32_t(run * kRun) * uint32_t(ld);
+    const uint32_t off = uint32_t(run * kRun) * uint32_t(ld) + at;
 #pragma unroll
     for (int r = 0; r < kRun; ++r) out[r] = *reinterpret_cast<const uint32_t*>(base + r * ld + off);
   } else {
 #pragma unroll
     for (int r = 0; r < kRun; ++r) {
       const int row = run * kRun + r;
-      out[r] = *reinterpret_cast<const uint32_t*>(base + (row < left ? row : left - 1) * ld);
+      out[r] = *reinterpret_cast<const uint32_t*>(base + (row < left ? row : left - 1) * ld + at);
     }
   }
 }
@@ -145,13 +146,18 @@ __device__ __forceinline__ float part_of(uint32_t raw, int v) {
   return v == 0 ? __uint_as_float(raw << 16) : __uint_as_float(raw & 0xffff0000u);
 }
 template <typename E>
-__device__ __forceinline__ void store_parts(char* at, const float* x) {
+__device__ __forceinline__ uint32_t packed(const float* x) {
   if constexpr (sizeof(E) == 4) {
-    *reinterpret_cast<float*>(at) = x[0];
+    return __float_as_uint(x[0]);
   } else {
-    bhalf2 r = {E(x[0]), E(x[1])};
-    *reinterpret_cast<bhalf2*>(at) = r;
+    const bhalf2 r = {E(x[0]), E(x[1])};
+    return __builtin_bit_cast(uint32_t, r);
   }
+}
+// Row r of a run goes to `base` (a span's first row) where it is present and the lane has channels.
+__device__ __forceinline__ void store_row(char* base, int64_t ld, int run, int r, uint32_t at, int64_t left, bool own, uint32_t x) {
+  const uint32_t off = uint32_t(run * kRun) * uint32_t(ld) + at;
+  if (own && run * kRun + r < left) *reinterpret_cast<uint32_t*>(base + r * ld + off) = x;
 }
 
 // Where a workgroup stands: blocks that follow each other on one XCD (their index modulo 8)
@@ -169,23 +175,25 @@ struct Place {
   }
 };
 
-// The runs of a tile's waves through LDS: joined up to this wave, and in all.
-template <int V, bool BACK>
-__device__ __forceinline__ void pass_waves(float4 (*part)[kLanes * V], int wave, int lane, const Run* own, State* carry,
-                                           float* in) {
+// The runs of a tile's waves through LDS, in order: `all` of them joined, and `mine`, those
+// before this wave's.
+template <int V, int NW, bool BACK>
+__device__ __forceinline__ void join_waves(float4 (*part)[kLanes * V], int wave, int lane, const Run* own, Run* mine, Run* all) {
   if (lane / kLanes == (BACK ? 0 : kRuns - 1)) {
 #pragma unroll
     for (int v = 0; v < V; ++v) part[wave][(lane % kLanes) * V + v] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
   }
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+  for (int v = 0; v < V; ++v) mine[v] = all[v] = empty_run();
+#pragma unroll 2   // all at once would hold every wave's runs in registers
+  for (int j = 0; j < NW; ++j) {
+    const int w = BACK ? NW - 1 - j : j;
 #pragma unroll
-    for (int j = 0; j < kWaves; ++j) {
-      const int w = BACK ? kWaves - 1 - j : j;
-      if (w == wave) in[v] = carry[v].value();
+    for (int v = 0; v < V; ++v) {
+      if (w == wave) mine[v] = all[v];
       const float4 t = part[w][(lane % kLanes) * V + v];
-      carry[v].pass({t.x, t.y, t.z});
+      all[v] = join(all[v], {t.x, t.y, t.z});
     }
   }
 }
@@ -211,57 +219,65 @@ __device__ __forceinline__ void join_lanes(Run* own, Run* before, int lane) {
   }
 }
 
-// Forward. TOTALS: only what each segment but the last makes of the state before it.
+// Forward. TOTALS: only what each segment but the last makes of the state before it. A tile's
+// rows are loaded while the one before it is joined and written.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N;
+  constexpr int V = Shape<E>::V, N = Shape<E>::N, kTile = kWaves * kSpan;
   __shared__ float4 part[2][kWaves][N];
   const Place at(p, TOTALS ? p.segs - 1 : p.segs);
   const int lane = threadIdx.x % 64, run = lane / kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t c_all = int64_t(at.slice) * N + (lane % kLanes) * V;
-  const bool own = c_all < p.C;
-  const int64_t c = own ? c_all : p.C - V;   // of a slice that ends behind C
+  const int64_t c0 = int64_t(at.slice) * N;
+  const bool own = c0 + (lane % kLanes) * V < p.C;
+  const uint32_t ch = own ? (lane % kLanes) * V : uint32_t(p.C - V - c0);   // of a slice that ends behind C
+  const uint32_t off = ch * sizeof(E);
+  const int64_t c = at.b * p.C + c0 + ch;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   if (begin >= n && at.seg > 0) return;
   const bool last = n - begin <= p.seg;
   if (TOTALS && at.seg == 0 && wave == 0 && run == 0 && own) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.start[at.b * p.C + c + v] = p.h0 != nullptr ? p.h0[at.b * p.C + c + v] : 0.0f;
+    for (int v = 0; v < V; ++v) p.start[c + v] = p.h0 != nullptr ? p.h0[c + v] : 0.0f;
   }
   if (TOTALS && last) return;
   const int64_t end = last ? n : begin + p.seg;
+  const int64_t ldh = p.C * sizeof(E);
+  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c0 * sizeof(E);
+  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c0 * sizeof(E);
+  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c0 * sizeof(E);
+  char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * sizeof(E);
+  uint32_t rx[kRun], rf[kRun], ri[kRun];
+  auto fetch = [&](int64_t t0) {
+    const int64_t left = end - t0;
+    if (left <= 0) return;
+    load_run(rx, x + t0 * p.ldx, p.ldx, run, off, left);
+    load_run(rf, f + t0 * p.ldf, p.ldf, run, off, left);
+    if constexpr (IG) load_run(ri, g + t0 * p.ldi, p.ldi, run, off, left);
+  };
+  fetch(begin + wave * kSpan);
   float decay[V];
   State carry[V];
-  float A_all[V], C_all[V];
+  Run total[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c + v] : 0.0f;
+    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c0 + ch + v] : 0.0f;
     const float* from = p.segs > 1 ? p.start : p.h0;
-    carry[v] = {TOTALS || from == nullptr ? 0.0f : from[at.b * p.C + c + v], 0.0f};
+    carry[v] = {TOTALS || from == nullptr ? 0.0f : from[c + v], 0.0f};
     if constexpr (!TOTALS) {
-      for (unsigned s = 0; s < at.seg; ++s) carry[v].pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c + v]);
+      for (unsigned s = 0; s < at.seg; ++s) carry[v].pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + ch + v]);
     }
-    A_all[v] = 1.0f, C_all[v] = 0.0f;
+    total[v] = empty_run();
   }
-  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c * sizeof(E);
-  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c * sizeof(E);
-  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c * sizeof(E);
-  const int64_t ldh = p.C * sizeof(E);
-  char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c * sizeof(E);
   int buf = 0;
   for (int64_t tile = begin; tile < end; tile += kTile, buf ^= 1) {
     const int64_t t0 = tile + wave * kSpan, left = end - t0;
     float a[kRun][V], b[kRun][V];
-    Run own_run[V], before[V];
+    Run own_run[V], before[V], mine[V], all[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) own_run[v] = empty_run();
     if (left > 0) {
-      uint32_t rx[kRun], rf[kRun], ri[kRun];
-      load_run(rx, x + t0 * p.ldx, p.ldx, run, left);
-      load_run(rf, f + t0 * p.ldf, p.ldf, run, left);
-      if constexpr (IG) load_run(ri, g + t0 * p.ldi, p.ldi, run, left);
 #pragma unroll
       for (int r = 0; r < kRun; ++r) {
         const bool here = run * kRun + r < left;
@@ -276,31 +292,27 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
         }
       }
     }
+    fetch(t0 + kTile);
     join_lanes<V, false>(own_run, before, lane);
-    float in[V];
+    join_waves<V, kWaves, false>(part[buf], wave, lane, own_run, mine, all);
     if constexpr (TOTALS) {
-      // the whole segment's A and C: joined like a state's, from the same parts
-      if (run == kRuns - 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          part[buf][wave][(lane % kLanes) * V + v] = make_float4(own_run[v].A, own_run[v].C, own_run[v].H, 0.0f);
-      }
-      __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float4 t = part[buf][w][(lane % kLanes) * V + v];
-          carry[v].pass({t.x, t.y, t.z});
-          C_all[v] = fmaf(t.y, A_all[v], C_all[v]);
-          A_all[v] *= t.x;
-        }
+        carry[v].pass(all[v]);
+        total[v] = join(total[v], all[v]);
       }
     } else {
-      pass_waves<V, false>(part[buf], wave, lane, own_run, carry, in);
+      float in[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        State s = carry[v];
+        s.pass(mine[v]);
+        in[v] = s.value();
+        carry[v].pass(all[v]);
+      }
       if (left > 0) {
         if (p.marks != nullptr && run == 0 && own) {
-          float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c;
+          float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
 #pragma unroll
           for (int v = 0; v < V; ++v) m[v] = in[v];
         }
@@ -312,22 +324,20 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
           for (int r = 0; r < kRun; ++r) {
 #pragma unroll
             for (int v = 0; v < V; ++v) y[v] = fmaf(a[r][v], y[v], b[r][v]);
-            const int row = run * kRun + r;
-            if (own && row < left) store_parts<E>(h + (t0 + row) * ldh, y);
+            store_row(h + t0 * ldh, ldh, run, r, off, left, own, packed<E>(y));
           }
         }
       }
     }
   }
+  if (wave != 0 || run != 0 || !own) return;
   if constexpr (TOTALS) {
-    if (wave == 0 && run == 0 && own) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c + v] = {A_all[v], C_all[v], carry[v].value()};
-    }
-  } else if (last && p.h_final != nullptr && wave == 0 && run == 0 && own) {
+    for (int v = 0; v < V; ++v)
+      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch + v] = {total[v].A, total[v].C, carry[v].value()};
+  } else if (last && p.h_final != nullptr) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.h_final[at.b * p.C + c + v] = carry[v].value();
+    for (int v = 0; v < V; ++v) p.h_final[c + v] = carry[v].value();
   }
 }
 
@@ -335,84 +345,101 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
 // value behind token t is l_t = d_h_t + G_{t+1}. h comes from the state before the span. TOTALS:
 // only what each segment but the first makes of the gradient behind it.
 template <typename E, int KIND, bool IG, bool TOTALS>
-__global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N;
-  __shared__ float4 part[2][kWaves][N];
+__global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
+  constexpr int V = Shape<E>::V, N = Shape<E>::N, kTile = kBackWaves * kSpan;
+  __shared__ float4 part[2][kBackWaves][N];
   Place at(p, TOTALS ? p.segs - 1 : p.segs);
   if (TOTALS) ++at.seg;
   const int lane = threadIdx.x % 64, run = lane / kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t c_all = int64_t(at.slice) * N + (lane % kLanes) * V;
-  const bool own = c_all < p.C;
-  const int64_t c = own ? c_all : p.C - V;
+  const int64_t c0 = int64_t(at.slice) * N;
+  const bool own = c0 + (lane % kLanes) * V < p.C;
+  const uint32_t ch = own ? (lane % kLanes) * V : uint32_t(p.C - V - c0);
+  const uint32_t off = ch * sizeof(E);
+  const int64_t c = at.b * p.C + c0 + ch;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
   const int64_t ldh = p.C * sizeof(E);
-  char* dx = static_cast<char*>(p.dx) + at.b * p.T * ldh + c * sizeof(E);
-  char* df = static_cast<char*>(p.df) + at.b * p.T * ldh + c * sizeof(E);
-  char* di = static_cast<char*>(p.di) + at.b * p.T * ldh + c * sizeof(E);
+  char* dx = static_cast<char*>(p.dx) + at.b * p.T * ldh + c0 * sizeof(E);
+  char* df = static_cast<char*>(p.df) + at.b * p.T * ldh + c0 * sizeof(E);
+  char* di = static_cast<char*>(p.di) + at.b * p.T * ldh + c0 * sizeof(E);
   if constexpr (!TOTALS) {
     // rows behind the length: zero
-    const float zero[V] = {};
-    for (int64_t t = std::max(begin, n) + wave * kRuns + run; t < stop; t += kWaves * kRuns) {
+    for (int64_t t = std::max(begin, n) + wave * kRuns + run; t < stop; t += kBackWaves * kRuns) {
       if (!own) break;
-      store_parts<E>(dx + t * ldh, zero), store_parts<E>(df + t * ldh, zero);
-      if constexpr (IG) store_parts<E>(di + t * ldh, zero);
+      *reinterpret_cast<uint32_t*>(dx + t * ldh + off) = 0, *reinterpret_cast<uint32_t*>(df + t * ldh + off) = 0;
+      if constexpr (IG) *reinterpret_cast<uint32_t*>(di + t * ldh + off) = 0;
     }
   }
   if (TOTALS && begin >= n) return;
+  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c0 * sizeof(E);
+  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c0 * sizeof(E);
+  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c0 * sizeof(E);
+  const char* d = static_cast<const char*>(p.d_h) + at.b * p.T * ldh + c0 * sizeof(E);
+  struct Rows {
+    uint32_t x[kRun], f[kRun], i[kRun], d[kRun];
+  } next;
+  auto fetch = [&](int64_t t0) {
+    const int64_t left = end - t0;
+    if (left <= 0) return;
+    load_run(next.f, f + t0 * p.ldf, p.ldf, run, off, left);
+    load_run(next.d, d + t0 * ldh, ldh, run, off, left);
+    if constexpr (!TOTALS) {
+      load_run(next.x, x + t0 * p.ldx, p.ldx, run, off, left);
+      if constexpr (IG) load_run(next.i, g + t0 * p.ldi, p.ldi, run, off, left);
+    }
+  };
+  const int64_t tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+  int64_t tile = begin + (tiles - 1) * kTile;
+  if (tiles > 0) fetch(tile + wave * kSpan);
   float decay[V], sum[V];
   State carry[V];
-  float A_all[V], C_all[V];
+  Run total[V];
   const int64_t segs_used = (n + p.seg - 1) / p.seg;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c + v] : 0.0f;
-    carry[v] = {TOTALS || p.d_final == nullptr ? 0.0f : p.d_final[at.b * p.C + c + v], 0.0f};
+    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c0 + ch + v] : 0.0f;
+    carry[v] = {TOTALS || p.d_final == nullptr ? 0.0f : p.d_final[c + v], 0.0f};
     if constexpr (!TOTALS) {
-      for (int64_t s = segs_used - 1; s > int64_t(at.seg); --s) carry[v].pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c + v]);
+      for (int64_t s = segs_used - 1; s > int64_t(at.seg); --s)
+        carry[v].pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + ch + v]);
     }
-    A_all[v] = 1.0f, C_all[v] = 0.0f, sum[v] = 0.0f;
+    total[v] = empty_run(), sum[v] = 0.0f;
   }
-  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c * sizeof(E);
-  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c * sizeof(E);
-  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c * sizeof(E);
-  const char* d = static_cast<const char*>(p.d_h) + at.b * p.T * ldh + c * sizeof(E);
   int buf = 0;
-  const int64_t tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
-  for (int64_t tile = begin + (tiles - 1) * kTile; tile >= begin && tiles > 0; tile -= kTile, buf ^= 1) {
+  for (int64_t k = 0; k < tiles; ++k, tile -= kTile, buf ^= 1) {
     const int64_t t0 = tile + wave * kSpan, left = end - t0;
-    uint32_t rx[kRun], rf[kRun], ri[kRun], rd[kRun];
-    float a[kRun][V], before[kRun][V];
-    Run own_run[V], lanes[V];
+    const Rows now = next;
+    Gate gate[kRun][V];
+    float si[kRun][V], resti[kRun][V], before[kRun][V];
+    Run own_run[V], lanes[V], mine[V], all[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) own_run[v] = empty_run();
     if (left > 0) {
-      load_run(rf, f + t0 * p.ldf, p.ldf, run, left);
-      load_run(rd, d + t0 * ldh, ldh, run, left);
-      if constexpr (!TOTALS) {
-        load_run(rx, x + t0 * p.ldx, p.ldx, run, left);
-        if constexpr (IG) load_run(ri, g + t0 * p.ldi, p.ldi, run, left);
-      }
       // G of the run, from its last token
 #pragma unroll
       for (int r = kRun - 1; r >= 0; --r) {
         const bool here = run * kRun + r < left;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const Gate t = gate_of<E, KIND>(part_of<E>(rf[r], v), decay[v]);
-          a[r][v] = here ? t.a : 1.0f;
-          const float up = here ? part_of<E>(rd[r], v) : 0.0f;
-          own_run[v] = join(own_run[v], Run{a[r][v], here ? t.c : 0.0f, a[r][v] * up});
+          Gate& t = gate[r][v];
+          t = gate_of<E, KIND>(part_of<E>(now.f[r], v), decay[v]);
+          t.a = here ? t.a : 1.0f;
+          const float up = here ? part_of<E>(now.d[r], v) : 0.0f;
+          own_run[v] = join(own_run[v], Run{t.a, here ? t.c : 0.0f, t.a * up});
           if constexpr (!TOTALS) {
-            float add = t.m * part_of<E>(rx[r], v);
-            if constexpr (IG) add *= sigmoid_of<E>(part_of<E>(ri[r], v));
+            float add = t.m * part_of<E>(now.x[r], v);
+            if constexpr (IG) {
+              sigmoids<E>(part_of<E>(now.i[r], v), &si[r][v], &resti[r][v]);
+              add *= si[r][v];
+            }
             before[r][v] = here ? add : 0.0f;
           }
         }
       }
     }
+    if (k + 1 < tiles) fetch(t0 - kTile);
     if constexpr (!TOTALS) {
       // h before each token: from what each adds
       Run fwd[V], ahead[V];
@@ -421,12 +448,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
         fwd[v] = empty_run();
         if (left > 0) {
 #pragma unroll
-          for (int r = 0; r < kRun; ++r) fwd[v] = join(fwd[v], Run{a[r][v], 0.0f, before[r][v]});
+          for (int r = 0; r < kRun; ++r) fwd[v] = join(fwd[v], Run{gate[r][v].a, 0.0f, before[r][v]});
         }
       }
       join_lanes<V, false>(fwd, ahead, lane);
       if (left > 0) {
-        const float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c;
+        const float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float y = fmaf(ahead[v].A, m[v], ahead[v].H);
@@ -434,51 +461,41 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
           for (int r = 0; r < kRun; ++r) {
             const float add = before[r][v];
             before[r][v] = y;
-            y = fmaf(a[r][v], y, add);
+            y = fmaf(gate[r][v].a, y, add);
           }
         }
       }
     }
     join_lanes<V, true>(own_run, lanes, lane);
-    float in[V];
+    join_waves<V, kBackWaves, true>(part[buf], wave, lane, own_run, mine, all);
     if constexpr (TOTALS) {
-      if (run == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          part[buf][wave][(lane % kLanes) * V + v] = make_float4(own_run[v].A, own_run[v].C, own_run[v].H, 0.0f);
-      }
-      __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-          const float4 t = part[buf][w][(lane % kLanes) * V + v];
-          carry[v].pass({t.x, t.y, t.z});
-          C_all[v] = fmaf(t.y, A_all[v], C_all[v]);
-          A_all[v] *= t.x;
-        }
+        carry[v].pass(all[v]);
+        total[v] = join(total[v], all[v]);
       }
     } else {
-      pass_waves<V, true>(part[buf], wave, lane, own_run, carry, in);
-      if (left > 0) {
-        float G[V];
+      float G[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) G[v] = fmaf(lanes[v].A, in[v], lanes[v].H);
+      for (int v = 0; v < V; ++v) {
+        State s = carry[v];
+        s.pass(mine[v]);
+        G[v] = fmaf(lanes[v].A, s.value(), lanes[v].H);
+        carry[v].pass(all[v]);
+      }
+      if (left > 0) {
 #pragma unroll
         for (int r = kRun - 1; r >= 0; --r) {
           float ox[V], of[V], oi[V];
-          const int row = run * kRun + r;
-          const bool here = row < left;
+          const bool here = run * kRun + r < left;
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const Gate t = gate_of<E, KIND>(part_of<E>(rf[r], v), decay[v]);
-            const float xv = part_of<E>(rx[r], v), l = part_of<E>(rd[r], v) + G[v];
-            float s = 1.0f, rest = 0.0f;
-            if constexpr (IG) sigmoids<E>(part_of<E>(ri[r], v), &s, &rest);
-            const float lm = l * t.m;
-            ox[v] = IG ? lm * s : lm;
-            if constexpr (IG) oi[v] = ox[v] * xv * rest;
-            const float gx = IG ? s * xv : xv;
+            const Gate& t = gate[r][v];
+            const float xv = part_of<E>(now.x[r], v), l = part_of<E>(now.d[r], v) + G[v];
+            const float lm = KIND == GDN_SCAN_LOG ? l : l * t.m;
+            ox[v] = IG ? lm * si[r][v] : lm;
+            if constexpr (IG) oi[v] = ox[v] * xv * resti[r][v];
+            const float gx = IG ? si[r][v] * xv : xv;
             if constexpr (KIND == GDN_SCAN_LOG) {
               of[v] = l * before[r][v] * t.a;
             } else if constexpr (KIND == GDN_SCAN_SIGMOID) {
@@ -492,11 +509,9 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
             }
             G[v] = here ? t.a * l : G[v];
           }
-          if (own && here) {
-            store_parts<E>(dx + (t0 + row) * ldh, ox);
-            store_parts<E>(df + (t0 + row) * ldh, of);
-            if constexpr (IG) store_parts<E>(di + (t0 + row) * ldh, oi);
-          }
+          store_row(dx + t0 * ldh, ldh, run, r, off, left, own, packed<E>(ox));
+          store_row(df + t0 * ldh, ldh, run, r, off, left, own, packed<E>(of));
+          if constexpr (IG) store_row(di + t0 * ldh, ldh, run, r, off, left, own, packed<E>(oi));
         }
       }
     }
@@ -505,12 +520,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
     if (wave == 0 && run == 0 && own) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c + v] = {A_all[v], C_all[v], carry[v].value()};
+        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch + v] = {total[v].A, total[v].C, carry[v].value()};
     }
   } else {
     if (at.seg == 0 && p.dh0 != nullptr && wave == 0 && run == 0 && own) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.dh0[at.b * p.C + c + v] = carry[v].value();
+      for (int v = 0; v < V; ++v) p.dh0[c + v] = carry[v].value();
     }
     if (KIND == GDN_SCAN_POWER && p.ddecay != nullptr) {
       // over the lane groups, then the waves
@@ -527,8 +542,8 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float t = 0.0f;
-          for (int w = 0; w < kWaves; ++w) t += sums[w * N + (lane % kLanes) * V + v];
-          p.ddecay[(at.b * p.segs + at.seg) * p.C + c + v] = t;
+          for (int w = 0; w < kBackWaves; ++w) t += sums[w * N + (lane % kLanes) * V + v];
+          p.ddecay[(at.b * p.segs + at.seg) * p.C + c0 + ch + v] = t;
         }
       }
     }
@@ -600,7 +615,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     if (p.segs > 1) {
       p.blocks = unsigned(q.a.B * slices * (p.segs - 1));
       if constexpr (BACK)
-        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
+        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
       else
         scan_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
       const int rc = int(hipGetLastError());
@@ -608,7 +623,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     }
     p.blocks = unsigned(q.a.B * slices * p.segs);
     if constexpr (BACK)
-      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
+      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
     else
       scan_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
     return int(hipGetLastError());
