@@ -1,9 +1,8 @@
 // The gated recurrence a channel, h_t = a_t h_{t-1} + b_t, over long sequences: kernels and
 // their launches for one element type.
 //
-// A span of 64 tokens is a wave's: eight lanes lie across the channels of a slice, four bytes
-// a lane and row, and eight groups of lanes hold eight consecutive tokens each. A lane joins
-// its eight tokens, the groups join theirs by shuffles, the waves of a workgroup theirs
+// Eight lanes of a wave lie across the channels of a slice, four bytes a lane and row, and eight
+// groups of lanes hold a run of consecutive tokens each. A lane joins the tokens of its run, the groups join theirs by shuffles, the waves of a workgroup theirs
 // through LDS, and the workgroup walks the tiles of its segment with the state it carries.
 // Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no division, so a decay
 // may be 0, and nothing exceeds what the recurrence itself does.
@@ -23,12 +22,12 @@
 namespace gdn {
 namespace scan {
 
-constexpr int kSpan = GDN_SCAN_SPAN;
+constexpr int kSpan = GDN_SCAN_SPAN;   // tokens between checkpoints
 constexpr int kLanes = 8;              // lanes across a slice's channels
 constexpr int kRuns = 64 / kLanes;     // lane groups, a run of tokens each
-constexpr int kRun = kSpan / kRuns;    // tokens a run
-constexpr int kWaves = 16;             // waves a workgroup of the forward pass: spans a tile
-constexpr int kBackWaves = 8;          // and of the gradients
+constexpr int kWaves = 8;              // waves a workgroup
+constexpr int kRun = kSpan / kRuns;    // tokens a run: a wave has a span
+constexpr int kTile = kWaves * kSpan;
 
 template <typename E> struct Shape {
   static constexpr int V = 4 / sizeof(E);   // channels a lane
@@ -87,6 +86,10 @@ __device__ __forceinline__ Run join(const Run& first, const Run& then) {
   return {first.A * then.A, fmaf(then.C, first.A, first.C), fmaf(then.A, first.H, then.H)};
 }
 
+// The product of a run's rounded a's is off by a step for each of them, 1 - C by one: where a run
+// leaves more than half, that is its A.
+__device__ __forceinline__ void settle(Run& r) { r.A = r.C < 0.5f ? 1.0f - r.C : r.A; }
+
 // A state held as hi + lo.
 struct State {
   float hi, lo;
@@ -124,21 +127,59 @@ struct Pass {
   float *dh0, *ddecay;  // ddecay: [B * segs][C] partial sums
 };
 
-// Rows of a run of tokens, four bytes a lane: `base` is a span's first row at a slice's first
-// channel, `at` the lane's channel in bytes. `left` (>= 1) tokens of the span are present; those
-// behind them repeat the last.
-__device__ __forceinline__ void load_run(uint32_t* out, const char* base, int64_t ld, int run, uint32_t at, int64_t left) {
-  if (left >= kSpan) {
-    const uint32_t off = uint32_t(run * kRun) * uint32_t(ld) + at;
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) out[r] = *reinterpret_cast<const uint32_t*>(base + r * ld + off);
-  } else {
-#pragma unroll
-    for (int r = 0; r < kRun; ++r) {
-      const int row = run * kRun + r;
-      out[r] = *reinterpret_cast<const uint32_t*>(base + (row < left ? row : left - 1) * ld + at);
-    }
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
+// A buffer of `rows` rows of `width` bytes from `base` on, `ld` bytes apart; none for rows <= 0.
+// Loads behind its last row give zero, stores are dropped. Strides are at most 2^26 bytes, so
+// a span's offsets fit in 32 bits.
+__device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_t rows, uint32_t width) {
+  auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
+  const uint64_t from = reinterpret_cast<uintptr_t>(base);
+  const uint32_t bytes = rows > 0 ? uint32_t(rows < kSpan ? rows - 1 : kSpan - 1) * uint32_t(ld) + width : 0u;
+  return {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(bytes), 0x00020000u};
+}
+
+// Rows on their way from memory to LDS, two tiles ahead of their use: 32 bytes a row of a slice,
+// a wave's own span, so that nothing but its own count of loads says when they are there. Lane l
+// of a load brings sixteen bytes to the wave's place 16 l: row (l / 2 % 8) * 8 + l / 16 (and four
+// on), so that the eight runs' rows r lie side by side and a lane reads its own at 256 r + 4 l,
+// free of bank conflicts. The loads are written as assembly, which has no registers to guard;
+// the compiler's own counts only ever wait for more.
+struct Feed {
+  uint32_t off[4];
+  int64_t ld[4];
+  const char* base[4];
+  __device__ __forceinline__ void open(int k, const void* p, int64_t ld_, int64_t first, int lane) {
+    base[k] = static_cast<const char*>(p) + first, ld[k] = ld_;
+    off[k] = uint32_t((lane / 2 % 8) * 8 + lane / 16) * uint32_t(ld_) + lane % 2 * 16;
   }
+  __device__ __forceinline__ void load(int k, char* to, int64_t t0, int64_t left, uint32_t width) const {
+    const uint4v range = rows_from(base[k] + t0 * ld[k], ld[k], left, width);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to))));
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(off[k]), "s"(range) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds + 1024), "v"(off[k] + 4 * uint32_t(ld[k])), "s"(range) : "memory");
+  }
+};
+// Four bytes a lane, one load.
+__device__ __forceinline__ void load_words(char* to, const char* from, uint32_t bytes, int lane) {
+  const uint4v range = rows_from(from, 0, bytes > 0 ? 1 : 0, bytes);
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to))));
+  asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(lane * 4), "s"(range) : "memory");
+}
+// Waits until no more than N of the wave's loads and stores are under way, the latest ones.
+template <int N>
+__device__ __forceinline__ void wait_memory() {
+  static_assert(N < 64, "the counter has six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Before tile k: behind its LOADS loads came those of the tile after it and, from each of the two
+// tiles before, STORES stores (others only add to what is waited for).
+template <int LOADS, int STORES>
+__device__ __forceinline__ void wait_tile(int64_t k) {
+  if (STORES == 0 || k == 0) wait_memory<LOADS>();
+  else if (k == 1) wait_memory<LOADS + STORES>();
+  else wait_memory<LOADS + 2 * STORES>();
 }
 template <typename E>
 __device__ __forceinline__ float part_of(uint32_t raw, int v) {
@@ -154,10 +195,13 @@ __device__ __forceinline__ uint32_t packed(const float* x) {
     return __builtin_bit_cast(uint32_t, r);
   }
 }
-// Row r of a run goes to `base` (a span's first row) where it is present and the lane has channels.
-__device__ __forceinline__ void store_row(char* base, int64_t ld, int run, int r, uint32_t at, int64_t left, bool own, uint32_t x) {
-  const uint32_t off = uint32_t(run * kRun) * uint32_t(ld) + at;
-  if (own && run * kRun + r < left) *reinterpret_cast<uint32_t*>(base + r * ld + off) = x;
+// A run's rows, one store each: `at` is the lane's place in the span's first row, behind the
+// buffer where it has no channels.
+__device__ __forceinline__ void store_run(char* base, int64_t ld, int64_t left, uint32_t width, int run, uint32_t at, const uint32_t* x) {
+  const auto to = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(rows_from(base, ld, left, width)[2]), 0x00020000);
+#pragma unroll
+  for (int r = 0; r < kRun; ++r)
+    __builtin_amdgcn_raw_buffer_store_b32(x[r], to, at + uint32_t(run * kRun + r) * uint32_t(ld), 0, 0);
 }
 
 // Where a workgroup stands: blocks that follow each other on one XCD (their index modulo 8)
@@ -177,7 +221,7 @@ struct Place {
 
 // The runs of a tile's waves through LDS, in order: `all` of them joined, and `mine`, those
 // before this wave's.
-template <int V, int NW, bool BACK>
+template <int V, bool BACK>
 __device__ __forceinline__ void join_waves(float4 (*part)[kLanes * V], int wave, int lane, const Run* own, Run* mine, Run* all) {
   if (lane / kLanes == (BACK ? 0 : kRuns - 1)) {
 #pragma unroll
@@ -187,8 +231,8 @@ __device__ __forceinline__ void join_waves(float4 (*part)[kLanes * V], int wave,
 #pragma unroll
   for (int v = 0; v < V; ++v) mine[v] = all[v] = empty_run();
 #pragma unroll 2   // all at once would hold every wave's runs in registers
-  for (int j = 0; j < NW; ++j) {
-    const int w = BACK ? NW - 1 - j : j;
+  for (int j = 0; j < kWaves; ++j) {
+    const int w = BACK ? kWaves - 1 - j : j;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (w == wave) mine[v] = all[v];
@@ -219,19 +263,18 @@ __device__ __forceinline__ void join_lanes(Run* own, Run* before, int lane) {
   }
 }
 
-// Forward. TOTALS: only what each segment but the last makes of the state before it. A tile's
-// rows are loaded while the one before it is joined and written.
+// Forward. TOTALS: only what each segment but the last makes of the state before it.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N, kTile = kWaves * kSpan;
+  constexpr int V = Shape<E>::V, N = Shape<E>::N, NT = IG ? 3 : 2, kLoads = 2 * NT;
+  __shared__ __attribute__((aligned(16))) char raw[2][kWaves][NT][32 * kSpan];
   __shared__ float4 part[2][kWaves][N];
   const Place at(p, TOTALS ? p.segs - 1 : p.segs);
   const int lane = threadIdx.x % 64, run = lane / kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t c0 = int64_t(at.slice) * N;
-  const bool own = c0 + (lane % kLanes) * V < p.C;
-  const uint32_t ch = own ? (lane % kLanes) * V : uint32_t(p.C - V - c0);   // of a slice that ends behind C
-  const uint32_t off = ch * sizeof(E);
+  const bool own = c0 + (lane % kLanes) * V < p.C;                          // a slice may end behind C
+  const uint32_t ch = own ? (lane % kLanes) * V : 0, width = (p.C - c0 < N ? uint32_t(p.C - c0) : N) * sizeof(E);
   const int64_t c = at.b * p.C + c0 + ch;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
@@ -244,19 +287,8 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   if (TOTALS && last) return;
   const int64_t end = last ? n : begin + p.seg;
   const int64_t ldh = p.C * sizeof(E);
-  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c0 * sizeof(E);
-  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c0 * sizeof(E);
-  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c0 * sizeof(E);
   char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * sizeof(E);
-  uint32_t rx[kRun], rf[kRun], ri[kRun];
-  auto fetch = [&](int64_t t0) {
-    const int64_t left = end - t0;
-    if (left <= 0) return;
-    load_run(rx, x + t0 * p.ldx, p.ldx, run, off, left);
-    load_run(rf, f + t0 * p.ldf, p.ldf, run, off, left);
-    if constexpr (IG) load_run(ri, g + t0 * p.ldi, p.ldi, run, off, left);
-  };
-  fetch(begin + wave * kSpan);
+  const uint32_t to = own ? ch * uint32_t(sizeof(E)) : 0x80000000u;
   float decay[V];
   State carry[V];
   Run total[V];
@@ -270,31 +302,53 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
     }
     total[v] = empty_run();
   }
-  int buf = 0;
-  for (int64_t tile = begin; tile < end; tile += kTile, buf ^= 1) {
-    const int64_t t0 = tile + wave * kSpan, left = end - t0;
+  Feed feed;
+  feed.open(0, p.x, p.ldx, at.b * p.T * p.ldx + c0 * int64_t(sizeof(E)), lane);
+  feed.open(1, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
+  if constexpr (IG) feed.open(2, p.i, p.ldi, at.b * p.T * p.ldi + c0 * int64_t(sizeof(E)), lane);
+  auto fetch = [&](int stage, int64_t t0) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) feed.load(k, raw[stage][wave][k], t0, end - t0, width);
+  };
+  const int64_t first = begin + wave * kSpan, tiles = (end - begin + kTile - 1) / kTile;
+  fetch(0, first);
+  fetch(1, first + kTile);
+  // a tile whose rows are all there, or the last
+  auto walk = [&](auto full, int64_t k) {
+    constexpr bool FULL = decltype(full)::value;
+    const int stage = k & 1;
+    const int64_t t0 = first + k * kTile, left = end - t0;
+    if (!TOTALS && p.h != nullptr) wait_tile<kLoads, kRun>(k);
+    else wait_tile<kLoads, 0>(k);
+    uint32_t in[NT][kRun];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int r = 0; r < kRun; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[stage][wave][t] + 256 * r + 4 * lane);
+    }
+    wait_lds();
+    fetch(stage, t0 + 2 * kTile);
     float a[kRun][V], b[kRun][V];
     Run own_run[V], before[V], mine[V], all[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) own_run[v] = empty_run();
-    if (left > 0) {
 #pragma unroll
-      for (int r = 0; r < kRun; ++r) {
-        const bool here = run * kRun + r < left;
+    for (int r = 0; r < kRun; ++r) {
+      const bool here = FULL || run * kRun + r < left;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const Gate t = gate_of<E, KIND>(part_of<E>(rf[r], v), decay[v]);
-          float add = t.m * part_of<E>(rx[r], v);
-          if constexpr (IG) add *= sigmoid_of<E>(part_of<E>(ri[r], v));
-          a[r][v] = here ? t.a : 1.0f;
-          b[r][v] = here ? add : 0.0f;
-          own_run[v] = join(own_run[v], Run{a[r][v], here ? t.c : 0.0f, b[r][v]});
-        }
+      for (int v = 0; v < V; ++v) {
+        const Gate t = gate_of<E, KIND>(part_of<E>(in[1][r], v), decay[v]);
+        a[r][v] = here ? t.a : 1.0f;
+        b[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[0][r], v) : t.m * part_of<E>(in[0][r], v);
+        if constexpr (IG) b[r][v] *= sigmoid_of<E>(part_of<E>(in[2][r], v));
+        if (!here) b[r][v] = 0.0f;
+        own_run[v] = join(own_run[v], Run{a[r][v], here ? t.c : 0.0f, b[r][v]});
       }
     }
-    fetch(t0 + kTile);
+#pragma unroll
+    for (int v = 0; v < V; ++v) settle(own_run[v]);
     join_lanes<V, false>(own_run, before, lane);
-    join_waves<V, kWaves, false>(part[buf], wave, lane, own_run, mine, all);
+    join_waves<V, false>(part[stage], wave, lane, own_run, mine, all);
     if constexpr (TOTALS) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -302,34 +356,35 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
         total[v] = join(total[v], all[v]);
       }
     } else {
-      float in[V];
+      float y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         State s = carry[v];
         s.pass(mine[v]);
-        in[v] = s.value();
+        y[v] = fmaf(before[v].A, s.value(), before[v].H);
         carry[v].pass(all[v]);
       }
-      if (left > 0) {
-        if (p.marks != nullptr && run == 0 && own) {
-          float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
+      if (p.marks != nullptr && run == 0 && own && left > 0) {
+        float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
 #pragma unroll
-          for (int v = 0; v < V; ++v) m[v] = in[v];
+        for (int v = 0; v < V; ++v) m[v] = y[v];
+      }
+      if (p.h != nullptr) {
+        uint32_t out[kRun];
+#pragma unroll
+        for (int r = 0; r < kRun; ++r) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) y[v] = fmaf(a[r][v], y[v], b[r][v]);
+          out[r] = packed<E>(y);
         }
-        if (p.h != nullptr) {
-          float y[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) y[v] = fmaf(before[v].A, in[v], before[v].H);
-#pragma unroll
-          for (int r = 0; r < kRun; ++r) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[v] = fmaf(a[r][v], y[v], b[r][v]);
-            store_row(h + t0 * ldh, ldh, run, r, off, left, own, packed<E>(y));
-          }
-        }
+        store_run(h + t0 * ldh, ldh, left, width, run, to, out);
       }
     }
-  }
+  };
+  int64_t k = 0;
+  for (; (k + 1) * kTile <= end - begin; ++k) walk(std::true_type{}, k);
+  if (k < tiles) walk(std::false_type{}, k);
+  wait_memory<0>();   // of LDS that the next workgroup may get
   if (wave != 0 || run != 0 || !own) return;
   if constexpr (TOTALS) {
 #pragma unroll
@@ -345,54 +400,37 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
 // value behind token t is l_t = d_h_t + G_{t+1}. h comes from the state before the span. TOTALS:
 // only what each segment but the first makes of the gradient behind it.
 template <typename E, int KIND, bool IG, bool TOTALS>
-__global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N, kTile = kBackWaves * kSpan;
-  __shared__ float4 part[2][kBackWaves][N];
+__global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
+  constexpr int V = Shape<E>::V, N = Shape<E>::N, R = kRun;
+  constexpr int NT = TOTALS ? 2 : IG ? 4 : 3, kLoads = 2 * NT + (TOTALS ? 0 : 1), kStores = TOTALS ? 0 : R * (IG ? 3 : 2);
+  __shared__ __attribute__((aligned(16))) char raw[2][kWaves][NT][32 * kSpan];
+  __shared__ __attribute__((aligned(16))) char raw_marks[2][kWaves][TOTALS ? 16 : 256];
+  __shared__ float4 part[2][kWaves][N];
   Place at(p, TOTALS ? p.segs - 1 : p.segs);
   if (TOTALS) ++at.seg;
   const int lane = threadIdx.x % 64, run = lane / kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t c0 = int64_t(at.slice) * N;
   const bool own = c0 + (lane % kLanes) * V < p.C;
-  const uint32_t ch = own ? (lane % kLanes) * V : uint32_t(p.C - V - c0);
-  const uint32_t off = ch * sizeof(E);
+  const uint32_t ch = own ? (lane % kLanes) * V : 0, channels = p.C - c0 < N ? uint32_t(p.C - c0) : N;
+  const uint32_t width = channels * sizeof(E);
   const int64_t c = at.b * p.C + c0 + ch;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
-  const int64_t ldh = p.C * sizeof(E);
-  char* dx = static_cast<char*>(p.dx) + at.b * p.T * ldh + c0 * sizeof(E);
-  char* df = static_cast<char*>(p.df) + at.b * p.T * ldh + c0 * sizeof(E);
-  char* di = static_cast<char*>(p.di) + at.b * p.T * ldh + c0 * sizeof(E);
+  const int64_t ldh = p.C * sizeof(E), row0 = at.b * p.T * ldh + c0 * int64_t(sizeof(E));
+  char* dx = static_cast<char*>(p.dx) + row0;
+  char* df = static_cast<char*>(p.df) + row0;
+  char* di = static_cast<char*>(p.di) + row0;
+  const uint32_t to = own ? ch * uint32_t(sizeof(E)) : 0x80000000u;
   if constexpr (!TOTALS) {
     // rows behind the length: zero
-    for (int64_t t = std::max(begin, n) + wave * kRuns + run; t < stop; t += kBackWaves * kRuns) {
-      if (!own) break;
-      *reinterpret_cast<uint32_t*>(dx + t * ldh + off) = 0, *reinterpret_cast<uint32_t*>(df + t * ldh + off) = 0;
-      if constexpr (IG) *reinterpret_cast<uint32_t*>(di + t * ldh + off) = 0;
+    for (int64_t t = std::max(begin, n) + wave * kRuns + run; own && t < stop; t += kWaves * kRuns) {
+      *reinterpret_cast<uint32_t*>(dx + t * ldh + to) = 0, *reinterpret_cast<uint32_t*>(df + t * ldh + to) = 0;
+      if constexpr (IG) *reinterpret_cast<uint32_t*>(di + t * ldh + to) = 0;
     }
   }
   if (TOTALS && begin >= n) return;
-  const char* x = static_cast<const char*>(p.x) + at.b * p.T * p.ldx + c0 * sizeof(E);
-  const char* f = static_cast<const char*>(p.f) + at.b * p.T * p.ldf + c0 * sizeof(E);
-  const char* g = static_cast<const char*>(p.i) + at.b * p.T * p.ldi + c0 * sizeof(E);
-  const char* d = static_cast<const char*>(p.d_h) + at.b * p.T * ldh + c0 * sizeof(E);
-  struct Rows {
-    uint32_t x[kRun], f[kRun], i[kRun], d[kRun];
-  } next;
-  auto fetch = [&](int64_t t0) {
-    const int64_t left = end - t0;
-    if (left <= 0) return;
-    load_run(next.f, f + t0 * p.ldf, p.ldf, run, off, left);
-    load_run(next.d, d + t0 * ldh, ldh, run, off, left);
-    if constexpr (!TOTALS) {
-      load_run(next.x, x + t0 * p.ldx, p.ldx, run, off, left);
-      if constexpr (IG) load_run(next.i, g + t0 * p.ldi, p.ldi, run, off, left);
-    }
-  };
-  const int64_t tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
-  int64_t tile = begin + (tiles - 1) * kTile;
-  if (tiles > 0) fetch(tile + wave * kSpan);
   float decay[V], sum[V];
   State carry[V];
   Run total[V];
@@ -407,67 +445,96 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
     total[v] = empty_run(), sum[v] = 0.0f;
   }
-  int buf = 0;
-  for (int64_t k = 0; k < tiles; ++k, tile -= kTile, buf ^= 1) {
-    const int64_t t0 = tile + wave * kSpan, left = end - t0;
-    const Rows now = next;
-    Gate gate[kRun][V];
-    float si[kRun][V], resti[kRun][V], before[kRun][V];
+  Feed feed;
+  feed.open(0, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
+  feed.open(1, p.d_h, ldh, row0, lane);
+  if constexpr (!TOTALS) feed.open(2, p.x, p.ldx, at.b * p.T * p.ldx + c0 * int64_t(sizeof(E)), lane);
+  if constexpr (!TOTALS && IG) feed.open(3, p.i, p.ldi, at.b * p.T * p.ldi + c0 * int64_t(sizeof(E)), lane);
+  const int64_t spans = (p.T + kSpan - 1) / kSpan;
+  auto fetch = [&](int stage, int64_t t0) {
+    const int64_t left = t0 < begin ? 0 : end - t0;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) feed.load(k, raw[stage][wave][k], t0, left, width);
+    if constexpr (!TOTALS) {
+      const float* m = p.marks + (at.b * spans + t0 / kSpan) * p.C + c0;
+      load_words(raw_marks[stage][wave], reinterpret_cast<const char*>(m), left > 0 ? 4 * channels : 0, lane);
+    }
+  };
+  const int64_t tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+  const int64_t first = begin + (tiles - 1) * kTile + wave * kSpan;   // the last tile comes first
+  if (tiles > 0) {
+    fetch(0, first);
+    fetch(1, first - kTile);
+  }
+  auto walk = [&](auto full, int64_t k) {
+    constexpr bool FULL = decltype(full)::value;
+    const int stage = k & 1;
+    const int64_t t0 = first - k * kTile, left = end - t0;
+    wait_tile<kLoads, kStores>(k);
+    uint32_t in[NT][R];
+    float mark[V];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[stage][wave][t] + 256 * r + 4 * lane);
+    }
+    if constexpr (!TOTALS) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) mark[v] = reinterpret_cast<const float*>(raw_marks[stage][wave])[(lane % kLanes) * V + v];
+    }
+    wait_lds();
+    fetch(stage, t0 - 2 * kTile);
+    Gate gate[R][V];
+    float si[R][V], resti[R][V], before[R][V];
     Run own_run[V], lanes[V], mine[V], all[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) own_run[v] = empty_run();
-    if (left > 0) {
-      // G of the run, from its last token
+    // G of the run, from its last token
 #pragma unroll
-      for (int r = kRun - 1; r >= 0; --r) {
-        const bool here = run * kRun + r < left;
+    for (int r = R - 1; r >= 0; --r) {
+      const bool here = FULL || run * R + r < left;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          Gate& t = gate[r][v];
-          t = gate_of<E, KIND>(part_of<E>(now.f[r], v), decay[v]);
-          t.a = here ? t.a : 1.0f;
-          const float up = here ? part_of<E>(now.d[r], v) : 0.0f;
-          own_run[v] = join(own_run[v], Run{t.a, here ? t.c : 0.0f, t.a * up});
-          if constexpr (!TOTALS) {
-            float add = t.m * part_of<E>(now.x[r], v);
-            if constexpr (IG) {
-              sigmoids<E>(part_of<E>(now.i[r], v), &si[r][v], &resti[r][v]);
-              add *= si[r][v];
-            }
-            before[r][v] = here ? add : 0.0f;
+      for (int v = 0; v < V; ++v) {
+        Gate& t = gate[r][v];
+        t = gate_of<E, KIND>(part_of<E>(in[0][r], v), decay[v]);
+        if (!here) t.a = 1.0f;
+        const float up = part_of<E>(in[1][r], v);
+        own_run[v] = join(own_run[v], Run{t.a, here ? t.c : 0.0f, here ? t.a * up : 0.0f});
+        if constexpr (!TOTALS) {
+          before[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[2][r], v) : t.m * part_of<E>(in[2][r], v);
+          if constexpr (IG) {
+            sigmoids<E>(part_of<E>(in[3][r], v), &si[r][v], &resti[r][v]);
+            before[r][v] *= si[r][v];
           }
+          if (!here) before[r][v] = 0.0f;
         }
       }
     }
-    if (k + 1 < tiles) fetch(t0 - kTile);
     if constexpr (!TOTALS) {
       // h before each token: from what each adds
       Run fwd[V], ahead[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        fwd[v] = empty_run();
-        if (left > 0) {
+        fwd[v] = {own_run[v].A, 0.0f, 0.0f};
 #pragma unroll
-          for (int r = 0; r < kRun; ++r) fwd[v] = join(fwd[v], Run{gate[r][v].a, 0.0f, before[r][v]});
-        }
+        for (int r = 0; r < R; ++r) fwd[v].H = fmaf(gate[r][v].a, fwd[v].H, before[r][v]);
       }
       join_lanes<V, false>(fwd, ahead, lane);
-      if (left > 0) {
-        const float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float y = fmaf(ahead[v].A, m[v], ahead[v].H);
+      for (int v = 0; v < V; ++v) {
+        float y = fmaf(ahead[v].A, mark[v], ahead[v].H);
 #pragma unroll
-          for (int r = 0; r < kRun; ++r) {
-            const float add = before[r][v];
-            before[r][v] = y;
-            y = fmaf(gate[r][v].a, y, add);
-          }
+        for (int r = 0; r < R; ++r) {
+          const float add = before[r][v];
+          before[r][v] = y;
+          y = fmaf(gate[r][v].a, y, add);
         }
       }
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) settle(own_run[v]);
     join_lanes<V, true>(own_run, lanes, lane);
-    join_waves<V, kBackWaves, true>(part[buf], wave, lane, own_run, mine, all);
+    join_waves<V, true>(part[stage], wave, lane, own_run, mine, all);
     if constexpr (TOTALS) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -483,39 +550,43 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
         G[v] = fmaf(lanes[v].A, s.value(), lanes[v].H);
         carry[v].pass(all[v]);
       }
-      if (left > 0) {
 #pragma unroll
-        for (int r = kRun - 1; r >= 0; --r) {
-          float ox[V], of[V], oi[V];
-          const bool here = run * kRun + r < left;
+      for (int r = R - 1; r >= 0; --r) {
+        const bool here = FULL || run * R + r < left;
+        float ox[V], of[V], oi[V];
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const Gate& t = gate[r][v];
-            const float xv = part_of<E>(now.x[r], v), l = part_of<E>(now.d[r], v) + G[v];
-            const float lm = KIND == GDN_SCAN_LOG ? l : l * t.m;
-            ox[v] = IG ? lm * si[r][v] : lm;
-            if constexpr (IG) oi[v] = ox[v] * xv * resti[r][v];
-            const float gx = IG ? si[r][v] * xv : xv;
-            if constexpr (KIND == GDN_SCAN_LOG) {
-              of[v] = l * before[r][v] * t.a;
-            } else if constexpr (KIND == GDN_SCAN_SIGMOID) {
-              of[v] = l * (before[r][v] - gx) * (t.a * t.c);
-            } else {
-              // d m / d a = -a / m
-              const float slope = t.m > 0.0f ? t.a * gx * __builtin_amdgcn_rcpf(t.m) : 0.0f;
-              const float dlog = l * t.a * (before[r][v] - slope) * t.s;
-              of[v] = -decay[v] * t.rest * dlog;
-              sum[v] -= here ? dlog : 0.0f;
-            }
-            G[v] = here ? t.a * l : G[v];
+        for (int v = 0; v < V; ++v) {
+          const Gate& t = gate[r][v];
+          const float xv = part_of<E>(in[2][r], v), l = part_of<E>(in[1][r], v) + G[v];
+          const float lm = KIND == GDN_SCAN_LOG ? l : l * t.m;
+          ox[v] = IG ? lm * si[r][v] : lm;
+          if constexpr (IG) oi[v] = ox[v] * xv * resti[r][v];
+          const float gx = IG ? si[r][v] * xv : xv;
+          if constexpr (KIND == GDN_SCAN_LOG) {
+            of[v] = l * before[r][v] * t.a;
+          } else if constexpr (KIND == GDN_SCAN_SIGMOID) {
+            of[v] = l * (before[r][v] - gx) * (t.a * t.c);
+          } else {
+            // d m / d a = -a / m
+            const float slope = t.m > 0.0f ? t.a * gx * __builtin_amdgcn_rcpf(t.m) : 0.0f;
+            const float dlog = l * t.a * (before[r][v] - slope) * t.s;
+            of[v] = -decay[v] * t.rest * dlog;
+            sum[v] -= here ? dlog : 0.0f;
           }
-          store_row(dx + t0 * ldh, ldh, run, r, off, left, own, packed<E>(ox));
-          store_row(df + t0 * ldh, ldh, run, r, off, left, own, packed<E>(of));
-          if constexpr (IG) store_row(di + t0 * ldh, ldh, run, r, off, left, own, packed<E>(oi));
+          G[v] = here ? t.a * l : G[v];
         }
+        in[2][r] = packed<E>(ox), in[0][r] = packed<E>(of);
+        if constexpr (IG) in[3][r] = packed<E>(oi);
       }
+      store_run(dx + t0 * ldh, ldh, left, width, run, to, in[2]);
+      store_run(df + t0 * ldh, ldh, left, width, run, to, in[0]);
+      if constexpr (IG) store_run(di + t0 * ldh, ldh, left, width, run, to, in[3]);
     }
-  }
+  };
+  int64_t k = 0;
+  if (tiles * kTile > end - begin && tiles > 0) walk(std::false_type{}, k++);
+  for (; k < tiles; ++k) walk(std::true_type{}, k);
+  wait_memory<0>();
   if constexpr (TOTALS) {
     if (wave == 0 && run == 0 && own) {
 #pragma unroll
@@ -542,7 +613,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float t = 0.0f;
-          for (int w = 0; w < kBackWaves; ++w) t += sums[w * N + (lane % kLanes) * V + v];
+          for (int w = 0; w < kWaves; ++w) t += sums[w * N + (lane % kLanes) * V + v];
           p.ddecay[(at.b * p.segs + at.seg) * p.C + c0 + ch + v] = t;
         }
       }
@@ -615,7 +686,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     if (p.segs > 1) {
       p.blocks = unsigned(q.a.B * slices * (p.segs - 1));
       if constexpr (BACK)
-        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
+        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
       else
         scan_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
       const int rc = int(hipGetLastError());
@@ -623,7 +694,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     }
     p.blocks = unsigned(q.a.B * slices * p.segs);
     if constexpr (BACK)
-      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
+      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
     else
       scan_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
     return int(hipGetLastError());
