@@ -18,7 +18,7 @@ int64_t spans_of(int64_t T) { return (T + scan::kSpan - 1) / scan::kSpan; }
 // sequences alone leave CUs idle, segments run side by side, at the price of a first pass over
 // the inputs for what each makes of the state.
 void cut(const gdn_scan_args& a, bool back, unsigned* segs, int64_t* seg) {
-  const int64_t tile = scan::kTile;
+  const int64_t tile = back ? scan::kBackTile : scan::kTile;
   const int64_t tiles = std::max<int64_t>(1, (a.T + tile - 1) / tile);
   const int64_t walks = a.B * ((a.C + channels_a_slice(a) - 1) / channels_a_slice(a));
   const int64_t want = std::min<int64_t>(tiles, std::max<int64_t>(1, kGroups / walks));

@@ -2,10 +2,11 @@
 // their launches for one element type.
 //
 // Eight lanes of a wave lie across the channels of a slice, four bytes a lane and row, and eight
-// groups of lanes hold a run of consecutive tokens each. A lane joins the tokens of its run, the groups join theirs by shuffles, the waves of a workgroup theirs
-// through LDS, and the workgroup walks the tiles of its segment with the state it carries.
-// Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no division, so a decay
-// may be 0, and nothing exceeds what the recurrence itself does.
+// groups of lanes hold a run of eight consecutive tokens each: a wave has a span of 64 tokens. A
+// lane joins the tokens of its run, the groups join theirs by DPP, the waves of a workgroup theirs
+// through LDS, a wave for each channel, and the workgroup walks the tiles of its segment with the
+// state it carries. Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no
+// division, so a decay may be 0, and nothing exceeds what the recurrence itself does.
 //
 // What a run leaves of the state before it is held twice: as the product A and as 1 - A,
 // summed from the 1 - a of its tokens. Where less than half goes, the state loses (1 - A) h
@@ -25,9 +26,10 @@ namespace scan {
 constexpr int kSpan = GDN_SCAN_SPAN;   // tokens between checkpoints
 constexpr int kLanes = 8;              // lanes across a slice's channels
 constexpr int kRuns = 64 / kLanes;     // lane groups, a run of tokens each
-constexpr int kWaves = 8;              // waves a workgroup
+constexpr int kWaves = 16;             // waves a workgroup, a span each: a tile
+constexpr int kBackWaves = 8;          // the same in the gradients, which take twice the registers
 constexpr int kRun = kSpan / kRuns;    // tokens a run: a wave has a span
-constexpr int kTile = kWaves * kSpan;
+constexpr int kTile = kWaves * kSpan, kBackTile = kBackWaves * kSpan;
 
 template <typename E> struct Shape {
   static constexpr int V = 4 / sizeof(E);   // channels a lane
@@ -139,19 +141,21 @@ __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_
   return {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(bytes), 0x00020000u};
 }
 
-// Rows on their way from memory to LDS, two tiles ahead of their use: 32 bytes a row of a slice,
+// Rows on their way from memory to LDS, ahead of their use: 32 bytes a row of a slice,
 // a wave's own span, so that nothing but its own count of loads says when they are there. Lane l
 // of a load brings sixteen bytes to the wave's place 16 l: row (l / 2 % 8) * 8 + l / 16 (and four
-// on), so that the eight runs' rows r lie side by side and a lane reads its own at 256 r + 4 l,
-// free of bank conflicts. The loads are written as assembly, which has no registers to guard;
+// on), so that the eight runs' rows r lie side by side, at 256 r + 32 run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
 // the compiler's own counts only ever wait for more.
 struct Feed {
   uint32_t off[4];
   int64_t ld[4];
   const char* base[4];
+  // a lane's place in a span for sixteen bytes
+  static __device__ __forceinline__ uint32_t place(int lane, int64_t ld) {
+    return uint32_t((lane / 2 % 8) * 8 + lane / 16) * uint32_t(ld) + lane % 2 * 16;
+  }
   __device__ __forceinline__ void open(int k, const void* p, int64_t ld_, int64_t first, int lane) {
-    base[k] = static_cast<const char*>(p) + first, ld[k] = ld_;
-    off[k] = uint32_t((lane / 2 % 8) * 8 + lane / 16) * uint32_t(ld_) + lane % 2 * 16;
+    base[k] = static_cast<const char*>(p) + first, ld[k] = ld_, off[k] = place(lane, ld_);
   }
   __device__ __forceinline__ void load(int k, char* to, int64_t t0, int64_t left, uint32_t width) const {
     const uint4v range = rows_from(base[k] + t0 * ld[k], ld[k], left, width);
@@ -195,13 +199,24 @@ __device__ __forceinline__ uint32_t packed(const float* x) {
     return __builtin_bit_cast(uint32_t, r);
   }
 }
-// A run's rows, one store each: `at` is the lane's place in the span's first row, behind the
-// buffer where it has no channels.
-__device__ __forceinline__ void store_run(char* base, int64_t ld, int64_t left, uint32_t width, int run, uint32_t at, const uint32_t* x) {
-  const auto to = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(rows_from(base, ld, left, width)[2]), 0x00020000);
+// A lane's place among the rows r of a span in LDS, and its channels.
+struct Lane {
+  int run, slot;
+  __device__ __forceinline__ Lane(int lane) : run(lane / 2 % 8), slot(lane / 16 * 2 + lane % 2) {}
+  __device__ __forceinline__ uint32_t at(int r) const { return 256 * r + 32 * run + 4 * slot; }
+};
+
+// A span's rows by way of LDS, laid as they came, in two stores: half of a slice of sixteen bytes
+// and rows that are not there lie behind the buffer.
+__device__ __forceinline__ void store_span(char* by, char* base, int64_t ld, int64_t left, uint32_t width, const Lane& l, int lane,
+                                           const uint32_t* x) {
 #pragma unroll
-  for (int r = 0; r < kRun; ++r)
-    __builtin_amdgcn_raw_buffer_store_b32(x[r], to, at + uint32_t(run * kRun + r) * uint32_t(ld), 0, 0);
+  for (int r = 0; r < kRun; ++r) *reinterpret_cast<uint32_t*>(by + l.at(r)) = x[r];
+  const auto to = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(rows_from(base, ld, left, width)[2]), 0x00020000);
+  const uint32_t at = lane % 2 * 16 < width ? Feed::place(lane, ld) : 0x80000000u;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const uint4v*>(by + 1024 * j + 16 * lane), to, at + j * 4 * uint32_t(ld), 0, 0);
 }
 
 // Where a workgroup stands: blocks that follow each other on one XCD (their index modulo 8)
@@ -219,122 +234,135 @@ struct Place {
   }
 };
 
-// The runs of a tile's waves through LDS, in order: `all` of them joined, and `mine`, those
-// before this wave's.
+// Lanes n before (BACK: behind) in a row of sixteen; `none` where there is no such lane.
+template <int N, bool BACK>
+__device__ __forceinline__ float beside(float x, float none) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(x), (BACK ? 0x100 : 0x110) + N, 0xf, 0xf, false));
+}
+template <int N, bool BACK>
+__device__ __forceinline__ Run beside(const Run& r) {
+  return {beside<N, BACK>(r.A, 1.0f), beside<N, BACK>(r.C, 0.0f), beside<N, BACK>(r.H, 0.0f)};
+}
+
+// Joins over the lane groups, which lie two lanes apart: own becomes the runs up to and with the
+// lane's (BACK: from the last one down to it), before those without it.
 template <int V, bool BACK>
-__device__ __forceinline__ void join_waves(float4 (*part)[kLanes * V], int wave, int lane, const Run* own, Run* mine, Run* all) {
-  if (lane / kLanes == (BACK ? 0 : kRuns - 1)) {
+__device__ __forceinline__ void join_lanes(Run* own, Run* before) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) part[wave][(lane % kLanes) * V + v] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) mine[v] = all[v] = empty_run();
-#pragma unroll 2   // all at once would hold every wave's runs in registers
-  for (int j = 0; j < kWaves; ++j) {
-    const int w = BACK ? kWaves - 1 - j : j;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (w == wave) mine[v] = all[v];
-      const float4 t = part[w][(lane % kLanes) * V + v];
-      all[v] = join(all[v], {t.x, t.y, t.z});
-    }
+  for (int v = 0; v < V; ++v) {
+    own[v] = join(beside<2, BACK>(own[v]), own[v]);
+    own[v] = join(beside<4, BACK>(own[v]), own[v]);
+    own[v] = join(beside<8, BACK>(own[v]), own[v]);
+    before[v] = beside<2, BACK>(own[v]);
   }
 }
 
-// Joins over the lane groups: own becomes the runs up to and with the lane's (BACK: from the
-// last one down to it); before those without it.
-template <int V, bool BACK>
-__device__ __forceinline__ void join_lanes(Run* own, Run* before, int lane) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int d = kLanes; d < 64; d *= 2) {
-      const Run o = BACK ? Run{__shfl_down(own[v].A, d), __shfl_down(own[v].C, d), __shfl_down(own[v].H, d)}
-                         : Run{__shfl_up(own[v].A, d), __shfl_up(own[v].C, d), __shfl_up(own[v].H, d)};
-      const Run j = join(o, own[v]);
-      const bool there = BACK ? lane + d < 64 : lane >= d;
-      own[v].A = there ? j.A : own[v].A, own[v].C = there ? j.C : own[v].C, own[v].H = there ? j.H : own[v].H;
-    }
-    const Run e = empty_run();
-    before[v] = BACK ? Run{__shfl_down(own[v].A, kLanes), 0.0f, __shfl_down(own[v].H, kLanes)}
-                     : Run{__shfl_up(own[v].A, kLanes), 0.0f, __shfl_up(own[v].H, kLanes)};
-    if (BACK ? lane >= 64 - kLanes : lane < kLanes) before[v] = e;
+// What the waves of a workgroup exchange: their spans' runs, a channel's side by side, and the state
+// before each.
+template <int N, int NW> struct Exchange {
+  float4 runs[N][NW + 1];
+  float before[NW][N];
+};
+
+// The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes, whose
+// lanes are the waves (BACK: from the last).
+template <int N, int NW, bool BACK> struct Keeper {
+  static constexpr int kOwn = N < NW ? 1 : N / NW;
+  int ch, from;   // channel of the slice, and the wave whose run the lane takes
+  bool on;
+  __device__ __forceinline__ Keeper(int wave, int lane) {
+    ch = wave * kOwn + lane / 16;
+    from = BACK ? NW - 1 - lane % 16 : lane % 16;
+    on = lane / 16 < kOwn && ch < N;
   }
-}
+  __device__ __forceinline__ bool first(int lane) const { return on && lane % 16 == 0; }
+  // Passes the carried state over a tile; gives each wave its own, and the tile's run.
+  __device__ __forceinline__ Run pass(Exchange<N, NW>& x, State& carry, int lane) const {
+    Run r = empty_run();
+    if (lane % 16 < NW) {
+      const float4 t = x.runs[ch][from];
+      r = {t.x, t.y, t.z};
+    }
+    r = join(beside<1, false>(r), r);
+    r = join(beside<2, false>(r), r);
+    r = join(beside<4, false>(r), r);
+    if constexpr (NW > 8) r = join(beside<8, false>(r), r);
+    State s = carry;
+    s.pass(beside<1, false>(r));
+    if (lane % 16 < NW) x.before[from][ch] = s.value();
+    const int end = (lane & 48) + NW - 1;
+    r = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
+    carry.pass(r);
+    return r;
+  }
+};
 
 // Forward. TOTALS: only what each segment but the last makes of the state before it.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N, NT = IG ? 3 : 2, kLoads = 2 * NT;
-  __shared__ __attribute__((aligned(16))) char raw[2][kWaves][NT][32 * kSpan];
-  __shared__ float4 part[2][kWaves][N];
+  constexpr int V = Shape<E>::V, N = Shape<E>::N, NT = IG ? 3 : 2;
+  __shared__ __attribute__((aligned(16))) char raw[kWaves][NT][32 * kSpan];
+  __shared__ __attribute__((aligned(16))) char out[kWaves][TOTALS ? 16 : 32 * kSpan];
+  __shared__ Exchange<N, kWaves> exchange;
   const Place at(p, TOTALS ? p.segs - 1 : p.segs);
-  const int lane = threadIdx.x % 64, run = lane / kLanes;
+  const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t c0 = int64_t(at.slice) * N;
-  const bool own = c0 + (lane % kLanes) * V < p.C;                          // a slice may end behind C
-  const uint32_t ch = own ? (lane % kLanes) * V : 0, width = (p.C - c0 < N ? uint32_t(p.C - c0) : N) * sizeof(E);
-  const int64_t c = at.b * p.C + c0 + ch;
+  const Lane l(lane);
+  const Keeper<N, kWaves, false> keeper(wave, lane);
+  const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
+  const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);   // a slice may end behind C
+  const bool keeps = keeper.on && uint32_t(keeper.ch) < channels;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   if (begin >= n && at.seg > 0) return;
   const bool last = n - begin <= p.seg;
-  if (TOTALS && at.seg == 0 && wave == 0 && run == 0 && own) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.start[c + v] = p.h0 != nullptr ? p.h0[c + v] : 0.0f;
-  }
+  if (TOTALS && at.seg == 0 && keeps && keeper.first(lane)) p.start[cb + keeper.ch] = p.h0 != nullptr ? p.h0[cb + keeper.ch] : 0.0f;
   if (TOTALS && last) return;
   const int64_t end = last ? n : begin + p.seg;
-  const int64_t ldh = p.C * sizeof(E);
-  char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * sizeof(E);
-  const uint32_t to = own ? ch * uint32_t(sizeof(E)) : 0x80000000u;
-  float decay[V];
-  State carry[V];
-  Run total[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c0 + ch + v] : 0.0f;
-    const float* from = p.segs > 1 ? p.start : p.h0;
-    carry[v] = {TOTALS || from == nullptr ? 0.0f : from[c + v], 0.0f};
-    if constexpr (!TOTALS) {
-      for (unsigned s = 0; s < at.seg; ++s) carry[v].pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + ch + v]);
-    }
-    total[v] = empty_run();
-  }
   Feed feed;
   feed.open(0, p.x, p.ldx, at.b * p.T * p.ldx + c0 * int64_t(sizeof(E)), lane);
   feed.open(1, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
   if constexpr (IG) feed.open(2, p.i, p.ldi, at.b * p.T * p.ldi + c0 * int64_t(sizeof(E)), lane);
-  auto fetch = [&](int stage, int64_t t0) {
+  auto fetch = [&](int64_t t0) {
 #pragma unroll
-    for (int k = 0; k < NT; ++k) feed.load(k, raw[stage][wave][k], t0, end - t0, width);
+    for (int k = 0; k < NT; ++k) feed.load(k, raw[wave][k], t0, end - t0, width);
   };
   const int64_t first = begin + wave * kSpan, tiles = (end - begin + kTile - 1) / kTile;
-  fetch(0, first);
-  fetch(1, first + kTile);
+  fetch(first);
+  const int64_t ldh = p.C * sizeof(E);
+  char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * int64_t(sizeof(E));
+  State carry = {0.0f, 0.0f};
+  Run total = empty_run();
+  if (!TOTALS && keeps) {
+    const float* from = p.segs > 1 ? p.start : p.h0;
+    if (from != nullptr) carry.hi = from[cb + keeper.ch];
+    for (unsigned s = 0; s < at.seg; ++s) carry.pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + keeper.ch]);
+  }
+  float decay[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    decay[v] = KIND == GDN_SCAN_POWER && uint32_t(l.slot * V) < channels ? p.decay[c0 + l.slot * V + v] : 0.0f;
   // a tile whose rows are all there, or the last
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
-    const int stage = k & 1;
     const int64_t t0 = first + k * kTile, left = end - t0;
-    if (!TOTALS && p.h != nullptr) wait_tile<kLoads, kRun>(k);
-    else wait_tile<kLoads, 0>(k);
+    if (!TOTALS && p.h != nullptr && k > 0) wait_memory<2>();   // the stores behind its loads
+    else wait_memory<0>();
     uint32_t in[NT][kRun];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int r = 0; r < kRun; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[stage][wave][t] + 256 * r + 4 * lane);
+      for (int r = 0; r < kRun; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[wave][t] + l.at(r));
     }
     wait_lds();
-    fetch(stage, t0 + 2 * kTile);
+    fetch(t0 + kTile);
     float a[kRun][V], b[kRun][V];
-    Run own_run[V], before[V], mine[V], all[V];
+    Run own[V], before[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) own_run[v] = empty_run();
+    for (int v = 0; v < V; ++v) own[v] = empty_run();
 #pragma unroll
     for (int r = 0; r < kRun; ++r) {
-      const bool here = FULL || run * kRun + r < left;
+      const bool here = FULL || l.run * kRun + r < left;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Gate t = gate_of<E, KIND>(part_of<E>(in[1][r], v), decay[v]);
@@ -342,42 +370,40 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
         b[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[0][r], v) : t.m * part_of<E>(in[0][r], v);
         if constexpr (IG) b[r][v] *= sigmoid_of<E>(part_of<E>(in[2][r], v));
         if (!here) b[r][v] = 0.0f;
-        own_run[v] = join(own_run[v], Run{a[r][v], here ? t.c : 0.0f, b[r][v]});
+        own[v] = join(own[v], Run{a[r][v], here ? t.c : 0.0f, b[r][v]});
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) settle(own_run[v]);
-    join_lanes<V, false>(own_run, before, lane);
-    join_waves<V, false>(part[stage], wave, lane, own_run, mine, all);
-    if constexpr (TOTALS) {
+    for (int v = 0; v < V; ++v) settle(own[v]);
+    join_lanes<V, false>(own, before);
+    if (l.run == kRuns - 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        carry[v].pass(all[v]);
-        total[v] = join(total[v], all[v]);
-      }
-    } else {
+      for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
+    }
+    __syncthreads();
+    if (keeper.on) {
+      const Run all = keeper.pass(exchange, carry, lane);
+      if constexpr (TOTALS) total = join(total, all);
+    }
+    __syncthreads();
+    if constexpr (!TOTALS) {
       float y[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        State s = carry[v];
-        s.pass(mine[v]);
-        y[v] = fmaf(before[v].A, s.value(), before[v].H);
-        carry[v].pass(all[v]);
-      }
-      if (p.marks != nullptr && run == 0 && own && left > 0) {
-        float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + ch;
+      for (int v = 0; v < V; ++v) y[v] = fmaf(before[v].A, exchange.before[wave][l.slot * V + v], before[v].H);
+      if (p.marks != nullptr && l.run == 0 && uint32_t(l.slot * V) < channels && left > 0) {
+        float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + l.slot * V;
 #pragma unroll
         for (int v = 0; v < V; ++v) m[v] = y[v];
       }
       if (p.h != nullptr) {
-        uint32_t out[kRun];
+        uint32_t rows[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
 #pragma unroll
           for (int v = 0; v < V; ++v) y[v] = fmaf(a[r][v], y[v], b[r][v]);
-          out[r] = packed<E>(y);
+          rows[r] = packed<E>(y);
         }
-        store_run(h + t0 * ldh, ldh, left, width, run, to, out);
+        store_span(out[wave], h + t0 * ldh, ldh, left, width, l, lane, rows);
       }
     }
   };
@@ -385,36 +411,33 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   for (; (k + 1) * kTile <= end - begin; ++k) walk(std::true_type{}, k);
   if (k < tiles) walk(std::false_type{}, k);
   wait_memory<0>();   // of LDS that the next workgroup may get
-  if (wave != 0 || run != 0 || !own) return;
-  if constexpr (TOTALS) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch + v] = {total[v].A, total[v].C, carry[v].value()};
-  } else if (last && p.h_final != nullptr) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.h_final[c + v] = carry[v].value();
-  }
+  if (!keeps || !keeper.first(lane)) return;
+  if constexpr (TOTALS)
+    p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + keeper.ch] = {total.A, total.C, carry.value()};
+  else if (last && p.h_final != nullptr)
+    p.h_final[cb + keeper.ch] = carry.value();
 }
 
 // Gradients, from a sequence's end: with G_t = a_t (d_h_t + G_{t+1}) the same recurrence, whose
 // value behind token t is l_t = d_h_t + G_{t+1}. h comes from the state before the span. TOTALS:
 // only what each segment but the first makes of the gradient behind it.
 template <typename E, int KIND, bool IG, bool TOTALS>
-__global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
+__global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   constexpr int V = Shape<E>::V, N = Shape<E>::N, R = kRun;
-  constexpr int NT = TOTALS ? 2 : IG ? 4 : 3, kLoads = 2 * NT + (TOTALS ? 0 : 1), kStores = TOTALS ? 0 : R * (IG ? 3 : 2);
-  __shared__ __attribute__((aligned(16))) char raw[2][kWaves][NT][32 * kSpan];
-  __shared__ __attribute__((aligned(16))) char raw_marks[2][kWaves][TOTALS ? 16 : 256];
-  __shared__ float4 part[2][kWaves][N];
+  constexpr int NT = TOTALS ? 2 : IG ? 4 : 3, kLoads = 2 * NT + (TOTALS ? 0 : 1), kStores = TOTALS ? 0 : IG ? 6 : 4;
+  __shared__ __attribute__((aligned(16))) char raw[2][kBackWaves][NT][32 * kSpan];
+  __shared__ __attribute__((aligned(16))) char raw_marks[2][kBackWaves][TOTALS ? 16 : 256];
+  __shared__ __attribute__((aligned(16))) char out[kBackWaves][TOTALS ? 16 : 32 * kSpan];
+  __shared__ Exchange<N, kBackWaves> exchange;
   Place at(p, TOTALS ? p.segs - 1 : p.segs);
   if (TOTALS) ++at.seg;
-  const int lane = threadIdx.x % 64, run = lane / kLanes;
+  const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t c0 = int64_t(at.slice) * N;
-  const bool own = c0 + (lane % kLanes) * V < p.C;
-  const uint32_t ch = own ? (lane % kLanes) * V : 0, channels = p.C - c0 < N ? uint32_t(p.C - c0) : N;
-  const uint32_t width = channels * sizeof(E);
-  const int64_t c = at.b * p.C + c0 + ch;
+  const Lane l(lane);
+  const Keeper<N, kBackWaves, true> keeper(wave, lane);
+  const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
+  const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);
+  const bool keeps = keeper.on && uint32_t(keeper.ch) < channels, own_lane = uint32_t(l.slot * V) < channels;
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
@@ -422,29 +445,15 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
   char* dx = static_cast<char*>(p.dx) + row0;
   char* df = static_cast<char*>(p.df) + row0;
   char* di = static_cast<char*>(p.di) + row0;
-  const uint32_t to = own ? ch * uint32_t(sizeof(E)) : 0x80000000u;
   if constexpr (!TOTALS) {
     // rows behind the length: zero
-    for (int64_t t = std::max(begin, n) + wave * kRuns + run; own && t < stop; t += kWaves * kRuns) {
-      *reinterpret_cast<uint32_t*>(dx + t * ldh + to) = 0, *reinterpret_cast<uint32_t*>(df + t * ldh + to) = 0;
-      if constexpr (IG) *reinterpret_cast<uint32_t*>(di + t * ldh + to) = 0;
+    for (int64_t t = std::max(begin, n) + wave * kRuns + l.run; own_lane && t < stop; t += kBackWaves * kRuns) {
+      const int64_t to = t * ldh + 4 * l.slot;
+      *reinterpret_cast<uint32_t*>(dx + to) = 0, *reinterpret_cast<uint32_t*>(df + to) = 0;
+      if constexpr (IG) *reinterpret_cast<uint32_t*>(di + to) = 0;
     }
   }
   if (TOTALS && begin >= n) return;
-  float decay[V], sum[V];
-  State carry[V];
-  Run total[V];
-  const int64_t segs_used = (n + p.seg - 1) / p.seg;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    decay[v] = KIND == GDN_SCAN_POWER ? p.decay[c0 + ch + v] : 0.0f;
-    carry[v] = {TOTALS || p.d_final == nullptr ? 0.0f : p.d_final[c + v], 0.0f};
-    if constexpr (!TOTALS) {
-      for (int64_t s = segs_used - 1; s > int64_t(at.seg); --s)
-        carry[v].pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + ch + v]);
-    }
-    total[v] = empty_run(), sum[v] = 0.0f;
-  }
   Feed feed;
   feed.open(0, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
   feed.open(1, p.d_h, ldh, row0, lane);
@@ -460,46 +469,56 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
       load_words(raw_marks[stage][wave], reinterpret_cast<const char*>(m), left > 0 ? 4 * channels : 0, lane);
     }
   };
-  const int64_t tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
-  const int64_t first = begin + (tiles - 1) * kTile + wave * kSpan;   // the last tile comes first
+  const int64_t tiles = end > begin ? (end - begin + kBackTile - 1) / kBackTile : 0;
+  const int64_t first = begin + (tiles - 1) * kBackTile + wave * kSpan;   // the last tile comes first
   if (tiles > 0) {
     fetch(0, first);
-    fetch(1, first - kTile);
+    fetch(1, first - kBackTile);
+  }
+  float decay[V], sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f, sum[v] = 0.0f;
+  State carry = {0.0f, 0.0f};
+  Run total = empty_run();
+  if (!TOTALS && keeps) {
+    if (p.d_final != nullptr) carry.hi = p.d_final[cb + keeper.ch];
+    for (int64_t s = (n + p.seg - 1) / p.seg - 1; s > int64_t(at.seg); --s)
+      carry.pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + keeper.ch]);
   }
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
     const int stage = k & 1;
-    const int64_t t0 = first - k * kTile, left = end - t0;
+    const int64_t t0 = first - k * kBackTile, left = end - t0;
     wait_tile<kLoads, kStores>(k);
     uint32_t in[NT][R];
     float mark[V];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[stage][wave][t] + 256 * r + 4 * lane);
+      for (int r = 0; r < R; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[stage][wave][t] + l.at(r));
     }
     if constexpr (!TOTALS) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) mark[v] = reinterpret_cast<const float*>(raw_marks[stage][wave])[(lane % kLanes) * V + v];
+      for (int v = 0; v < V; ++v) mark[v] = reinterpret_cast<const float*>(raw_marks[stage][wave])[l.slot * V + v];
     }
     wait_lds();
-    fetch(stage, t0 - 2 * kTile);
+    fetch(stage, t0 - 2 * kBackTile);
     Gate gate[R][V];
     float si[R][V], resti[R][V], before[R][V];
-    Run own_run[V], lanes[V], mine[V], all[V];
+    Run own[V], lanes[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) own_run[v] = empty_run();
+    for (int v = 0; v < V; ++v) own[v] = empty_run();
     // G of the run, from its last token
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      const bool here = FULL || run * R + r < left;
+      const bool here = FULL || l.run * R + r < left;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         Gate& t = gate[r][v];
         t = gate_of<E, KIND>(part_of<E>(in[0][r], v), decay[v]);
         if (!here) t.a = 1.0f;
         const float up = part_of<E>(in[1][r], v);
-        own_run[v] = join(own_run[v], Run{t.a, here ? t.c : 0.0f, here ? t.a * up : 0.0f});
+        own[v] = join(own[v], Run{t.a, here ? t.c : 0.0f, here ? t.a * up : 0.0f});
         if constexpr (!TOTALS) {
           before[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[2][r], v) : t.m * part_of<E>(in[2][r], v);
           if constexpr (IG) {
@@ -515,11 +534,11 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
       Run fwd[V], ahead[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        fwd[v] = {own_run[v].A, 0.0f, 0.0f};
+        fwd[v] = {own[v].A, 0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < R; ++r) fwd[v].H = fmaf(gate[r][v].a, fwd[v].H, before[r][v]);
       }
-      join_lanes<V, false>(fwd, ahead, lane);
+      join_lanes<V, false>(fwd, ahead);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float y = fmaf(ahead[v].A, mark[v], ahead[v].H);
@@ -532,90 +551,81 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(Pass p) {
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) settle(own_run[v]);
-    join_lanes<V, true>(own_run, lanes, lane);
-    join_waves<V, true>(part[stage], wave, lane, own_run, mine, all);
-    if constexpr (TOTALS) {
+    for (int v = 0; v < V; ++v) settle(own[v]);
+    join_lanes<V, true>(own, lanes);
+    if (l.run == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        carry[v].pass(all[v]);
-        total[v] = join(total[v], all[v]);
-      }
-    } else {
+      for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
+    }
+    __syncthreads();
+    if (keeper.on) {
+      const Run all = keeper.pass(exchange, carry, lane);
+      if constexpr (TOTALS) total = join(total, all);
+    }
+    __syncthreads();
+    if constexpr (!TOTALS) {
       float G[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        State s = carry[v];
-        s.pass(mine[v]);
-        G[v] = fmaf(lanes[v].A, s.value(), lanes[v].H);
-        carry[v].pass(all[v]);
-      }
+      for (int v = 0; v < V; ++v) G[v] = fmaf(lanes[v].A, exchange.before[wave][l.slot * V + v], lanes[v].H);
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
-        const bool here = FULL || run * R + r < left;
+        const bool here = FULL || l.run * R + r < left;
         float ox[V], of[V], oi[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const Gate& t = gate[r][v];
-          const float xv = part_of<E>(in[2][r], v), l = part_of<E>(in[1][r], v) + G[v];
-          const float lm = KIND == GDN_SCAN_LOG ? l : l * t.m;
-          ox[v] = IG ? lm * si[r][v] : lm;
+          const float xv = part_of<E>(in[2][r], v), g = part_of<E>(in[1][r], v) + G[v];
+          const float gm = KIND == GDN_SCAN_LOG ? g : g * t.m;
+          ox[v] = IG ? gm * si[r][v] : gm;
           if constexpr (IG) oi[v] = ox[v] * xv * resti[r][v];
           const float gx = IG ? si[r][v] * xv : xv;
           if constexpr (KIND == GDN_SCAN_LOG) {
-            of[v] = l * before[r][v] * t.a;
+            of[v] = g * before[r][v] * t.a;
           } else if constexpr (KIND == GDN_SCAN_SIGMOID) {
-            of[v] = l * (before[r][v] - gx) * (t.a * t.c);
+            of[v] = g * (before[r][v] - gx) * (t.a * t.c);
           } else {
             // d m / d a = -a / m
             const float slope = t.m > 0.0f ? t.a * gx * __builtin_amdgcn_rcpf(t.m) : 0.0f;
-            const float dlog = l * t.a * (before[r][v] - slope) * t.s;
+            const float dlog = g * t.a * (before[r][v] - slope) * t.s;
             of[v] = -decay[v] * t.rest * dlog;
             sum[v] -= here ? dlog : 0.0f;
           }
-          G[v] = here ? t.a * l : G[v];
+          G[v] = here ? t.a * g : G[v];
         }
         in[2][r] = packed<E>(ox), in[0][r] = packed<E>(of);
         if constexpr (IG) in[3][r] = packed<E>(oi);
       }
-      store_run(dx + t0 * ldh, ldh, left, width, run, to, in[2]);
-      store_run(df + t0 * ldh, ldh, left, width, run, to, in[0]);
-      if constexpr (IG) store_run(di + t0 * ldh, ldh, left, width, run, to, in[3]);
+      store_span(out[wave], dx + t0 * ldh, ldh, left, width, l, lane, in[2]);
+      store_span(out[wave], df + t0 * ldh, ldh, left, width, l, lane, in[0]);
+      if constexpr (IG) store_span(out[wave], di + t0 * ldh, ldh, left, width, l, lane, in[3]);
     }
   };
   int64_t k = 0;
-  if (tiles * kTile > end - begin && tiles > 0) walk(std::false_type{}, k++);
+  if (tiles * kBackTile > end - begin && tiles > 0) walk(std::false_type{}, k++);
   for (; k < tiles; ++k) walk(std::true_type{}, k);
   wait_memory<0>();
   if constexpr (TOTALS) {
-    if (wave == 0 && run == 0 && own) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch + v] = {total[v].A, total[v].C, carry[v].value()};
-    }
+    if (keeps && keeper.first(lane))
+      p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + keeper.ch] = {total.A, total.C, carry.value()};
   } else {
-    if (at.seg == 0 && p.dh0 != nullptr && wave == 0 && run == 0 && own) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.dh0[c + v] = carry[v].value();
-    }
+    if (at.seg == 0 && p.dh0 != nullptr && keeps && keeper.first(lane)) p.dh0[cb + keeper.ch] = carry.value();
     if (KIND == GDN_SCAN_POWER && p.ddecay != nullptr) {
       // over the lane groups, then the waves
-      float* sums = reinterpret_cast<float*>(part);
-      __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int m = kLanes; m < 64; m *= 2) sum[v] += __shfl_xor(sum[v], m);
-        if (run == 0) sums[wave * N + (lane % kLanes) * V + v] = sum[v];
+        for (int m = 2; m < 16; m *= 2) sum[v] += __shfl_xor(sum[v], m);
       }
       __syncthreads();
-      if (wave == 0 && run == 0 && own) {
+      if (l.run == 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float t = 0.0f;
-          for (int w = 0; w < kWaves; ++w) t += sums[w * N + (lane % kLanes) * V + v];
-          p.ddecay[(at.b * p.segs + at.seg) * p.C + c0 + ch + v] = t;
-        }
+        for (int v = 0; v < V; ++v) exchange.before[wave][l.slot * V + v] = sum[v];
+      }
+      __syncthreads();
+      if (threadIdx.x < channels) {
+        float t = 0.0f;
+        for (int w = 0; w < kBackWaves; ++w) t += exchange.before[w][threadIdx.x];
+        p.ddecay[(at.b * p.segs + at.seg) * p.C + c0 + threadIdx.x] = t;
       }
     }
   }
@@ -686,7 +696,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     if (p.segs > 1) {
       p.blocks = unsigned(q.a.B * slices * (p.segs - 1));
       if constexpr (BACK)
-        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
+        scan_bwd_kernel<E, K, G, true><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
       else
         scan_kernel<E, K, G, true><<<p.blocks, 64 * kWaves, 0, s>>>(p);
       const int rc = int(hipGetLastError());
@@ -694,7 +704,7 @@ int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
     }
     p.blocks = unsigned(q.a.B * slices * p.segs);
     if constexpr (BACK)
-      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
+      scan_bwd_kernel<E, K, G, false><<<p.blocks, 64 * kBackWaves, 0, s>>>(p);
     else
       scan_kernel<E, K, G, false><<<p.blocks, 64 * kWaves, 0, s>>>(p);
     return int(hipGetLastError());
