@@ -138,63 +138,91 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(Norm a) {
 }
 
 // Gradients, r' from the inputs once more. A workgroup walks every gridDim-th row and keeps its
-// sums for the weights in registers.
-template <typename E, typename R, int NV, bool SILU>
-__global__ __launch_bounds__(1024) void block_norm_bwd_kernel(Norm a) {
+// sums for the weights in registers. MOST threads a workgroup. One vector a lane (rows of up to
+// 4,096 channels) leaves registers for the weights too and for a row's loads one ahead of its use.
+template <typename E, typename R, int NV, bool SILU, int MOST>
+__global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(Norm a) {
+  constexpr bool KEEP = NV == 1;
   __shared__ float part[2][3][kMaxWaves][2];
   const int waves = blockDim.x / 64;
   float s_w[NV][8] = {}, s_p[NV][8] = {}, s_s[NV][8] = {};
+  float kept[KEEP ? 3 : 1][NV][8];
   int64_t c[NV];
   bool own[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     c[k] = 8 * (int64_t(k) * blockDim.x + threadIdx.x);
     own[k] = c[k] < a.C;
+    if (!own[k]) c[k] = 0;
+    if constexpr (KEEP) ones_or(a.w, c[k], kept[0][k]), ones_or(a.post_w, c[k], kept[1][k]), ones_or(a.scale, c[k], kept[2][k]);
   }
+  struct Loaded {
+    vec<R, 8> r, up;
+    vec<E, 8> y, z, dn;
+  };
+  // rows of absent inputs are zero; so are a lane's channels behind the last
+  auto fetch = [&](Loaded* f, int64_t row) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      f[k] = Loaded{};
+      if (!own[k]) continue;
+      f[k].r = *reinterpret_cast<const vec<R, 8>*>(static_cast<const R*>(a.r) + row * a.ldr + c[k]);
+      if (a.y != nullptr) f[k].y = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.y) + row * a.ldy + c[k]);
+      if (a.gate != nullptr) f[k].z = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.gate) + row * a.ldg + c[k]);
+      if (a.d_out != nullptr) f[k].dn = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.d_out) + row * a.C + c[k]);
+      if (a.d_r != nullptr) f[k].up = *reinterpret_cast<const vec<R, 8>*>(static_cast<const R*>(a.d_r) + row * a.C + c[k]);
+    }
+  };
+  Loaded next[NV];
   int buf = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
-    float r[NV][8] = {}, y[NV][8] = {}, dn[NV][8] = {}, act[NV][8], slope[NV][8];
+  int64_t row = blockIdx.x;
+  if (KEEP && row < a.rows) fetch(next, row);
+  for (; row < a.rows; row += gridDim.x, buf ^= 1) {
+    if constexpr (!KEEP) fetch(next, row);
+    float r[NV][8], y[NV][8], dn[NV][8], up[NV][8], act[NV][8], slope[NV][8];
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) act[k][i] = 1.0f, slope[k][i] = 0.0f;
-      if (!own[k]) continue;
-      load8<R>(a.r, row * a.ldr + c[k], r[k]);
-      if (a.y != nullptr) load8<E>(a.y, row * a.ldy + c[k], y[k]);
-      if (a.d_out != nullptr) load8<E>(a.d_out, row * a.C + c[k], dn[k]);
-      if (a.gate != nullptr) {
-        float z[8];
-        load8<E>(a.gate, row * a.ldg + c[k], z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {
+        r[k][i] = float(next[k].r[i]), y[k][i] = float(next[k].y[i]), dn[k][i] = float(next[k].dn[i]), up[k][i] = float(next[k].up[i]);
+        act[k][i] = 1.0f, slope[k][i] = 0.0f;
+        if (a.gate != nullptr) {
+          const float z = float(next[k].z[i]);
           float s, rest;
-          sigmoids<E>(z[i], &s, &rest);
-          act[k][i] = SILU ? z[i] * s : s;
-          slope[k][i] = SILU ? s * (1.0f + z[i] * rest) : s * rest;
+          sigmoids<E>(z, &s, &rest);
+          act[k][i] = SILU ? z * s : s;
+          slope[k][i] = SILU ? s * (1.0f + z * rest) : s * rest;
         }
+        sum[0] += y[k][i] * y[k][i];
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] += y[k][i] * y[k][i];
     }
+    if (KEEP && row + gridDim.x < a.rows) fetch(next, row + gridDim.x);
     float post = 1.0f;
     if (a.post) {
       block_sum<1>(sum, reinterpret_cast<float(*)[1]>(part[buf][0]), waves);
       post = 1.0f / sqrtf(sum[0] * a.mean + a.eps);
     }
-    // y becomes y rms(y) (or stays), r becomes r', dn becomes d n / d (r' rms) = dn weight
+    // y becomes y rms(y) (or stays), r becomes r'
+    auto weights = [&](int k, float* w, float* pw, float* sc) {
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = kept[0][k][i], pw[i] = kept[1][k][i], sc[i] = kept[2][k][i];
+      } else {
+        ones_or(a.w, c[k], w), ones_or(a.post_w, c[k], pw), ones_or(a.scale, c[k], sc);
+      }
+    };
     sum[0] = sum[1] = 0.0f;
-    float w[NV][8], pw[NV][8], sc[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (!own[k]) continue;
-      ones_or(a.w, c[k], w[k]), ones_or(a.post_w, c[k], pw[k]), ones_or(a.scale, c[k], sc[k]);
+      float w[8], pw[8], sc[8];
+      weights(k, w, pw, sc);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         y[k][i] *= post;
-        r[k][i] = fmaf(a.rho, r[k][i], y[k][i] * pw[k][i] * sc[k][i] * act[k][i]);
+        r[k][i] = fmaf(a.rho, r[k][i], y[k][i] * pw[i] * sc[i] * act[k][i]);
         sum[0] += r[k][i] * r[k][i];
-        sum[1] += dn[k][i] * w[k][i] * r[k][i];
+        sum[1] += dn[k][i] * w[i] * r[k][i];
       }
     }
     block_sum<2>(sum, part[buf][1], waves);
@@ -203,25 +231,24 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(Norm a) {
     sum[0] = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (!own[k]) continue;
-      float up[8] = {}, out[8];
-      if (a.d_r != nullptr) load8<R>(a.d_r, row * a.C + c[k], up);
+      float w[8], pw[8], sc[8], out[8];
+      weights(k, w, pw, sc);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = r[k][i] * rms;
         s_w[k][i] += dn[k][i] * n;
-        const float d = up[i] + rms * (dn[k][i] * w[k][i] - n * dot);   // of r'
+        const float d = up[k][i] + rms * (dn[k][i] * w[i] - n * dot);   // of r'
         out[i] = a.rho * d;
-        const float u = y[k][i] * pw[k][i], du = d * act[k][i];
+        const float u = y[k][i] * pw[i], du = d * act[k][i];
         s_s[k][i] += du * u;
-        slope[k][i] *= d * sc[k][i] * u;    // of the gate
-        dn[k][i] = du * sc[k][i];           // of u
+        slope[k][i] *= d * sc[i] * u;    // of the gate
+        dn[k][i] = du * sc[i];           // of u
         s_p[k][i] += dn[k][i] * y[k][i];
-        dn[k][i] *= pw[k][i];               // of y rms(y)
+        dn[k][i] *= pw[i];               // of y rms(y)
         sum[0] += dn[k][i] * y[k][i];
       }
-      if (a.dr != nullptr) store8<R>(a.dr, row * a.C + c[k], out);
-      if (a.dgate != nullptr) store8<E>(a.dgate, row * a.C + c[k], slope[k]);
+      if (a.dr != nullptr && own[k]) store8<R>(a.dr, row * a.C + c[k], out);
+      if (a.dgate != nullptr && own[k]) store8<E>(a.dgate, row * a.C + c[k], slope[k]);
     }
     if (a.dy == nullptr) continue;
     float back = 0.0f;
@@ -231,10 +258,9 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(Norm a) {
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (!own[k]) continue;
 #pragma unroll
       for (int i = 0; i < 8; ++i) dn[k][i] = post * (dn[k][i] - y[k][i] * back);
-      store8<E>(a.dy, row * a.C + c[k], dn[k]);
+      if (own[k]) store8<E>(a.dy, row * a.C + c[k], dn[k]);
     }
   }
   if (a.partial == nullptr) return;
@@ -248,10 +274,15 @@ __global__ __launch_bounds__(1024) void block_norm_bwd_kernel(Norm a) {
   }
 }
 
-// Blocks of a gradient launch: partial sums of so many rows.
+// Threads of a gradient launch: two vectors a lane from 4,096 channels on, whose sums and rows take
+// 256 registers, so 512 threads.
+unsigned bwd_threads(int64_t C) {
+  const int64_t lanes = C <= 4096 ? 512 : 1024;   // channels a wave
+  return unsigned((C + lanes - 1) / lanes * 64);
+}
+// Blocks of a gradient launch, eight waves a CU: partial sums of so many rows.
 int64_t bwd_blocks(int64_t rows, int64_t C) {
-  const int64_t waves = (C + 511) / 512;
-  return std::max<int64_t>(1, std::min<int64_t>(rows, std::max<int64_t>(256, 2048 / waves)));
+  return std::max<int64_t>(1, std::min<int64_t>(rows, std::max<int64_t>(256, 2048 * 64 / bwd_threads(C))));
 }
 
 Norm norm_of(const BlockNormProblem& p) {
@@ -301,9 +332,19 @@ int launch_block_norm_bwd(const BlockNormProblem& p, const gdn_block_norm_grads&
   const bool sums = g.dweight != nullptr || g.dpost_weight != nullptr || g.dscale != nullptr;
   n.partial = sums ? static_cast<float*>(ws) : nullptr;
   const int64_t blocks = bwd_blocks(n.rows, n.C);
-  const int rc = by_types(p.a, [&](auto e, auto r, auto nv, auto silu) {
-    block_norm_bwd_kernel<decltype(e), decltype(r), decltype(nv)::value, decltype(silu)::value>
-        <<<unsigned(blocks), threads_of(n.C), 0, s>>>(n);
+  const int rc = by_types(p.a, [&](auto e, auto r, auto, auto silu) {
+    typedef decltype(e) E;
+    typedef decltype(r) R;
+    constexpr bool SILU = decltype(silu)::value;
+    const unsigned threads = bwd_threads(n.C);
+    if (n.C <= 2048)
+      block_norm_bwd_kernel<E, R, 1, SILU, 256><<<unsigned(blocks), threads, 0, s>>>(n);
+    else if (n.C <= 4096)
+      block_norm_bwd_kernel<E, R, 1, SILU, 512><<<unsigned(blocks), threads, 0, s>>>(n);
+    else if (n.C <= 8192)
+      block_norm_bwd_kernel<E, R, 2, SILU, 512><<<unsigned(blocks), threads, 0, s>>>(n);
+    else
+      block_norm_bwd_kernel<E, R, 2, SILU, 1024><<<unsigned(blocks), threads, 0, s>>>(n);
     return int(hipGetLastError());
   });
   if (rc != 0 || !sums) return rc;
