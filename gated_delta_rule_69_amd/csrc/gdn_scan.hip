@@ -8,8 +8,9 @@ namespace {
 using scan::Pass;
 using scan::Run;
 
-int64_t channels_a_slice(const gdn_scan_args& a) {
-  return a.dtype == GDN_DTYPE_BF16 ? scan::Shape<__bf16>::N : scan::Shape<float>::N;
+int64_t slices_of(const gdn_scan_args& a, bool back) {
+  const int64_t row = back ? scan::Geo<scan::kBackLanes>::kRow : scan::Geo<scan::kLanes>::kRow;
+  return (a.C * (a.dtype == GDN_DTYPE_BF16 ? 2 : 4) + row - 1) / row;
 }
 constexpr int64_t kGroups = 256;   // workgroups that fill the CUs
 int64_t spans_of(int64_t T) { return (T + scan::kSpan - 1) / scan::kSpan; }
@@ -20,7 +21,7 @@ int64_t spans_of(int64_t T) { return (T + scan::kSpan - 1) / scan::kSpan; }
 void cut(const gdn_scan_args& a, bool back, unsigned* segs, int64_t* seg) {
   const int64_t tile = back ? scan::kBackTile : scan::kTile;
   const int64_t tiles = std::max<int64_t>(1, (a.T + tile - 1) / tile);
-  const int64_t walks = a.B * ((a.C + channels_a_slice(a) - 1) / channels_a_slice(a));
+  const int64_t walks = a.B * slices_of(a, back);
   const int64_t want = std::min<int64_t>(tiles, std::max<int64_t>(1, kGroups / walks));
   const int64_t each = (tiles + want - 1) / want;
   *segs = unsigned((tiles + each - 1) / each);

@@ -24,17 +24,24 @@ namespace gdn {
 namespace scan {
 
 constexpr int kSpan = GDN_SCAN_SPAN;   // tokens between checkpoints
-constexpr int kLanes = 8;              // lanes across a slice's channels
-constexpr int kRuns = 64 / kLanes;     // lane groups, a run of tokens each
-constexpr int kWaves = 16;             // waves a workgroup, a span each: a tile
+constexpr int kRun = 8;                // tokens a lane joins by itself
+constexpr int kWaves = 16;             // waves a workgroup, each with a span of its own: a tile
 constexpr int kBackWaves = 8;          // the same in the gradients, which take twice the registers
-constexpr int kRun = kSpan / kRuns;    // tokens a run: a wave has a span
-constexpr int kTile = kWaves * kSpan, kBackTile = kBackWaves * kSpan;
 
-template <typename E> struct Shape {
-  static constexpr int V = 4 / sizeof(E);   // channels a lane
-  static constexpr int N = kLanes * V;      // channels a slice
+// How a wave lies over rows and channels: LANES lanes across a slice, four bytes each, and groups of
+// lanes with a run of consecutive tokens each.
+template <int LANES> struct Geo {
+  static constexpr int kRuns = 64 / LANES;
+  static constexpr int kTokens = kRuns * kRun;   // of a wave
+  static constexpr int kRow = 4 * LANES;         // bytes of a slice's row
+  static constexpr int kApart = 16 / kRuns;      // lanes from group to group
+  template <typename E> static constexpr int kChannels = kRow / int(sizeof(E));
 };
+// The forward pass reads whole lines of 128 bytes, where a CU's loads under way hold the most; the
+// gradients' waves have a checkpoint's span, whose states before each token they form alone.
+constexpr int kLanes = 32, kBackLanes = 8;
+constexpr int kTile = kWaves * Geo<kLanes>::kTokens, kBackTile = kBackWaves * Geo<kBackLanes>::kTokens;
+static_assert(Geo<kBackLanes>::kTokens == kSpan, "a checkpoint is the state before a wave's tokens");
 
 // 1 - e^y for y <= 0 (and what it is above), to a few steps of its own: a series where the
 // difference would cancel.
@@ -131,34 +138,38 @@ struct Pass {
 
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
-// A buffer of `rows` rows of `width` bytes from `base` on, `ld` bytes apart; none for rows <= 0.
+// A buffer of `rows` rows (at most `most`, up to 64) of `width` bytes from `base` on, `ld` bytes
+// apart; none for rows <= 0.
 // Loads behind its last row give zero, stores are dropped. Strides are at most 2^26 bytes, so
 // a span's offsets fit in 32 bits.
-__device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_t rows, uint32_t width) {
+__device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_t rows, int most, uint32_t width) {
   auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
   const uint64_t from = reinterpret_cast<uintptr_t>(base);
-  const uint32_t bytes = rows > 0 ? uint32_t(rows < kSpan ? rows - 1 : kSpan - 1) * uint32_t(ld) + width : 0u;
+  const uint32_t bytes = rows > 0 ? uint32_t(rows < most ? rows - 1 : most - 1) * uint32_t(ld) + width : 0u;
   return {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(bytes), 0x00020000u};
 }
 
 // Rows on their way from memory to LDS, ahead of their use: 32 bytes a row of a slice,
 // a wave's own span, so that nothing but its own count of loads says when they are there. Lane l
-// of a load brings sixteen bytes to the wave's place 16 l: row (l / 2 % 8) * 8 + l / 16 (and four
-// on), so that the eight runs' rows r lie side by side, at 256 r + 32 run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
+// of a load brings sixteen bytes to the wave's place 16 l: the rows r of the runs lie side
+// by side there, at 256 r + kRow run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
 // the compiler's own counts only ever wait for more.
-struct Feed {
+template <int LANES> struct Feed {
+  static constexpr int kRuns = Geo<LANES>::kRuns;
   uint32_t off[4];
   int64_t ld[4];
   const char* base[4];
-  // a lane's place in a span for sixteen bytes
+  // a lane's place in a span for sixteen bytes, and in its row
+  static __device__ __forceinline__ uint32_t column(int lane) { return lane % (LANES / 4) * 16; }
   static __device__ __forceinline__ uint32_t place(int lane, int64_t ld) {
-    return uint32_t((lane / 2 % 8) * 8 + lane / 16) * uint32_t(ld) + lane % 2 * 16;
+    const int p = lane / (LANES / 4);
+    return uint32_t((p % kRuns) * kRun + p / kRuns) * uint32_t(ld) + column(lane);
   }
   __device__ __forceinline__ void open(int k, const void* p, int64_t ld_, int64_t first, int lane) {
     base[k] = static_cast<const char*>(p) + first, ld[k] = ld_, off[k] = place(lane, ld_);
   }
   __device__ __forceinline__ void load(int k, char* to, int64_t t0, int64_t left, uint32_t width) const {
-    const uint4v range = rows_from(base[k] + t0 * ld[k], ld[k], left, width);
+    const uint4v range = rows_from(base[k] + t0 * ld[k], ld[k], left, Geo<LANES>::kTokens, width);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to))));
     asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(off[k]), "s"(range) : "memory");
     asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds + 1024), "v"(off[k] + 4 * uint32_t(ld[k])), "s"(range) : "memory");
@@ -166,7 +177,7 @@ struct Feed {
 };
 // Four bytes a lane, one load.
 __device__ __forceinline__ void load_words(char* to, const char* from, uint32_t bytes, int lane) {
-  const uint4v range = rows_from(from, 0, bytes > 0 ? 1 : 0, bytes);
+  const uint4v range = rows_from(from, 0, bytes > 0 ? 1 : 0, 1, bytes);
   const uint32_t lds = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to))));
   asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(lane * 4), "s"(range) : "memory");
 }
@@ -200,20 +211,22 @@ __device__ __forceinline__ uint32_t packed(const float* x) {
   }
 }
 // A lane's place among the rows r of a span in LDS, and its channels.
-struct Lane {
+template <int LANES> struct Lane {
+  static constexpr int kApart = Geo<LANES>::kApart;
   int run, slot;
-  __device__ __forceinline__ Lane(int lane) : run(lane / 2 % 8), slot(lane / 16 * 2 + lane % 2) {}
-  __device__ __forceinline__ uint32_t at(int r) const { return 256 * r + 32 * run + 4 * slot; }
+  __device__ __forceinline__ Lane(int lane) : run(lane / kApart % Geo<LANES>::kRuns), slot(lane / 16 * kApart + lane % kApart) {}
+  __device__ __forceinline__ uint32_t at(int r) const { return 256 * r + Geo<LANES>::kRow * run + 4 * slot; }
 };
 
-// A span's rows by way of LDS, laid as they came, in two stores: half of a slice of sixteen bytes
-// and rows that are not there lie behind the buffer.
-__device__ __forceinline__ void store_span(char* by, char* base, int64_t ld, int64_t left, uint32_t width, const Lane& l, int lane,
+// A wave's rows by way of LDS, laid as they came, in two stores: channels behind the last and rows
+// that are not there lie behind the buffer.
+template <int LANES>
+__device__ __forceinline__ void store_span(char* by, char* base, int64_t ld, int64_t left, uint32_t width, const Lane<LANES>& l, int lane,
                                            const uint32_t* x) {
 #pragma unroll
   for (int r = 0; r < kRun; ++r) *reinterpret_cast<uint32_t*>(by + l.at(r)) = x[r];
-  const auto to = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(rows_from(base, ld, left, width)[2]), 0x00020000);
-  const uint32_t at = lane % 2 * 16 < width ? Feed::place(lane, ld) : 0x80000000u;
+  const auto to = __builtin_amdgcn_make_buffer_rsrc(base, 0, int(rows_from(base, ld, left, Geo<LANES>::kTokens, width)[2]), 0x00020000);
+  const uint32_t at = Feed<LANES>::column(lane) < width ? Feed<LANES>::place(lane, ld) : 0x80000000u;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const uint4v*>(by + 1024 * j + 16 * lane), to, at + j * 4 * uint32_t(ld), 0, 0);
@@ -244,16 +257,16 @@ __device__ __forceinline__ Run beside(const Run& r) {
   return {beside<N, BACK>(r.A, 1.0f), beside<N, BACK>(r.C, 0.0f), beside<N, BACK>(r.H, 0.0f)};
 }
 
-// Joins over the lane groups, which lie two lanes apart: own becomes the runs up to and with the
+// Joins over the lane groups, own becomes the runs up to and with the
 // lane's (BACK: from the last one down to it), before those without it.
-template <int V, bool BACK>
+template <int V, int LANES, bool BACK>
 __device__ __forceinline__ void join_lanes(Run* own, Run* before) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    own[v] = join(beside<2, BACK>(own[v]), own[v]);
-    own[v] = join(beside<4, BACK>(own[v]), own[v]);
+    if constexpr (Geo<LANES>::kRuns >= 8) own[v] = join(beside<2, BACK>(own[v]), own[v]);
+    if constexpr (Geo<LANES>::kRuns >= 4) own[v] = join(beside<4, BACK>(own[v]), own[v]);
     own[v] = join(beside<8, BACK>(own[v]), own[v]);
-    before[v] = beside<2, BACK>(own[v]);
+    before[v] = beside<Geo<LANES>::kApart, BACK>(own[v]);
   }
 }
 
@@ -264,62 +277,78 @@ template <int N, int NW> struct Exchange {
   float before[NW][N];
 };
 
-// The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes, whose
-// lanes are the waves (BACK: from the last).
+// The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes (in
+// turns, where there are more than four), whose lanes are the waves (BACK: from the last).
 template <int N, int NW, bool BACK> struct Keeper {
-  static constexpr int kOwn = N < NW ? 1 : N / NW;
-  int ch, from;   // channel of the slice, and the wave whose run the lane takes
-  bool on;
-  __device__ __forceinline__ Keeper(int wave, int lane) {
-    ch = wave * kOwn + lane / 16;
+  static constexpr int kOwn = N < NW ? 1 : N / NW, kTurns = kOwn <= 4 ? 1 : kOwn / 4;
+  int base, from, channels;   // first channel of the slice, the wave whose run the lane takes, channels there are
+  bool on, first;
+  State carry[kTurns];
+  __device__ __forceinline__ Keeper(int wave, int lane, int channels_) : channels(channels_) {
+    base = wave * kOwn + lane / 16;
     from = BACK ? NW - 1 - lane % 16 : lane % 16;
-    on = lane / 16 < kOwn && ch < N;
+    on = lane / 16 < kOwn && base < N;
+    first = on && lane % 16 == 0;
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) carry[t] = {0.0f, 0.0f};
   }
-  __device__ __forceinline__ bool first(int lane) const { return on && lane % 16 == 0; }
-  // Passes the carried state over a tile; gives each wave its own, and the tile's run.
-  __device__ __forceinline__ Run pass(Exchange<N, NW>& x, State& carry, int lane) const {
-    Run r = empty_run();
-    if (lane % 16 < NW) {
-      const float4 t = x.runs[ch][from];
-      r = {t.x, t.y, t.z};
+  // f(turn, channel) for each of the lane's channels that there are
+  template <typename F>
+  __device__ __forceinline__ void all(F f) const {
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t)
+      if (on && base + 4 * t < channels) f(t, base + 4 * t);
+  }
+  // Passes the carried state over a tile; gives each wave its own, and joins the tile to `total`.
+  template <bool TOTALS>
+  __device__ __forceinline__ void pass(Exchange<N, NW>& x, int lane, Run* total) {
+    if (!on) return;
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      Run r = empty_run();
+      if (lane % 16 < NW) {
+        const float4 q = x.runs[base + 4 * t][from];
+        r = {q.x, q.y, q.z};
+      }
+      r = join(beside<1, false>(r), r);
+      r = join(beside<2, false>(r), r);
+      r = join(beside<4, false>(r), r);
+      if constexpr (NW > 8) r = join(beside<8, false>(r), r);
+      State s = carry[t];
+      s.pass(beside<1, false>(r));
+      if (lane % 16 < NW) x.before[from][base + 4 * t] = s.value();
+      const int end = (lane & 48) + NW - 1;
+      r = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
+      carry[t].pass(r);
+      if constexpr (TOTALS) total[t] = join(total[t], r);
     }
-    r = join(beside<1, false>(r), r);
-    r = join(beside<2, false>(r), r);
-    r = join(beside<4, false>(r), r);
-    if constexpr (NW > 8) r = join(beside<8, false>(r), r);
-    State s = carry;
-    s.pass(beside<1, false>(r));
-    if (lane % 16 < NW) x.before[from][ch] = s.value();
-    const int end = (lane & 48) + NW - 1;
-    r = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
-    carry.pass(r);
-    return r;
   }
 };
 
 // Forward. TOTALS: only what each segment but the last makes of the state before it.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N, NT = IG ? 3 : 2;
-  __shared__ __attribute__((aligned(16))) char raw[kWaves][NT][32 * kSpan];
-  __shared__ __attribute__((aligned(16))) char out[kWaves][TOTALS ? 16 : 32 * kSpan];
+  constexpr int V = 4 / int(sizeof(E)), N = Geo<kLanes>::kChannels<E>, NT = IG ? 3 : 2, kTokens = Geo<kLanes>::kTokens;
+  __shared__ __attribute__((aligned(16))) char raw[kWaves][NT][64 * 4 * kRun];
+  __shared__ __attribute__((aligned(16))) char out[kWaves][TOTALS ? 16 : 64 * 4 * kRun];
   __shared__ Exchange<N, kWaves> exchange;
   const Place at(p, TOTALS ? p.segs - 1 : p.segs);
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const Lane l(lane);
-  const Keeper<N, kWaves, false> keeper(wave, lane);
+  const Lane<kLanes> l(lane);
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);   // a slice may end behind C
-  const bool keeps = keeper.on && uint32_t(keeper.ch) < channels;
+  typedef Keeper<N, kWaves, false> Keep;
+  Keep keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   if (begin >= n && at.seg > 0) return;
   const bool last = n - begin <= p.seg;
-  if (TOTALS && at.seg == 0 && keeps && keeper.first(lane)) p.start[cb + keeper.ch] = p.h0 != nullptr ? p.h0[cb + keeper.ch] : 0.0f;
+  if (TOTALS && at.seg == 0 && keeper.first)
+    keeper.all([&](int, int ch) { p.start[cb + ch] = p.h0 != nullptr ? p.h0[cb + ch] : 0.0f; });
   if (TOTALS && last) return;
   const int64_t end = last ? n : begin + p.seg;
-  Feed feed;
+  Feed<kLanes> feed;
   feed.open(0, p.x, p.ldx, at.b * p.T * p.ldx + c0 * int64_t(sizeof(E)), lane);
   feed.open(1, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
   if constexpr (IG) feed.open(2, p.i, p.ldi, at.b * p.T * p.ldi + c0 * int64_t(sizeof(E)), lane);
@@ -327,16 +356,19 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
 #pragma unroll
     for (int k = 0; k < NT; ++k) feed.load(k, raw[wave][k], t0, end - t0, width);
   };
-  const int64_t first = begin + wave * kSpan, tiles = (end - begin + kTile - 1) / kTile;
+  const int64_t first = begin + wave * kTokens, tiles = (end - begin + kTile - 1) / kTile;
   fetch(first);
   const int64_t ldh = p.C * sizeof(E);
   char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * int64_t(sizeof(E));
-  State carry = {0.0f, 0.0f};
-  Run total = empty_run();
-  if (!TOTALS && keeps) {
+  Run total[Keep::kTurns];
+#pragma unroll
+  for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
+  if constexpr (!TOTALS) {
     const float* from = p.segs > 1 ? p.start : p.h0;
-    if (from != nullptr) carry.hi = from[cb + keeper.ch];
-    for (unsigned s = 0; s < at.seg; ++s) carry.pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + keeper.ch]);
+    keeper.all([&](int t, int ch) {
+      if (from != nullptr) keeper.carry[t].hi = from[cb + ch];
+      for (unsigned s = 0; s < at.seg; ++s) keeper.carry[t].pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + ch]);
+    });
   }
   float decay[V];
 #pragma unroll
@@ -375,22 +407,19 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) settle(own[v]);
-    join_lanes<V, false>(own, before);
-    if (l.run == kRuns - 1) {
+    join_lanes<V, kLanes, false>(own, before);
+    if (l.run == Geo<kLanes>::kRuns - 1) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
     }
     __syncthreads();
-    if (keeper.on) {
-      const Run all = keeper.pass(exchange, carry, lane);
-      if constexpr (TOTALS) total = join(total, all);
-    }
+    keeper.template pass<TOTALS>(exchange, lane, total);
     __syncthreads();
     if constexpr (!TOTALS) {
       float y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) y[v] = fmaf(before[v].A, exchange.before[wave][l.slot * V + v], before[v].H);
-      if (p.marks != nullptr && l.run == 0 && uint32_t(l.slot * V) < channels && left > 0) {
+      if (p.marks != nullptr && l.run == 0 && uint32_t(l.slot * V) < channels && left > 0 && t0 % kSpan == 0) {
         float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + l.slot * V;
 #pragma unroll
         for (int v = 0; v < V; ++v) m[v] = y[v];
@@ -411,11 +440,13 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   for (; (k + 1) * kTile <= end - begin; ++k) walk(std::true_type{}, k);
   if (k < tiles) walk(std::false_type{}, k);
   wait_memory<0>();   // of LDS that the next workgroup may get
-  if (!keeps || !keeper.first(lane)) return;
-  if constexpr (TOTALS)
-    p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + keeper.ch] = {total.A, total.C, carry.value()};
-  else if (last && p.h_final != nullptr)
-    p.h_final[cb + keeper.ch] = carry.value();
+  if (!keeper.first) return;
+  keeper.all([&](int t, int ch) {
+    if constexpr (TOTALS)
+      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch] = {total[t].A, total[t].C, keeper.carry[t].value()};
+    else if (last && p.h_final != nullptr)
+      p.h_final[cb + ch] = keeper.carry[t].value();
+  });
 }
 
 // Gradients, from a sequence's end: with G_t = a_t (d_h_t + G_{t+1}) the same recurrence, whose
@@ -423,21 +454,22 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
 // only what each segment but the first makes of the gradient behind it.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
-  constexpr int V = Shape<E>::V, N = Shape<E>::N, R = kRun;
+  constexpr int V = 4 / int(sizeof(E)), N = Geo<kBackLanes>::kChannels<E>, R = kRun, kRuns = Geo<kBackLanes>::kRuns;
   constexpr int NT = TOTALS ? 2 : IG ? 4 : 3, kLoads = 2 * NT + (TOTALS ? 0 : 1), kStores = TOTALS ? 0 : IG ? 6 : 4;
-  __shared__ __attribute__((aligned(16))) char raw[2][kBackWaves][NT][32 * kSpan];
+  __shared__ __attribute__((aligned(16))) char raw[2][kBackWaves][NT][64 * 4 * kRun];
   __shared__ __attribute__((aligned(16))) char raw_marks[2][kBackWaves][TOTALS ? 16 : 256];
-  __shared__ __attribute__((aligned(16))) char out[kBackWaves][TOTALS ? 16 : 32 * kSpan];
+  __shared__ __attribute__((aligned(16))) char out[kBackWaves][TOTALS ? 16 : 64 * 4 * kRun];
   __shared__ Exchange<N, kBackWaves> exchange;
   Place at(p, TOTALS ? p.segs - 1 : p.segs);
   if (TOTALS) ++at.seg;
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const Lane l(lane);
-  const Keeper<N, kBackWaves, true> keeper(wave, lane);
+  const Lane<kBackLanes> l(lane);
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);
-  const bool keeps = keeper.on && uint32_t(keeper.ch) < channels, own_lane = uint32_t(l.slot * V) < channels;
+  const bool own_lane = uint32_t(l.slot * V) < channels;
+  typedef Keeper<N, kBackWaves, true> Keep;
+  Keep keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
@@ -454,7 +486,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
   }
   if (TOTALS && begin >= n) return;
-  Feed feed;
+  Feed<kBackLanes> feed;
   feed.open(0, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
   feed.open(1, p.d_h, ldh, row0, lane);
   if constexpr (!TOTALS) feed.open(2, p.x, p.ldx, at.b * p.T * p.ldx + c0 * int64_t(sizeof(E)), lane);
@@ -478,12 +510,15 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   float decay[V], sum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f, sum[v] = 0.0f;
-  State carry = {0.0f, 0.0f};
-  Run total = empty_run();
-  if (!TOTALS && keeps) {
-    if (p.d_final != nullptr) carry.hi = p.d_final[cb + keeper.ch];
-    for (int64_t s = (n + p.seg - 1) / p.seg - 1; s > int64_t(at.seg); --s)
-      carry.pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + keeper.ch]);
+  Run total[Keep::kTurns];
+#pragma unroll
+  for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
+  if constexpr (!TOTALS) {
+    keeper.all([&](int t, int ch) {
+      if (p.d_final != nullptr) keeper.carry[t].hi = p.d_final[cb + ch];
+      for (int64_t s = (n + p.seg - 1) / p.seg - 1; s > int64_t(at.seg); --s)
+        keeper.carry[t].pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + ch]);
+    });
   }
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
@@ -538,7 +573,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
 #pragma unroll
         for (int r = 0; r < R; ++r) fwd[v].H = fmaf(gate[r][v].a, fwd[v].H, before[r][v]);
       }
-      join_lanes<V, false>(fwd, ahead);
+      join_lanes<V, kBackLanes, false>(fwd, ahead);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float y = fmaf(ahead[v].A, mark[v], ahead[v].H);
@@ -552,16 +587,13 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) settle(own[v]);
-    join_lanes<V, true>(own, lanes);
+    join_lanes<V, kBackLanes, true>(own, lanes);
     if (l.run == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
     }
     __syncthreads();
-    if (keeper.on) {
-      const Run all = keeper.pass(exchange, carry, lane);
-      if constexpr (TOTALS) total = join(total, all);
-    }
+    keeper.template pass<TOTALS>(exchange, lane, total);
     __syncthreads();
     if constexpr (!TOTALS) {
       float G[V];
@@ -605,16 +637,18 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   for (; k < tiles; ++k) walk(std::true_type{}, k);
   wait_memory<0>();
   if constexpr (TOTALS) {
-    if (keeps && keeper.first(lane))
-      p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + keeper.ch] = {total.A, total.C, carry.value()};
+    if (keeper.first)
+      keeper.all([&](int t, int ch) {
+        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch] = {total[t].A, total[t].C, keeper.carry[t].value()};
+      });
   } else {
-    if (at.seg == 0 && p.dh0 != nullptr && keeps && keeper.first(lane)) p.dh0[cb + keeper.ch] = carry.value();
+    if (at.seg == 0 && p.dh0 != nullptr && keeper.first) keeper.all([&](int t, int ch) { p.dh0[cb + ch] = keeper.carry[t].value(); });
     if (KIND == GDN_SCAN_POWER && p.ddecay != nullptr) {
       // over the lane groups, then the waves
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int m = 2; m < 16; m *= 2) sum[v] += __shfl_xor(sum[v], m);
+        for (int m = Geo<kBackLanes>::kApart; m < 16; m *= 2) sum[v] += __shfl_xor(sum[v], m);
       }
       __syncthreads();
       if (l.run == 0) {
@@ -688,7 +722,8 @@ int launch_step(const ScanProblem& q, const Pass& p, hipStream_t s) {
 // BACK: the gradients. Segments side by side take a first launch for their totals.
 template <typename E, bool BACK>
 int launch_pass(const ScanProblem& q, Pass p, hipStream_t s) {
-  const int64_t slices = (q.a.C + Shape<E>::N - 1) / Shape<E>::N;
+  constexpr int N = Geo<BACK ? kBackLanes : kLanes>::template kChannels<E>;
+  const int64_t slices = (q.a.C + N - 1) / N;
   p.slices = unsigned(slices);
   return by_gate(q.a, [&](auto kind, auto gated) {
     constexpr int K = decltype(kind)::value;

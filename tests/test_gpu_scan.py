@@ -27,6 +27,7 @@ def _device(case, wide):
 def test_scan(case, dt, gate, igate):
     import gated_delta_rule_69_amd as gdn
     from block_util import host, lengths, scan_case
+    from gated_delta_rule_69_amd._block import SCAN_SPAN as SPAN
     from layer_util import check, f64
     B, T, C, lens = case
     print(f"scan {case} {dt} {gate} igate={igate}", flush=True)
@@ -45,8 +46,8 @@ def test_scan(case, dt, gate, igate):
     for b in range(B):
         n = T if lens is None else min(max(lens[b], 0), T)
         assert torch.equal(given[b, :n], out[b, :n]) and (given[b, n:] == 7.0).all() and (out[b, n:] == 0).all()
-        for j in range(-(-n // 64)):
-            before = want[b, 64 * j - 1] if j else (np.zeros(C) if h["h0"] is None else h["h0"][b])
+        for j in range(-(-n // SPAN)):
+            before = want[b, SPAN * j - 1] if j else (np.zeros(C) if h["h0"] is None else h["h0"][b])
             np.testing.assert_allclose(f64(marks[b, j]), before, rtol=0, atol=1e-5 * max(1, abs(want).max()))
     # gradients, with the checkpoints and without
     ref["h0"] = h["h0"]
