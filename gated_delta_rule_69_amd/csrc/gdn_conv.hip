@@ -14,6 +14,8 @@ namespace {
 
 constexpr int kAcross = 32, kDown = 8, kThreads = kAcross * kDown;
 constexpr int kStep = 4;   // rows whose loads are under way together
+constexpr int kBackChannels = 4;   // channels a thread in the gradients: eight would take 210 registers, two waves a SIMD
+constexpr int64_t kFew = 8;   // tokens that go one by one
 
 struct Conv {
   const void* x;
@@ -134,12 +136,65 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a) {
   }
 }
 
+// A few tokens a sequence: G sequences a thread, so that the weights (16 bytes a channel of four
+// taps, as much as a token's rows) are read once for them, and their rows are under way together.
+template <typename E, int W, bool SILU, int G>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, int64_t B) {
+  constexpr int N = 16 / sizeof(E);
+  typedef vec<E, N> Row;
+  const unsigned col = blockIdx.x % a.columns, q = blockIdx.x / a.columns;
+  const int64_t c = (int64_t(col) * kAcross + threadIdx.x % kAcross) * N;
+  if (c >= a.C) return;
+  const int64_t first = (int64_t(q) * kDown + threadIdx.x / kAcross) * G;
+  float w[W][N], bias[N];
+  load_weights<W, N>(a, c, w, bias);
+  Row past[G][W - 1], now[G];
+  int64_t n[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int64_t b = first + g;
+    n[g] = b < B ? tokens_of(a.lens, b, a.T) : 0;
+    now[g] = Row{};
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) past[g][j] = Row{};
+    if (b >= B) continue;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) past[g][j] = input_row<E, W, N>(a, b, j - (W - 1), c);
+    if (n[g] > 0) now[g] = input_row<E, W, N>(a, b, 0, c);
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int64_t b = first + g;
+    for (int64_t t = 0; t < n[g]; ++t) {
+      if (t > 0) now[g] = input_row<E, W, N>(a, b, t, c);
+      float out[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float z = bias[i];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][i], float(past[g][j][i]), z);
+        z = fmaf(w[W - 1][i], float(now[g][i]), z);
+        out[i] = SILU ? z * sigmoid_of<E>(z) : z;
+      }
+      store_row<E, N>(static_cast<E*>(a.y) + (b * a.T + t) * a.C + c, out);
+#pragma unroll
+      for (int j = 0; j + 1 < W - 1; ++j) past[g][j] = past[g][j + 1];
+      past[g][W - 2] = now[g];
+    }
+    if (b < B && a.s_final != nullptr && (n[g] > 0 || a.s_final != a.s0)) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        *reinterpret_cast<Row*>(static_cast<E*>(a.s_final) + (b * (W - 1) + j) * a.C + c) = past[g][j];
+    }
+  }
+}
+
 // Gradients: dz_t = d_y_t act'(z_t), dx_t = sum_j w_j dz_{t + W - 1 - j}, dw_j = sum_t dz_t
 // x_{t - W + 1 + j}. A run forms the dz of its own tokens and of the W - 1 behind it; those of
 // its own go into the workgroup's sums for the weights.
 template <typename E, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(Conv a) {
-  constexpr int N = 16 / sizeof(E);
+  constexpr int N = kBackChannels;
   typedef vec<E, N> Row;
   const unsigned col = blockIdx.x % a.columns, q = blockIdx.x / a.columns;
   const unsigned down = q % a.runs;
@@ -163,13 +218,15 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(Conv a) {
     const E* dy = static_cast<const E*>(a.d_y) + b * a.T * a.C + c;
     E* dx = static_cast<E*>(a.dx) + b * a.T * a.C + c;
     const int64_t mine = std::min(stop, n);   // tokens from here on are another run's, or none
-    for (int64_t t = begin; t < stop + W - 1; t += kStep) {
+    // INSIDE: kStep tokens of the run's own whose rows' gradients are the run's too
+    auto step = [&](auto inside, int64_t t) {
+      constexpr bool INSIDE = decltype(inside)::value;
       Row rx[kStep], rd[kStep];
 #pragma unroll
       for (int k = 0; k < kStep; ++k) {
-        const int64_t at = std::min(t + k, n - 1);
         rx[k] = rd[k] = Row{};
-        if (n > 0) {
+        if (INSIDE || n > 0) {
+          const int64_t at = INSIDE ? t + k : std::min(t + k, n - 1);
           rx[k] = *reinterpret_cast<const Row*>(x + at * a.ldx);
           rd[k] = *reinterpret_cast<const Row*>(dy + at * a.C);
         }
@@ -190,13 +247,12 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(Conv a) {
             sigmoids<E>(z, &s, &rest);
             g[i] *= s * (1.0f + z * rest);
           }
-          g[i] = here < n ? g[i] : 0.0f;
-          const float add = here < mine ? g[i] : 0.0f;
-          if (here < mine) {
+          if (!INSIDE) g[i] = here < n ? g[i] : 0.0f;
+          if (INSIDE || here < mine) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) sums[j][i] = fmaf(add, past[j][i], sums[j][i]);
-            sums[W - 1][i] = fmaf(add, now[i], sums[W - 1][i]);
-            sums[W][i] += add;
+            for (int j = 0; j < W - 1; ++j) sums[j][i] = fmaf(g[i], past[j][i], sums[j][i]);
+            sums[W - 1][i] = fmaf(g[i], now[i], sums[W - 1][i]);
+            sums[W][i] += g[i];
           }
           // row `to` is read by tokens to .. to + W - 1 through w[W - 1] .. w[0]
           float d = w[0][i] * g[i];
@@ -207,25 +263,34 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(Conv a) {
           for (int j = 0; j + 1 < W - 1; ++j) past[j][i] = past[j + 1][i], dz[j][i] = dz[j + 1][i];
           past[W - 2][i] = now[i], dz[W - 2][i] = g[i];
         }
-        if (to >= stop || (to < begin && r > 0)) continue;
-        // the final state's rows are inputs n - W + 1 .. n - 1
-        const int64_t j = to - (n - (W - 1));
-        if (a.d_s != nullptr && j >= 0 && j < W - 1) {
-          float up[N];
-          unpack<E, N>(*reinterpret_cast<const Row*>(static_cast<const E*>(a.d_s) + (b * (W - 1) + j) * a.C + c), up);
-#pragma unroll
-          for (int i = 0; i < N; ++i) out[i] += up[i];
-        }
-        if (to >= n) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) out[i] = 0.0f;
-        }
-        if (to >= 0)
+        if constexpr (INSIDE) {
           store_row<E, N>(dx + to * a.C, out);
-        else if (a.ds0 != nullptr && to >= -(W - 1))
-          store_row<E, N>(static_cast<E*>(a.ds0) + (b * (W - 1) + to + W - 1) * a.C + c, out);
+        } else {
+          if (to >= stop || (to < begin && r > 0)) continue;
+          // the final state's rows are inputs n - W + 1 .. n - 1
+          const int64_t j = to - (n - (W - 1));
+          if (a.d_s != nullptr && j >= 0 && j < W - 1) {
+            float up[N];
+            unpack<E, N>(*reinterpret_cast<const Row*>(static_cast<const E*>(a.d_s) + (b * (W - 1) + j) * a.C + c), up);
+#pragma unroll
+            for (int i = 0; i < N; ++i) out[i] += up[i];
+          }
+          if (to >= n) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) out[i] = 0.0f;
+          }
+          if (to >= 0)
+            store_row<E, N>(dx + to * a.C, out);
+          else if (a.ds0 != nullptr && to >= -(W - 1))
+            store_row<E, N>(static_cast<E*>(a.ds0) + (b * (W - 1) + to + W - 1) * a.C + c, out);
+        }
       }
-    }
+    };
+    // the final state's gradient meets rows from n - W + 1 on, with tokens n and behind
+    int64_t t = begin;
+    step(std::false_type{}, t);
+    for (t += kStep; t + kStep <= mine; t += kStep) step(std::true_type{}, t);
+    for (; t < stop + W - 1; t += kStep) step(std::false_type{}, t);
   }
   if (a.partial == nullptr) return;
   // over the workgroup's runs, in order
@@ -246,25 +311,26 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(Conv a) {
   }
 }
 
-int64_t columns_of(const gdn_conv_args& a) {
-  return (a.C * (a.dtype == GDN_DTYPE_BF16 ? 2 : 4) + 16 * kAcross - 1) / (16 * kAcross);
+int64_t columns_of(const gdn_conv_args& a, bool back) {
+  const int64_t channels = kAcross * (back || a.dtype == GDN_DTYPE_F32 ? 4 : 8);
+  return (a.C + channels - 1) / channels;
 }
 int64_t runs_of(const gdn_conv_args& a, int64_t run) { return std::max<int64_t>(1, (a.T + run * kDown - 1) / (run * kDown)); }
 // Tokens a run: long ones read fewer rows twice, short ones give every CU its threads. A launch
 // has fewer than 2^32 threads (B * C <= 2^24 keeps the workgroups of one run each under 2^22).
-int64_t run_of(const gdn_conv_args& a) {
+int64_t run_of(const gdn_conv_args& a, bool back) {
   int64_t run = 32;
-  while (run > 8 && a.B * columns_of(a) * runs_of(a, run) < 1024) run /= 2;
-  while (a.B * columns_of(a) * runs_of(a, run) > 1 << 22 && runs_of(a, run) > 1) run *= 2;
+  while (run > 8 && a.B * columns_of(a, back) * runs_of(a, run) < 1024) run /= 2;
+  while (a.B * columns_of(a, back) * runs_of(a, run) > 1 << 22 && runs_of(a, run) > 1) run *= 2;
   return run;
 }
 
-Conv conv_of(const gdn_conv_args& a) {
+Conv conv_of(const gdn_conv_args& a, bool back) {
   Conv k{};
   k.x = a.x, k.w = a.w, k.bias = a.bias, k.lens = a.seq_lens, k.y = a.y;
   k.T = a.T, k.C = a.C, k.ldx = a.x_stride;
-  k.run = run_of(a);
-  k.columns = unsigned(columns_of(a));
+  k.run = run_of(a, back);
+  k.columns = unsigned(columns_of(a, back));
   k.runs = unsigned(runs_of(a, k.run));
   k.blocks = unsigned(a.B * k.columns * k.runs);
   return k;
@@ -289,8 +355,23 @@ int by_width(const gdn_conv_args& a, F f) {
 
 int launch_conv_fwd(const ConvProblem& p, const void* s0, void* s_final, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  Conv k = conv_of(p.a);
+  Conv k = conv_of(p.a, false);
   k.s0 = s0, k.s_final = s_final;
+  if (p.a.T <= kFew) {
+    const int64_t B = p.a.B;
+    return by_width(p.a, [&](auto type, auto width, auto silu) {
+      typedef decltype(type) E;
+      constexpr int W = decltype(width)::value;
+      constexpr bool S = decltype(silu)::value;
+      // four sequences a thread where that leaves every CU two workgroups
+      const int64_t four = (B + 4 * kDown - 1) / (4 * kDown) * k.columns;
+      if (four >= 512)
+        conv_step_kernel<E, W, S, 4><<<unsigned(four), kThreads, 0, s>>>(k, B);
+      else
+        conv_step_kernel<E, W, S, 1><<<unsigned((B + kDown - 1) / kDown * k.columns), kThreads, 0, s>>>(k, B);
+      return int(hipGetLastError());
+    });
+  }
   return by_width(p.a, [&](auto type, auto width, auto silu) {
     conv_kernel<decltype(type), decltype(width)::value, decltype(silu)::value><<<k.blocks, kThreads, 0, s>>>(k);
     return int(hipGetLastError());
@@ -298,13 +379,13 @@ int launch_conv_fwd(const ConvProblem& p, const void* s0, void* s_final, void* s
 }
 
 size_t conv_bwd_workspace(const ConvProblem& p) {
-  return std::max<size_t>(256, size_t(p.a.B) * runs_of(p.a, run_of(p.a)) * p.a.C * (p.a.W + 1) * sizeof(float));
+  return std::max<size_t>(256, size_t(p.a.B) * runs_of(p.a, run_of(p.a, true)) * p.a.C * (p.a.W + 1) * sizeof(float));
 }
 
 int launch_conv_bwd(const ConvProblem& p, const void* d_y, const void* d_s_final, const gdn_conv_grads& g, void* ws,
                     void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  Conv k = conv_of(p.a);
+  Conv k = conv_of(p.a, true);
   k.s0 = p.a.s0, k.d_y = d_y, k.d_s = d_s_final, k.dx = g.dx, k.ds0 = g.ds0;
   const bool sums = g.dw != nullptr || g.dbias != nullptr;
   k.partial = sums ? static_cast<float*>(ws) : nullptr;
