@@ -95,9 +95,10 @@ __device__ __forceinline__ Run join(const Run& first, const Run& then) {
   return {first.A * then.A, fmaf(then.C, first.A, first.C), fmaf(then.A, first.H, then.H)};
 }
 
-// The product of a run's rounded a's is off by a step for each of them, 1 - C by one: where a run
-// leaves more than half, that is its A.
-__device__ __forceinline__ void settle(Run& r) { r.A = r.C < 0.5f ? 1.0f - r.C : r.A; }
+// The product of rounded A's is off by a step for each of them, 1 - C by one: where a run leaves more
+// than half, that is its A.
+__device__ __forceinline__ Run settle(const Run& r) { return {r.C < 0.5f ? 1.0f - r.C : r.A, r.C, r.H}; }
+__device__ __forceinline__ Run join_settled(const Run& first, const Run& then) { return settle(join(first, then)); }
 
 // A state held as hi + lo.
 struct State {
@@ -188,14 +189,6 @@ __device__ __forceinline__ void wait_memory() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-// Before tile k: behind its LOADS loads came those of the tile after it and, from each of the two
-// tiles before, STORES stores (others only add to what is waited for).
-template <int LOADS, int STORES>
-__device__ __forceinline__ void wait_tile(int64_t k) {
-  if (STORES == 0 || k == 0) wait_memory<LOADS>();
-  else if (k == 1) wait_memory<LOADS + STORES>();
-  else wait_memory<LOADS + 2 * STORES>();
-}
 template <typename E>
 __device__ __forceinline__ float part_of(uint32_t raw, int v) {
   if constexpr (sizeof(E) == 4) return __uint_as_float(raw);
@@ -257,15 +250,16 @@ __device__ __forceinline__ Run beside(const Run& r) {
   return {beside<N, BACK>(r.A, 1.0f), beside<N, BACK>(r.C, 0.0f), beside<N, BACK>(r.H, 0.0f)};
 }
 
-// Joins over the lane groups, own becomes the runs up to and with the
-// lane's (BACK: from the last one down to it), before those without it.
-template <int V, int LANES, bool BACK>
+// Joins over the lane groups: own becomes the runs up to and with the lane's (BACK: from the last one
+// down to it), before those without it. Without C (AH) A is the product.
+template <int V, int LANES, bool BACK, bool AH>
 __device__ __forceinline__ void join_lanes(Run* own, Run* before) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if constexpr (Geo<LANES>::kRuns >= 8) own[v] = join(beside<2, BACK>(own[v]), own[v]);
-    if constexpr (Geo<LANES>::kRuns >= 4) own[v] = join(beside<4, BACK>(own[v]), own[v]);
-    own[v] = join(beside<8, BACK>(own[v]), own[v]);
+    auto take = [&](const Run& o) { own[v] = AH ? join(o, own[v]) : join_settled(o, own[v]); };
+    if constexpr (Geo<LANES>::kRuns >= 8) take(beside<2, BACK>(own[v]));
+    if constexpr (Geo<LANES>::kRuns >= 4) take(beside<4, BACK>(own[v]));
+    take(beside<8, BACK>(own[v]));
     before[v] = beside<Geo<LANES>::kApart, BACK>(own[v]);
   }
 }
@@ -299,33 +293,71 @@ template <int N, int NW, bool BACK> struct Keeper {
     for (int t = 0; t < kTurns; ++t)
       if (on && base + 4 * t < channels) f(t, base + 4 * t);
   }
-  // Passes the carried state over a tile; gives each wave its own, and joins the tile to `total`.
-  template <bool TOTALS>
-  __device__ __forceinline__ void pass(Exchange<N, NW>& x, int lane, Run* total) {
+  // Joins the runs of a row's lanes: up to and with the lane's, and of all.
+  static __device__ __forceinline__ Run join_row(Run r, int lane, Run* whole) {
+    r = join_settled(beside<1, false>(r), r);
+    r = join_settled(beside<2, false>(r), r);
+    r = join_settled(beside<4, false>(r), r);
+    r = join_settled(beside<8, false>(r), r);
+    const int end = lane | 15;
+    *whole = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
+    return r;
+  }
+  // The runs of a tile's waves.
+  __device__ __forceinline__ Run tile(const Exchange<N, NW>& x, int lane, int t, Run* whole) const {
+    Run r = empty_run();
+    if (lane % 16 < NW) {
+      const float4 q = x.runs[base + 4 * t][from];
+      r = {q.x, q.y, q.z};
+    }
+    return join_row(r, lane, whole);
+  }
+  // Passes the carried state over `count` segments, of(channel, k) the k-th to be passed: sixteen of
+  // them at a time, a lane each, for one after the other each would wait for its load.
+  template <typename F>
+  __device__ __forceinline__ void over(int64_t count, int lane, F of) {
+    for (int64_t first = 0; first < count; first += 16) {
+      if (!on) continue;
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) {
+        Run r = empty_run(), whole;
+        if (first + lane % 16 < count && base + 4 * t < channels) r = of(base + 4 * t, first + lane % 16);
+        join_row(r, lane, &whole);
+        carry[t].pass(whole);
+      }
+    }
+  }
+  // Passes the carried state over a tile; gives each wave its own.
+  __device__ __forceinline__ void pass(Exchange<N, NW>& x, int lane) {
     if (!on) return;
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-      Run r = empty_run();
-      if (lane % 16 < NW) {
-        const float4 q = x.runs[base + 4 * t][from];
-        r = {q.x, q.y, q.z};
-      }
-      r = join(beside<1, false>(r), r);
-      r = join(beside<2, false>(r), r);
-      r = join(beside<4, false>(r), r);
-      if constexpr (NW > 8) r = join(beside<8, false>(r), r);
+      Run whole;
+      const Run r = tile(x, lane, t, &whole);
       State s = carry[t];
       s.pass(beside<1, false>(r));
       if (lane % 16 < NW) x.before[from][base + 4 * t] = s.value();
-      const int end = (lane & 48) + NW - 1;
-      r = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
-      carry[t].pass(r);
-      if constexpr (TOTALS) total[t] = join(total[t], r);
+      carry[t].pass(whole);
     }
+  }
+  // Joins a tile before those of `total`; whether nothing of what lies before can be left.
+  __device__ __forceinline__ bool extend(const Exchange<N, NW>& x, int lane, Run* total) const {
+    bool gone = true;
+    if (on) {
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) {
+        Run whole;
+        tile(x, lane, t, &whole);
+        total[t] = join_settled(whole, total[t]);
+        gone = gone && (total[t].A == 0.0f || base + 4 * t >= channels);
+      }
+    }
+    return gone;
   }
 };
 
-// Forward. TOTALS: only what each segment but the last makes of the state before it.
+// Forward. TOTALS: only what each segment but the last makes of the state before it, from its end
+// backwards, as far as rows have a weight that float32 holds.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   constexpr int V = 4 / int(sizeof(E)), N = Geo<kLanes>::kChannels<E>, NT = IG ? 3 : 2, kTokens = Geo<kLanes>::kTokens;
@@ -353,10 +385,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   feed.open(1, p.f, p.ldf, at.b * p.T * p.ldf + c0 * int64_t(sizeof(E)), lane);
   if constexpr (IG) feed.open(2, p.i, p.ldi, at.b * p.T * p.ldi + c0 * int64_t(sizeof(E)), lane);
   auto fetch = [&](int64_t t0) {
+    const int64_t left = t0 < begin ? 0 : end - t0;
 #pragma unroll
-    for (int k = 0; k < NT; ++k) feed.load(k, raw[wave][k], t0, end - t0, width);
+    for (int k = 0; k < NT; ++k) feed.load(k, raw[wave][k], t0, left, width);
   };
-  const int64_t first = begin + wave * kTokens, tiles = (end - begin + kTile - 1) / kTile;
+  const int64_t tiles = (end - begin + kTile - 1) / kTile, step = TOTALS ? -kTile : kTile;
+  const int64_t first = begin + wave * kTokens + (TOTALS ? (tiles - 1) * kTile : 0);
   fetch(first);
   const int64_t ldh = p.C * sizeof(E);
   char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * int64_t(sizeof(E));
@@ -365,10 +399,8 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
   if constexpr (!TOTALS) {
     const float* from = p.segs > 1 ? p.start : p.h0;
-    keeper.all([&](int t, int ch) {
-      if (from != nullptr) keeper.carry[t].hi = from[cb + ch];
-      for (unsigned s = 0; s < at.seg; ++s) keeper.carry[t].pass(p.totals[(at.b * (p.segs - 1) + s) * p.C + c0 + ch]);
-    });
+    if (from != nullptr) keeper.all([&](int t, int ch) { keeper.carry[t].hi = from[cb + ch]; });
+    keeper.over(at.seg, lane, [&](int ch, int64_t k) { return p.totals[(at.b * (p.segs - 1) + k) * p.C + c0 + ch]; });
   }
   float decay[V];
 #pragma unroll
@@ -377,7 +409,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   // a tile whose rows are all there, or the last
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
-    const int64_t t0 = first + k * kTile, left = end - t0;
+    const int64_t t0 = first + k * step, left = end - t0;
     if (!TOTALS && p.h != nullptr && k > 0) wait_memory<2>();   // the stores behind its loads
     else wait_memory<0>();
     uint32_t in[NT][kRun];
@@ -387,7 +419,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
       for (int r = 0; r < kRun; ++r) in[t][r] = *reinterpret_cast<const uint32_t*>(raw[wave][t] + l.at(r));
     }
     wait_lds();
-    fetch(t0 + kTile);
+    fetch(t0 + step);
     float a[kRun][V], b[kRun][V];
     Run own[V], before[V];
 #pragma unroll
@@ -406,16 +438,18 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) settle(own[v]);
-    join_lanes<V, kLanes, false>(own, before);
+    for (int v = 0; v < V; ++v) own[v] = settle(own[v]);
+    join_lanes<V, kLanes, false, false>(own, before);
     if (l.run == Geo<kLanes>::kRuns - 1) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
     }
     __syncthreads();
-    keeper.template pass<TOTALS>(exchange, lane, total);
-    __syncthreads();
-    if constexpr (!TOTALS) {
+    if constexpr (TOTALS) {
+      return __syncthreads_and(keeper.extend(exchange, lane, total)) != 0;
+    } else {
+      keeper.pass(exchange, lane);
+      __syncthreads();
       float y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) y[v] = fmaf(before[v].A, exchange.before[wave][l.slot * V + v], before[v].H);
@@ -434,16 +468,18 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
         }
         store_span(out[wave], h + t0 * ldh, ldh, left, width, l, lane, rows);
       }
+      return false;
     }
   };
   int64_t k = 0;
-  for (; (k + 1) * kTile <= end - begin; ++k) walk(std::true_type{}, k);
-  if (k < tiles) walk(std::false_type{}, k);
+  for (; (k + 1) * kTile <= end - begin; ++k)
+    if (walk(std::true_type{}, k)) break;
+  if (!TOTALS && k < tiles) walk(std::false_type{}, k);
   wait_memory<0>();   // of LDS that the next workgroup may get
   if (!keeper.first) return;
   keeper.all([&](int t, int ch) {
     if constexpr (TOTALS)
-      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch] = {total[t].A, total[t].C, keeper.carry[t].value()};
+      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch] = total[t];
     else if (last && p.h_final != nullptr)
       p.h_final[cb + ch] = keeper.carry[t].value();
   });
@@ -451,7 +487,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
 
 // Gradients, from a sequence's end: with G_t = a_t (d_h_t + G_{t+1}) the same recurrence, whose
 // value behind token t is l_t = d_h_t + G_{t+1}. h comes from the state before the span. TOTALS:
-// only what each segment but the first makes of the gradient behind it.
+// only what each segment but the first makes of the gradient behind it, from its start on.
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   constexpr int V = 4 / int(sizeof(E)), N = Geo<kBackLanes>::kChannels<E>, R = kRun, kRuns = Geo<kBackLanes>::kRuns;
@@ -502,10 +538,11 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
   };
   const int64_t tiles = end > begin ? (end - begin + kBackTile - 1) / kBackTile : 0;
-  const int64_t first = begin + (tiles - 1) * kBackTile + wave * kSpan;   // the last tile comes first
+  const int64_t step = TOTALS ? kBackTile : -kBackTile;
+  const int64_t first = begin + wave * kSpan + (TOTALS ? 0 : (tiles - 1) * kBackTile);
   if (tiles > 0) {
     fetch(0, first);
-    fetch(1, first - kBackTile);
+    fetch(1, first + step);
   }
   float decay[V], sum[V];
 #pragma unroll
@@ -514,17 +551,22 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
 #pragma unroll
   for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
   if constexpr (!TOTALS) {
-    keeper.all([&](int t, int ch) {
-      if (p.d_final != nullptr) keeper.carry[t].hi = p.d_final[cb + ch];
-      for (int64_t s = (n + p.seg - 1) / p.seg - 1; s > int64_t(at.seg); --s)
-        keeper.carry[t].pass(p.totals[(at.b * (p.segs - 1) + s - 1) * p.C + c0 + ch]);
-    });
+    if (p.d_final != nullptr) keeper.all([&](int t, int ch) { keeper.carry[t].hi = p.d_final[cb + ch]; });
+    const int64_t last = (n + p.seg - 1) / p.seg - 1;   // the last segment with tokens
+    keeper.over(last - at.seg, lane, [&](int ch, int64_t k) { return p.totals[(at.b * (p.segs - 1) + last - k - 1) * p.C + c0 + ch]; });
   }
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
     const int stage = k & 1;
-    const int64_t t0 = first - k * kBackTile, left = end - t0;
-    wait_tile<kLoads, kStores>(k);
+    const int64_t t0 = first + k * step, left = end - t0;
+    // Behind the tile's loads came those of the next one and the stores of the two before it. What may be
+    // out of range in part (the next tile's loads at an end, the first tile's stores) is not counted on.
+    const int64_t next = t0 + step;
+    const bool ahead = next >= begin && end - next >= kSpan;
+    if (!ahead) wait_memory<0>();
+    else if (TOTALS || k <= 1) wait_memory<kLoads>();
+    else if (k == 2) wait_memory<kLoads + kStores>();
+    else wait_memory<kLoads + 2 * kStores>();
     uint32_t in[NT][R];
     float mark[V];
 #pragma unroll
@@ -537,7 +579,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
       for (int v = 0; v < V; ++v) mark[v] = reinterpret_cast<const float*>(raw_marks[stage][wave])[l.slot * V + v];
     }
     wait_lds();
-    fetch(stage, t0 - 2 * kBackTile);
+    fetch(stage, t0 + 2 * step);
     Gate gate[R][V];
     float si[R][V], resti[R][V], before[R][V];
     Run own[V], lanes[V];
@@ -566,17 +608,17 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
     if constexpr (!TOTALS) {
       // h before each token: from what each adds
-      Run fwd[V], ahead[V];
+      Run fwd[V], earlier[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         fwd[v] = {own[v].A, 0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < R; ++r) fwd[v].H = fmaf(gate[r][v].a, fwd[v].H, before[r][v]);
       }
-      join_lanes<V, kBackLanes, false>(fwd, ahead);
+      join_lanes<V, kBackLanes, false, true>(fwd, earlier);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float y = fmaf(ahead[v].A, mark[v], ahead[v].H);
+        float y = fmaf(earlier[v].A, mark[v], earlier[v].H);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float add = before[r][v];
@@ -586,16 +628,18 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) settle(own[v]);
-    join_lanes<V, kBackLanes, true>(own, lanes);
+    for (int v = 0; v < V; ++v) own[v] = settle(own[v]);
+    join_lanes<V, kBackLanes, true, false>(own, lanes);
     if (l.run == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
     }
     __syncthreads();
-    keeper.template pass<TOTALS>(exchange, lane, total);
-    __syncthreads();
-    if constexpr (!TOTALS) {
+    if constexpr (TOTALS) {
+      return __syncthreads_and(keeper.extend(exchange, lane, total)) != 0;
+    } else {
+      keeper.pass(exchange, lane);
+      __syncthreads();
       float G[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) G[v] = fmaf(lanes[v].A, exchange.before[wave][l.slot * V + v], lanes[v].H);
@@ -630,16 +674,21 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
       store_span(out[wave], dx + t0 * ldh, ldh, left, width, l, lane, in[2]);
       store_span(out[wave], df + t0 * ldh, ldh, left, width, l, lane, in[0]);
       if constexpr (IG) store_span(out[wave], di + t0 * ldh, ldh, left, width, l, lane, in[3]);
+      return false;
     }
   };
+  // the tile that may be in part behind the end is the last one of the segment
+  const bool part = tiles > 0 && tiles * kBackTile > end - begin;
   int64_t k = 0;
-  if (tiles * kBackTile > end - begin && tiles > 0) walk(std::false_type{}, k++);
-  for (; k < tiles; ++k) walk(std::true_type{}, k);
+  if (!TOTALS && part) walk(std::false_type{}, k++);
+  bool gone = false;
+  for (; k < tiles - (TOTALS && part) && !gone; ++k) gone = walk(std::true_type{}, k);
+  if (TOTALS && part && !gone) walk(std::false_type{}, k);
   wait_memory<0>();
   if constexpr (TOTALS) {
     if (keeper.first)
       keeper.all([&](int t, int ch) {
-        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch] = {total[t].A, total[t].C, keeper.carry[t].value()};
+        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch] = total[t];
       });
   } else {
     if (at.seg == 0 && p.dh0 != nullptr && keeper.first) keeper.all([&](int t, int ch) { p.dh0[cb + ch] = keeper.carry[t].value(); });
