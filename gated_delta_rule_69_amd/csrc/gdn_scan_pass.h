@@ -714,11 +714,13 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   }
 }
 
-// Token by token, four channels a thread: single tokens, where each sequence's state is read
-// and written once. Where less than half of a state goes, (1 - a) h is taken from it.
+// Token by token, four channels a thread, for few tokens: each sequence's state is read and written
+// once, and the rows of AT tokens are loaded together. Where less than half of a state goes, (1 - a) h
+// is taken from it.
 constexpr int kStepThreads = 256;
-template <typename E, int KIND, bool IG>
+template <typename E, int KIND, bool IG, int AT>
 __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(Pass p) {
+  typedef vec<E, 4> Row;
   const unsigned per = unsigned(p.C / 4);
   const unsigned id = blockIdx.x * kStepThreads + threadIdx.x;
   if (id >= p.blocks) return;   // (sequence, channels): B * C / 4 of them
@@ -727,24 +729,35 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(Pass p) {
   float h[4] = {}, decay[4] = {};
   if (p.h0 != nullptr) load4(p.h0 + b * p.C + c, h);
   if constexpr (KIND == GDN_SCAN_POWER) load4(p.decay + c, decay);
-  const int64_t ldh = p.C * int64_t(sizeof(E));
-  for (int64_t t = 0; t < n; ++t) {
-    const int64_t row = b * p.T + t;
-    float x[4], f[4], i[4], out[4];
-    load4(reinterpret_cast<const E*>(static_cast<const char*>(p.x) + row * p.ldx) + c, x);
-    load4(reinterpret_cast<const E*>(static_cast<const char*>(p.f) + row * p.ldf) + c, f);
-    if constexpr (IG) load4(reinterpret_cast<const E*>(static_cast<const char*>(p.i) + row * p.ldi) + c, i);
-    if (p.marks != nullptr && t % kSpan == 0) store4(p.marks + (b * ((p.T + kSpan - 1) / kSpan) + t / kSpan) * p.C + c, h);
+  const char* x = static_cast<const char*>(p.x) + b * p.T * p.ldx + c * sizeof(E);
+  const char* f = static_cast<const char*>(p.f) + b * p.T * p.ldf + c * sizeof(E);
+  const char* g = static_cast<const char*>(p.i) + b * p.T * p.ldi + c * sizeof(E);
+  E* out = static_cast<E*>(p.h) + b * p.T * p.C + c;
+  for (int64_t t0 = 0; t0 < n; t0 += AT) {
+    Row rx[AT], rf[AT], ri[AT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const Gate g = gate_of<E, KIND>(f[v], decay[v]);
-      float add = g.m * x[v];
-      if constexpr (IG) add *= sigmoid_of<E>(i[v]);
-      out[v] = h[v] = g.c < 0.5f ? h[v] + fmaf(-g.c, h[v], add) : fmaf(g.a, h[v], add);
+    for (int k = 0; k < AT; ++k) {
+      const int64_t t = t0 + k < n ? t0 + k : n - 1;
+      rx[k] = *reinterpret_cast<const Row*>(x + t * p.ldx);
+      rf[k] = *reinterpret_cast<const Row*>(f + t * p.ldf);
+      if constexpr (IG) ri[k] = *reinterpret_cast<const Row*>(g + t * p.ldi);
     }
-    store4(reinterpret_cast<E*>(static_cast<char*>(p.h) + row * ldh) + c, out);
+#pragma unroll
+    for (int k = 0; k < AT; ++k) {
+      const int64_t t = t0 + k;
+      if (t >= n) break;
+      if (p.marks != nullptr && t % kSpan == 0) store4(p.marks + (b * ((p.T + kSpan - 1) / kSpan) + t / kSpan) * p.C + c, h);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const Gate q = gate_of<E, KIND>(float(rf[k][v]), decay[v]);
+        float add = q.m * float(rx[k][v]);
+        if constexpr (IG) add *= sigmoid_of<E>(float(ri[k][v]));
+        h[v] = q.c < 0.5f ? h[v] + fmaf(-q.c, h[v], add) : fmaf(q.a, h[v], add);
+      }
+      if (p.h != nullptr) store4(out + t * p.C, h);
+    }
   }
-  if (p.h_final != nullptr) store4(p.h_final + b * p.C + c, h);
+  if (p.h_final != nullptr && (n > 0 || p.h_final != p.h0)) store4(p.h_final + b * p.C + c, h);
 }
 
 template <typename F>
@@ -762,8 +775,13 @@ int by_gate(const gdn_scan_args& a, F f) {
 template <typename E>
 int launch_step(const ScanProblem& q, const Pass& p, hipStream_t s) {
   return by_gate(q.a, [&](auto kind, auto gated) {
-    scan_step_kernel<E, decltype(kind)::value, decltype(gated)::value>
-        <<<(p.blocks + kStepThreads - 1) / kStepThreads, kStepThreads, 0, s>>>(p);
+    constexpr int K = decltype(kind)::value;
+    constexpr bool G = decltype(gated)::value;
+    const unsigned blocks = (p.blocks + kStepThreads - 1) / kStepThreads;
+    if (p.T == 1)
+      scan_step_kernel<E, K, G, 1><<<blocks, kStepThreads, 0, s>>>(p);
+    else
+      scan_step_kernel<E, K, G, 4><<<blocks, kStepThreads, 0, s>>>(p);
     return int(hipGetLastError());
   });
 }
