@@ -2,8 +2,11 @@
 //     u = y rms(y) post_weight (or y),  r' = rho r + scale act(gate) u,  n = r' rms(r') weight
 //
 // A row is a workgroup's: eight channels a lane, a wave for every 512 channels (two vectors a
-// lane above 8,192), so that each tensor is read and written once and a row's sums are a few
-// DPP adds and one exchange through LDS. Memory bounds it.
+// lane above 8,192, in the gradients above 4,096), so that each tensor is read and written once and
+// a row's sums are a few DPP adds and one exchange through LDS. Memory bounds it.
+//
+// bf16, gate, norm after and before, C 2,048: 65,536 tokens 252 us (1.34 GB, 5.3 TB/s: a copy's rate); the
+// gradients of 8,192 tokens 61 us (268 MB, 4.4 TB/s), 5 of them the weights' sums in a second kernel.
 #include <algorithm>
 
 #include "gdn_block.h"

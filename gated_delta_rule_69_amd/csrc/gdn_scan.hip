@@ -16,8 +16,9 @@ constexpr int64_t kGroups = 256;   // workgroups that fill the CUs
 int64_t spans_of(int64_t T) { return (T + scan::kSpan - 1) / scan::kSpan; }
 
 // Segments of a sequence and the tokens of each. A workgroup walks its segment; where slices and
-// sequences alone leave CUs idle, segments run side by side, at the price of a first pass over
-// the inputs for what each makes of the state.
+// sequences alone leave CUs idle, segments of two tiles and more run side by side, at the price of a
+// first pass over the inputs for what each makes of the state (B2 T32768 C2048 bf16: 512 and 1,024
+// workgroups 289 and 282 us against 272 with 256; 300 tokens in one walk 12.6 against 16.6).
 void cut(const gdn_scan_args& a, bool back, unsigned* segs, int64_t* seg) {
   const int64_t tile = back ? scan::kBackTile : scan::kTile;
   const int64_t tiles = std::max<int64_t>(1, (a.T + tile - 1) / tile);
@@ -47,7 +48,9 @@ size_t totals_bytes(const gdn_scan_args& a, bool back) {
   return rounded(size_t(a.B) * (segs - 1) * a.C * sizeof(Run));
 }
 size_t start_bytes(const gdn_scan_args& a) { return rounded(size_t(a.B) * a.C * sizeof(float)); }
-size_t marks_bytes(const gdn_scan_args& a) { return rounded(size_t(a.B) * spans_of(a.T) * a.C * sizeof(float)); }
+size_t marks_bytes(const gdn_scan_args& a) {
+  return a.checkpoints != nullptr ? 0 : rounded(size_t(a.B) * spans_of(a.T) * a.C * sizeof(float));
+}
 size_t sums_bytes(const gdn_scan_args& a) {
   unsigned segs;
   int64_t seg;
@@ -90,7 +93,7 @@ int launch_scan_step(const ScanProblem& q, const float* before, float* after, vo
 }
 
 // Gradients' workspace: the forward pass's or the totals from the end, the states before the
-// spans, and the segments' sums for ddecay.
+// spans where they are not given, and the segments' sums for ddecay.
 size_t scan_bwd_workspace(const ScanProblem& q) {
   return std::max(scan_fwd_workspace(q), totals_bytes(q.a, true)) + marks_bytes(q.a) + sums_bytes(q.a);
 }

@@ -13,6 +13,18 @@
 // instead of being multiplied by a rounded A near 1, whose error a channel that keeps many
 // tokens would add up at every step; and the state a workgroup carries is a sum of two
 // floats, for the same reason.
+//
+// Where slices and sequences do not fill the CUs, segments of a sequence run side by side: a first
+// launch finds what each makes of the state before it, walking it from its end until nothing before
+// can be left in float32 (a thousand tokens and more under forget gates of logits around 3), and the
+// second joins those before its own.
+//
+// Memory bounds it, as long as a CU's loads under way are long ones: rows of 32, 64 and 128 bytes a slice
+// took 308, 196 and 164 us for the second launch of B2 T32768 C2048 (bf16, sigmoid). Now 206 us in both
+// launches (805 MB, 3.9 TB/s; 176 with C 2112, whose rows do not start at the same 4 KiB), 147 for B8 T1024
+// C8192 with an input gate (537 MB), where one launch does; B1 T4096 C2048 39 us, two short launches. The
+// gradients of B2 T4096 C2048 with power and input gate 80 us (235 MB): their vector instructions, a
+// hundred a channel and token, are as much as their bytes.
 #pragma once
 
 #include <algorithm>
@@ -150,10 +162,9 @@ __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_
   return {uniform(uint32_t(from)), uniform(uint32_t(from >> 32) & 0xffffu), uniform(bytes), 0x00020000u};
 }
 
-// Rows on their way from memory to LDS, ahead of their use: 32 bytes a row of a slice,
-// a wave's own span, so that nothing but its own count of loads says when they are there. Lane l
-// of a load brings sixteen bytes to the wave's place 16 l: the rows r of the runs lie side
-// by side there, at 256 r + kRow run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
+// Rows on their way from memory to LDS, ahead of their use: a wave's own, so that nothing but its own
+// count of loads says when they are there. Lane l of a load brings sixteen bytes to the wave's place
+// 16 l: the rows r of the runs lie side by side there, at 256 r + kRow run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
 // the compiler's own counts only ever wait for more.
 template <int LANES> struct Feed {
   static constexpr int kRuns = Geo<LANES>::kRuns;

@@ -462,9 +462,12 @@ int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_gra
  *                writes them if given; the gradients read them if given, and otherwise run
  *                over x, f and i once more to get them.
  * GDN_ERR_UNSUPPORTED above C = 2^16, B * C = 2^24, and the limits of B, T, B * T and strides
- * of the linear entry points. The state is float32; a sequence's tokens are joined in a
- * fixed tree. A NaN or Inf in row t makes its channel of h NaN or Inf from t on, until a row
- * of a = 0 or beyond (0 times NaN is NaN), and nothing else. */
+ * of the linear entry points. The state is float32; a sequence's tokens are joined in a tree that
+ * goes by the sizes alone. A NaN or Inf in row t makes its channel of h NaN or Inf from t on, at
+ * least as long as its weight, the product of the a's since, is over 2^-127, and nothing else;
+ * behind that weight nothing is promised (0 times NaN is NaN within a part of the sequence, while
+ * rows that weigh nothing are not read from the next). The same holds along the gradients'
+ * formulas, from a row backwards. */
 enum gdn_scan_gate { GDN_SCAN_LOG = 1, GDN_SCAN_SIGMOID = 2, GDN_SCAN_POWER = 3 };
 #define GDN_SCAN_SPAN 64
 
@@ -506,7 +509,7 @@ typedef struct gdn_scan_grads {
   float* dh0;
 } gdn_scan_grads;
 
-/* Bytes of device workspace gdn_gated_scan_bwd needs (0 for an invalid set). */
+/* Bytes of device workspace gdn_gated_scan_bwd needs (0 for an invalid set); fewer with checkpoints. */
 size_t gdn_gated_scan_bwd_workspace_bytes(const gdn_scan_args* args);
 
 /* Gradients of h and h_final: with d_h [B, T, C] in args->dtype (contiguous; rows behind a

@@ -12,6 +12,7 @@ CASES = [
     (1, 1, 8, None), (2, 2, 16, None), (1, 7, 24, None), (3, 8, 40, [8, 0, 3]), (1, 9, 8, None), (2, 63, 24, None),
     (2, 64, 16, None), (1, 65, 136, None), (2, 255, 32, [255, 64]), (1, 256, 8, None), (4, 257, 72, [257, 0, 1, 256]),
     (2, 511, 24, [-3, 900]), (1, 1025, 264, None), (2, 2500, 40, [2500, 1200]), (1, 5000, 16, None),
+    (40, 30, 512, None), (40, 35, 512, None),     # more than 256 workgroups: up to 32 tokens one by one
 ]
 
 
@@ -155,6 +156,33 @@ def test_scan_extreme_gates(dt):
         if gate == "power":
             ok = (decay > 1e-20).numpy()      # at decay 0 the slope of m has no limit
             check(g["ddecay"][torch.from_numpy(ok).to(dev())], ref["ddecay"][ok], "ddecay")
+
+
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("T,B,C", [(9000, 1, 2048), (9000, 2, 256)])
+def test_scan_long_segments(T, B, C, slow):
+    """Segments of several tiles, whose totals stop where nothing before them is left: in no slice, or in
+    those that hold one channel that forgets nothing. Both directions (C 2048 and 256: several tiles a
+    segment forwards, and in the gradients)."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import check, dev, f64
+    gen = torch.Generator().manual_seed(C)
+    x, d_h = (torch.randn((B, T, C), generator=gen) for _ in range(2))
+    f = -torch.rand((B, T, C), generator=gen) * 0.5
+    if slow:
+        f[:, :, 5::130] = -1e-4
+    h0, up = (torch.randn((B, C), generator=gen) for _ in range(2))
+    out, end = gdn.gdn_gated_scan_fwd(x.to(dev()), f.to(dev()), gate="log", h0=h0.to(dev()))
+    g = gdn.gdn_gated_scan_bwd(x.to(dev()), f.to(dev()), gate="log", h0=h0.to(dev()), d_h=d_h.to(dev()), dh_final=up.to(dev()))
+    want, want_end = block.scan_forward(f64(x), f64(f), gate="log", h0=f64(h0))
+    ref = block.scan_backward(f64(x), f64(f), d_h=f64(d_h), gate="log", h0=f64(h0), dh_final=f64(up))
+    check(out, want, "h")
+    check(end, want_end, "end")
+    for n in ("dx", "df", "dh0"):
+        check(g[n], ref[n], n)
+    inplace = h0.to(dev())
+    again, same = gdn.gdn_gated_scan_fwd(x.to(dev()), f.to(dev()), gate="log", h0=inplace, h_final=inplace)
+    assert same is inplace and torch.equal(same, end) and torch.equal(again, out)
 
 
 def test_scan_jump_of_magnitude_leaves_later_rows_exact():
