@@ -55,18 +55,28 @@ constexpr int kLanes = 32, kBackLanes = 8;
 constexpr int kTile = kWaves * Geo<kLanes>::kTokens, kBackTile = kBackWaves * Geo<kBackLanes>::kTokens;
 static_assert(Geo<kBackLanes>::kTokens == kSpan, "a checkpoint is the state before a wave's tokens");
 
-// 1 - e^y for y <= 0 (and what it is above), to a few steps of its own: a series where the
-// difference would cancel.
+// e^y and 1 - e^y for y <= 0 (and what they are above), the second to a few steps of its own: a series
+// where the difference would cancel. For bf16 y comes times log2 e, which takes one instruction for 2^y;
+// for float32 as it is.
 template <typename E>
-__device__ __forceinline__ float one_minus_exp(float y, float ey) {
+__device__ __forceinline__ void exp_both(float y, float* a, float* c) {
   float p;
-  if constexpr (sizeof(E) == 2) {   // |y| < 1/4: y^5/720 is 2^-19 of y
-    p = 1.0f + y * (0.5f + y * (1.0f / 6 + y * (1.0f / 24 + y * (1.0f / 120))));
-  } else {                          // y^8/9! is 2^-34
+  bool near;
+  if constexpr (sizeof(E) == 2) {   // z = y ln 2, |z| < 1/4: z^5 / 720 is 2^-19 of z
+    constexpr float L = 0.69314718056f;
+    *a = __builtin_amdgcn_exp2f(y);
+    p = -L + y * (-L * L / 2 + y * (-L * L * L / 6 + y * (-L * L * L * L / 24 + y * (-L * L * L * L * L / 120))));
+    p *= y;
+    near = fabsf(y) < 0.36f;
+  } else {                          // y^8 / 9! is 2^-34
+    *a = expf(y);
     p = 1.0f / 24 + y * (1.0f / 120 + y * (1.0f / 720 + y * (1.0f / 5040 + y * (1.0f / 40320))));
-    p = 1.0f + y * (0.5f + y * (1.0f / 6 + y * p));
+    p = -y * (1.0f + y * (0.5f + y * (1.0f / 6 + y * p)));
+    near = fabsf(y) < 0.25f;
   }
-  return fabsf(y) < 0.25f ? -y * p : 1.0f - ey;
+  // both sides in every lane: a branch for the series costs more than it
+  asm volatile("" : "+v"(p));
+  *c = near ? p : 1.0f - *a;
 }
 
 // A token's factors: h = a h + m g x with c = 1 - a. s and rest (sigmoid(f) and its
@@ -74,12 +84,16 @@ __device__ __forceinline__ float one_minus_exp(float y, float ey) {
 struct Gate {
   float a, c, m, s, rest;
 };
+// What gate_of takes for a channel's decay.
+template <typename E>
+__device__ __forceinline__ float scaled_decay(float decay) {
+  return sizeof(E) == 2 ? -1.44269504089f * decay : -decay;
+}
 template <typename E, int KIND>
 __device__ __forceinline__ Gate gate_of(float f, float decay) {
   Gate g;
   if constexpr (KIND == GDN_SCAN_LOG) {
-    g.a = exp_of<E>(f);
-    g.c = one_minus_exp<E>(f, g.a);
+    exp_both<E>(sizeof(E) == 2 ? 1.44269504089f * f : f, &g.a, &g.c);
     g.m = 1.0f;
     g.s = g.rest = 0.0f;
   } else {
@@ -88,11 +102,10 @@ __device__ __forceinline__ Gate gate_of(float f, float decay) {
       g.a = g.s;
       g.c = g.m = g.rest;
     } else {
-      const float y = -decay * g.s;
-      g.a = exp_of<E>(y);
-      g.c = one_minus_exp<E>(y, g.a);
+      exp_both<E>(decay * g.s, &g.a, &g.c);
       // 1 - a^2 = c (1 + a)
-      g.m = sizeof(E) == 2 ? __builtin_amdgcn_sqrtf(g.c * (1.0f + g.a)) : sqrtf(g.c * (1.0f + g.a));
+      const float m2 = fmaf(g.c, g.a, g.c);
+      g.m = sizeof(E) == 2 ? __builtin_amdgcn_sqrtf(m2) : sqrtf(m2);
     }
   }
   return g;
@@ -168,8 +181,7 @@ __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_
 // the compiler's own counts only ever wait for more.
 template <int LANES> struct Feed {
   static constexpr int kRuns = Geo<LANES>::kRuns;
-  uint32_t off[4];
-  int64_t ld[4];
+  uint32_t off[4], ld[4];
   const char* base[4];
   // a lane's place in a span for sixteen bytes, and in its row
   static __device__ __forceinline__ uint32_t column(int lane) { return lane % (LANES / 4) * 16; }
@@ -178,10 +190,10 @@ template <int LANES> struct Feed {
     return uint32_t((p % kRuns) * kRun + p / kRuns) * uint32_t(ld) + column(lane);
   }
   __device__ __forceinline__ void open(int k, const void* p, int64_t ld_, int64_t first, int lane) {
-    base[k] = static_cast<const char*>(p) + first, ld[k] = ld_, off[k] = place(lane, ld_);
+    base[k] = static_cast<const char*>(p) + first, ld[k] = uint32_t(ld_), off[k] = place(lane, ld_);
   }
   __device__ __forceinline__ void load(int k, char* to, int64_t t0, int64_t left, uint32_t width) const {
-    const uint4v range = rows_from(base[k] + t0 * ld[k], ld[k], left, Geo<LANES>::kTokens, width);
+    const uint4v range = rows_from(base[k] + t0 * int64_t(ld[k]), ld[k], left, Geo<LANES>::kTokens, width);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(to))));
     asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds), "v"(off[k]), "s"(range) : "memory");
     asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(lds + 1024), "v"(off[k] + 4 * uint32_t(ld[k])), "s"(range) : "memory");
@@ -416,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   float decay[V];
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    decay[v] = KIND == GDN_SCAN_POWER && uint32_t(l.slot * V) < channels ? p.decay[c0 + l.slot * V + v] : 0.0f;
+    decay[v] = KIND == GDN_SCAN_POWER && uint32_t(l.slot * V) < channels ? scaled_decay<E>(p.decay[c0 + l.slot * V + v]) : 0.0f;
   // a tile whose rows are all there, or the last
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
@@ -555,9 +567,12 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     fetch(0, first);
     fetch(1, first + step);
   }
-  float decay[V], sum[V];
+  float raw_decay[V], decay[V], sum[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f, sum[v] = 0.0f;
+  for (int v = 0; v < V; ++v) {
+    raw_decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f;
+    decay[v] = scaled_decay<E>(raw_decay[v]), sum[v] = 0.0f;
+  }
   Run total[Keep::kTurns];
 #pragma unroll
   for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
@@ -674,7 +689,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
             // d m / d a = -a / m
             const float slope = t.m > 0.0f ? t.a * gx * __builtin_amdgcn_rcpf(t.m) : 0.0f;
             const float dlog = g * t.a * (before[r][v] - slope) * t.s;
-            of[v] = -decay[v] * t.rest * dlog;
+            of[v] = -raw_decay[v] * t.rest * dlog;
             sum[v] -= here ? dlog : 0.0f;
           }
           G[v] = here ? t.a * g : G[v];
@@ -739,7 +754,11 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(Pass p) {
   const int64_t n = tokens_of(p.lens, b, p.T);
   float h[4] = {}, decay[4] = {};
   if (p.h0 != nullptr) load4(p.h0 + b * p.C + c, h);
-  if constexpr (KIND == GDN_SCAN_POWER) load4(p.decay + c, decay);
+  if constexpr (KIND == GDN_SCAN_POWER) {
+    load4(p.decay + c, decay);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) decay[v] = scaled_decay<E>(decay[v]);
+  }
   const char* x = static_cast<const char*>(p.x) + b * p.T * p.ldx + c * sizeof(E);
   const char* f = static_cast<const char*>(p.f) + b * p.T * p.ldf + c * sizeof(E);
   const char* g = static_cast<const char*>(p.i) + b * p.T * p.ldi + c * sizeof(E);
