@@ -339,10 +339,16 @@ def gdn_block_norm_fwd(residual, y=None, gate=None, *, weight=None, post_norm=Fa
     shape, dev = residual.shape, residual.get_device()
     if residual_out is None:
         residual_out = _beside(residual)
+        to_r = residual_out.data_ptr()
+    else:
+        to_r = _whole(residual_out, "residual_out", shape, residual.dtype, dev)
     if out is None:
-        out = torch.empty_like(residual, dtype=dtype, memory_format=torch.contiguous_format)
-    a = _norm_args(residual, y, gate, weight, post_norm, post_weight, scale, activation, residual_scale, eps, dtype,
-                   _whole(residual_out, "residual_out", shape, residual.dtype, dev), _whole(out, "out", shape, dtype, dev))
+        like = residual if y is None or residual.dtype is dtype else y
+        out = _beside(like) if like.dtype is dtype else residual.new_empty(shape, dtype=dtype)
+        to = out.data_ptr()
+    else:
+        to = _whole(out, "out", shape, dtype, dev)
+    a = _norm_args(residual, y, gate, weight, post_norm, post_weight, scale, activation, residual_scale, eps, dtype, to_r, to)
     _done(_library().gdn_block_norm_fwd(a, _current_stream(dev)), "gdn_block_norm_fwd")
     return residual_out, out
 
