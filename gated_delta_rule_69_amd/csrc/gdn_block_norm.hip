@@ -54,18 +54,21 @@ __device__ __forceinline__ void block_sum(float* s, float (*part)[K], int waves)
   }
 }
 
+// Eight channels; rows start at any multiple of sixteen bytes, also of float32.
+template <typename E> using Eight = E __attribute__((ext_vector_type(8), aligned(16)));
+
 template <typename E>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
-  const vec<E, 8> r = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(p) + at);
+  const Eight<E> r = *reinterpret_cast<const Eight<E>*>(static_cast<const E*>(p) + at);
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = float(r[i]);
 }
 template <typename E>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float* x) {
-  vec<E, 8> r;
+  Eight<E> r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = E(x[i]);
-  *reinterpret_cast<vec<E, 8>*>(static_cast<E*>(p) + at) = r;
+  *reinterpret_cast<Eight<E>*>(static_cast<E*>(p) + at) = r;
 }
 __device__ __forceinline__ void ones_or(const float* w, int64_t c, float* out) {
 #pragma unroll
@@ -160,8 +163,8 @@ __global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(Norm a) {
     if constexpr (KEEP) ones_or(a.w, c[k], kept[0][k]), ones_or(a.post_w, c[k], kept[1][k]), ones_or(a.scale, c[k], kept[2][k]);
   }
   struct Loaded {
-    vec<R, 8> r, up;
-    vec<E, 8> y, z, dn;
+    Eight<R> r, up;
+    Eight<E> y, z, dn;
   };
   // rows of absent inputs are zero; so are a lane's channels behind the last
   auto fetch = [&](Loaded* f, int64_t row) {
@@ -169,11 +172,11 @@ __global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(Norm a) {
     for (int k = 0; k < NV; ++k) {
       f[k] = Loaded{};
       if (!own[k]) continue;
-      f[k].r = *reinterpret_cast<const vec<R, 8>*>(static_cast<const R*>(a.r) + row * a.ldr + c[k]);
-      if (a.y != nullptr) f[k].y = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.y) + row * a.ldy + c[k]);
-      if (a.gate != nullptr) f[k].z = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.gate) + row * a.ldg + c[k]);
-      if (a.d_out != nullptr) f[k].dn = *reinterpret_cast<const vec<E, 8>*>(static_cast<const E*>(a.d_out) + row * a.C + c[k]);
-      if (a.d_r != nullptr) f[k].up = *reinterpret_cast<const vec<R, 8>*>(static_cast<const R*>(a.d_r) + row * a.C + c[k]);
+      f[k].r = *reinterpret_cast<const Eight<R>*>(static_cast<const R*>(a.r) + row * a.ldr + c[k]);
+      if (a.y != nullptr) f[k].y = *reinterpret_cast<const Eight<E>*>(static_cast<const E*>(a.y) + row * a.ldy + c[k]);
+      if (a.gate != nullptr) f[k].z = *reinterpret_cast<const Eight<E>*>(static_cast<const E*>(a.gate) + row * a.ldg + c[k]);
+      if (a.d_out != nullptr) f[k].dn = *reinterpret_cast<const Eight<E>*>(static_cast<const E*>(a.d_out) + row * a.C + c[k]);
+      if (a.d_r != nullptr) f[k].up = *reinterpret_cast<const Eight<R>*>(static_cast<const R*>(a.d_r) + row * a.C + c[k]);
     }
   };
   Loaded next[NV];

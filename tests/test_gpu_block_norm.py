@@ -71,6 +71,30 @@ def test_block_norm_absent_inputs(absent, types):
     _compare(c, wide=False, post_norm=True, activation="silu")
 
 
+@pytest.mark.parametrize("C", [8, 512, 2056, 8200])
+def test_block_norm_rows_at_odd_multiples_of_sixteen_bytes(C):
+    """Float32 rows that start sixteen bytes after a multiple of 32: views four channels into tensors of
+    C + 4."""
+    import gated_delta_rule_69_amd as gdn
+    from block_util import host
+    from layer_util import check, dev
+    c = _case(2, 5, C, ("f32", "f32"), seed=9)
+    d, h = _device(c), host(c)
+    for n in ("residual", "y", "gate"):
+        big = torch.full((2, 5, C + 4), float("nan"), device=dev())
+        big[..., 4:] = d[n]
+        d[n] = big[..., 4:]
+        assert d[n].data_ptr() % 32 == 16
+    ins, ups = {k: v for k, v in d.items() if k not in UPS}, {k: d[k] for k in UPS}
+    r, n = gdn.gdn_block_norm_fwd(**ins, post_norm=True)
+    g = gdn.gdn_block_norm_bwd(**ins, **ups, post_norm=True)
+    want_r, want_n, want = block.block_norm(**h, post_norm=True)
+    check(r, want_r, "residual_out")
+    check(n, want_n, "out")
+    for k, t in g.items():
+        check(t, want[k], k)
+
+
 @pytest.mark.parametrize("types", TYPES, ids="-".join)
 def test_norm_before_a_first_block(types):
     """No output of a block yet: the norm of the residual alone."""

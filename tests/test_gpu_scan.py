@@ -293,7 +293,35 @@ def test_scan_rows_far_apart():
     want, want_end = block.scan_forward(f64(x), f64(f))
     check(h, want, "h")
     check(end, want_end, "end")
+    d_h = torch.randn((1, T, C), generator=gen).bfloat16()
+    g = gdn.gdn_gated_scan_bwd(view, f.to(dev()), d_h=d_h.to(dev()))
+    ref = block.scan_backward(f64(x), f64(f), d_h=f64(d_h))
+    for n in ("dx", "df", "dh0"):
+        check(g[n], ref[n], n)
+    one = gdn.gdn_short_conv_fwd(view, torch.ones((C, 3), device=dev()), activation=None)[0]
+    check(one, block.conv_forward(f64(x), np.ones((C, 3)), activation=None)[0], "conv")
     del view, big
+
+
+@pytest.mark.parametrize("C", [8, 40])
+def test_scan_rows_at_odd_multiples_of_sixteen_bytes(C):
+    import gated_delta_rule_69_amd as gdn
+    from block_util import dev, host, scan_case
+    from layer_util import check
+    c = scan_case(2, 300, C, "f32", "sigmoid", True, seed=21)
+    d, h = _device(c, wide=False), host(c)
+    for n in "xfi":
+        big = torch.full((2, 300, C + 4), float("nan"), device=dev())
+        big[..., 4:] = d[n]
+        d[n] = big[..., 4:]
+    out, end = gdn.gdn_gated_scan_fwd(d["x"], d["f"], d["i"], h0=d["h0"])
+    g = gdn.gdn_gated_scan_bwd(d["x"], d["f"], d["i"], h0=d["h0"], d_h=d["d_h"], dh_final=d["dh_final"])
+    want, want_end = block.scan_forward(h["x"], h["f"], h["i"], h0=h["h0"])
+    ref = block.scan_backward(h["x"], h["f"], h["i"], h0=h["h0"], d_h=h["d_h"], dh_final=h["dh_final"])
+    check(out, want, "h")
+    check(end, want_end, "end")
+    for n, t in g.items():
+        check(t, ref[n], n)
 
 
 @pytest.mark.parametrize("B,C", [(4096, 8), (3, 16384), (1, 65536)])
