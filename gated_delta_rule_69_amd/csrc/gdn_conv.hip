@@ -6,8 +6,8 @@
 // a run. A workgroup is 32 such threads across the channels and eight runs. Memory bounds it.
 //
 // bf16, four taps: 32,768 tokens of 6,144 channels 165 us (805 MB, 4.9 TB/s; a copy of 512 MiB reaches
-// 5.25), float32 8,192 x 2,048 26 us; one token of 512 sequences 13 us (50 MB, and 3 for the call); the
-// gradients of 8,192 x 6,144 73 us, 4 of them the weights' sums in a second kernel (4.1 TB/s: 160 registers,
+// 5.25), float32 8,192 x 2,048 26 us; one token of 512 sequences 11 us (50 MB); the
+// gradients of 8,192 x 6,144 71 us, 4 of them the weights' sums in a second kernel (4.1 TB/s: 160 registers,
 // three waves a SIMD, whose vector instructions take two thirds of the issue slots).
 #include <algorithm>
 
@@ -20,7 +20,6 @@ namespace {
 constexpr int kAcross = 32, kDown = 8, kThreads = kAcross * kDown;
 constexpr int kStep = 4;   // rows whose loads are under way together
 constexpr int kBackChannels = 4;   // channels a thread in the gradients: eight would take 210 registers, two waves a SIMD
-constexpr int64_t kFew = 8;   // tokens that go one by one
 
 struct Conv {
   const void* x;
@@ -331,6 +330,11 @@ int64_t run_of(const gdn_conv_args& a, bool back) {
   return run;
 }
 
+// Few tokens go one by one, more of them where the sequences alone fill the CUs (C 6144, bf16, against
+// runs: one sequence of 8 tokens 6.1 and 5.9 us, of 16 8.9 and 5.4; 64 sequences of 32 20.1 and 20.6, of 64
+// 36 and 23; 512 sequences of 32 97 and 120).
+int64_t few_tokens(const gdn_conv_args& a) { return a.B * columns_of(a, false) >= 1024 ? 32 : 8; }
+
 Conv conv_of(const gdn_conv_args& a, bool back) {
   Conv k{};
   k.x = a.x, k.w = a.w, k.bias = a.bias, k.lens = a.seq_lens, k.y = a.y;
@@ -363,16 +367,17 @@ int launch_conv_fwd(const ConvProblem& p, const void* s0, void* s_final, void* s
   hipStream_t s = static_cast<hipStream_t>(stream);
   Conv k = conv_of(p.a, false);
   k.s0 = s0, k.s_final = s_final;
-  if (p.a.T <= kFew) {
+  if (p.a.T <= few_tokens(p.a)) {
     const int64_t B = p.a.B;
     return by_width(p.a, [&](auto type, auto width, auto silu) {
       typedef decltype(type) E;
       constexpr int W = decltype(width)::value;
       constexpr bool S = decltype(silu)::value;
-      // four sequences a thread where that leaves every CU two workgroups
-      const int64_t four = (B + 4 * kDown - 1) / (4 * kDown) * k.columns;
-      if (four >= 512)
-        conv_step_kernel<E, W, S, 4><<<unsigned(four), kThreads, 0, s>>>(k, B);
+      // two sequences a thread where that leaves every CU two workgroups (C 6144, bf16: 512 sequences 11.1
+      // us against 13.4 with one, 8 sequences 4.4 against 3.7; four take 11.8 and 5.9)
+      const int64_t two = (B + 2 * kDown - 1) / (2 * kDown) * k.columns;
+      if (two >= 512)
+        conv_step_kernel<E, W, S, 2><<<unsigned(two), kThreads, 0, s>>>(k, B);
       else
         conv_step_kernel<E, W, S, 1><<<unsigned((B + kDown - 1) / kDown * k.columns), kThreads, 0, s>>>(k, B);
       return int(hipGetLastError());

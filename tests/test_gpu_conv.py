@@ -7,7 +7,8 @@ from oracle import block
 pytestmark = pytest.mark.gpu
 
 CASES = [(1, 1, 8, None), (2, 2, 24, None), (3, 3, 16, [3, 0, 1]), (1, 5, 264, None), (2, 31, 8, [2, 31]), (1, 64, 40, None),
-         (4, 65, 520, [65, 1, 33, 64]), (2, 257, 136, [-1, 300]), (1, 1000, 24, None), (2, 2049, 16, [2049, 2048])]
+         (4, 65, 520, [65, 1, 33, 64]), (2, 257, 136, [-1, 300]), (1, 1000, 24, None), (2, 2049, 16, [2049, 2048]),
+         (1030, 9, 8, None), (1030, 33, 8, None)]   # many sequences: up to 32 tokens one by one
 
 
 def _case(B, T, C, W, dt, seed, lens=None, bias=True):
