@@ -13,7 +13,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool dtype_ok(int d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; }
 
 // Sizes: every element offset stays far inside int64, every grid inside 31 bits and every
-// launch under 2^32 threads (64 for each of the 16 channels of a sequence).
+// launch under 2^32 threads (at most 128 a channel of a sequence).
 int sizes(int64_t B, int64_t T, int64_t C) {
   if (B < 1 || T < 0 || C < 8 || C % 8 != 0) return GDN_ERR_ARG;
   if (B > (1 << 20) || C > (1 << 16) || T > (int64_t(1) << 31) - (1 << 16)) return GDN_ERR_UNSUPPORTED;

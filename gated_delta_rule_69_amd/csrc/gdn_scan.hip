@@ -18,7 +18,7 @@ int64_t spans_of(int64_t T) { return (T + scan::kSpan - 1) / scan::kSpan; }
 // Segments of a sequence and the tokens of each. A workgroup walks its segment; where slices and
 // sequences alone leave CUs idle, segments of two tiles and more run side by side, at the price of a
 // first pass over the inputs for what each makes of the state (B2 T32768 C2048 bf16: 512 and 1,024
-// workgroups 289 and 282 us against 272 with 256; 300 tokens in one walk 12.6 against 16.6).
+// workgroups 223 and 268 us against 205 with 256; 300 tokens in one walk 13.1 against 16.4).
 void cut(const gdn_scan_args& a, bool back, unsigned* segs, int64_t* seg) {
   const int64_t tile = back ? scan::kBackTile : scan::kTile;
   const int64_t tiles = std::max<int64_t>(1, (a.T + tile - 1) / tile);

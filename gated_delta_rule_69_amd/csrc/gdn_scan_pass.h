@@ -1,12 +1,12 @@
 // The gated recurrence a channel, h_t = a_t h_{t-1} + b_t, over long sequences: kernels and
 // their launches for one element type.
 //
-// Eight lanes of a wave lie across the channels of a slice, four bytes a lane and row, and eight
-// groups of lanes hold a run of eight consecutive tokens each: a wave has a span of 64 tokens. A
-// lane joins the tokens of its run, the groups join theirs by DPP, the waves of a workgroup theirs
-// through LDS, a wave for each channel, and the workgroup walks the tiles of its segment with the
-// state it carries. Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no
-// division, so a decay may be 0, and nothing exceeds what the recurrence itself does.
+// Eight or 32 lanes of a wave lie across the channels of a slice, four bytes a lane and row, and groups
+// of such lanes hold a run of eight consecutive tokens each. A lane joins the tokens of its run, the
+// groups join theirs by DPP, the waves of a workgroup theirs through LDS, in a row of sixteen lanes
+// for each channel, and the workgroup walks the tiles of its segment with the state it carries.
+// Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no division, so a decay may be
+// 0, and nothing exceeds what the recurrence itself does.
 //
 // What a run leaves of the state before it is held twice: as the product A and as 1 - A,
 // summed from the 1 - a of its tokens. Where less than half goes, the state loses (1 - A) h
@@ -21,8 +21,8 @@
 //
 // Memory bounds it, as long as a CU's loads under way are long ones: rows of 32, 64 and 128 bytes a slice
 // took 308, 196 and 164 us for the second launch of B2 T32768 C2048 (bf16, sigmoid). Now 206 us in both
-// launches (805 MB, 3.9 TB/s; 176 with C 2112, whose rows do not start at the same 4 KiB), 147 for B8 T1024
-// C8192 with an input gate (537 MB), where one launch does; B1 T4096 C2048 39 us, two short launches. The
+// launches (805 MB, 3.9 TB/s; 176 with C 2112, whose rows do not start at the same 4 KiB), 145 for B8 T1024
+// C8192 with an input gate (537 MB), where one launch does; B1 T4096 C2048 25 us, two short launches. The
 // gradients of B2 T4096 C2048 with power and input gate 80 us (235 MB): their vector instructions, a
 // hundred a channel and token, are as much as their bytes.
 #pragma once
@@ -37,7 +37,7 @@ namespace scan {
 
 constexpr int kSpan = GDN_SCAN_SPAN;   // tokens between checkpoints
 constexpr int kRun = 8;                // tokens a lane joins by itself
-constexpr int kWaves = 16;             // waves a workgroup, each with a span of its own: a tile
+constexpr int kWaves = 16;             // waves a workgroup, each with tokens of its own: a tile
 constexpr int kBackWaves = 8;          // the same in the gradients, which take twice the registers
 
 // How a wave lies over rows and channels: LANES lanes across a slice, four bytes each, and groups of
@@ -165,9 +165,8 @@ struct Pass {
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
 // A buffer of `rows` rows (at most `most`, up to 64) of `width` bytes from `base` on, `ld` bytes
-// apart; none for rows <= 0.
-// Loads behind its last row give zero, stores are dropped. Strides are at most 2^26 bytes, so
-// a span's offsets fit in 32 bits.
+// apart; none for rows <= 0. Loads behind its last row give zero, stores are dropped. Strides are at
+// most 2^26 bytes, so that offsets fit in 32 bits.
 __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_t rows, int most, uint32_t width) {
   auto uniform = [](uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); };
   const uint64_t from = reinterpret_cast<uintptr_t>(base);
@@ -177,8 +176,9 @@ __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_
 
 // Rows on their way from memory to LDS, ahead of their use: a wave's own, so that nothing but its own
 // count of loads says when they are there. Lane l of a load brings sixteen bytes to the wave's place
-// 16 l: the rows r of the runs lie side by side there, at 256 r + kRow run, free of bank conflicts. The loads are written as assembly, which has no registers to guard;
-// the compiler's own counts only ever wait for more.
+// 16 l: the rows r of the runs lie side by side there, at 256 r + kRow run, free of bank conflicts. The
+// loads are written as assembly, which has no registers to guard; the compiler's own counts only ever
+// wait for more.
 template <int LANES> struct Feed {
   static constexpr int kRuns = Geo<LANES>::kRuns;
   uint32_t off[4], ld[4];
@@ -211,12 +211,15 @@ __device__ __forceinline__ void wait_memory() {
   static_assert(N < 64, "the counter has six bits");
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 template <typename E>
 __device__ __forceinline__ float part_of(uint32_t raw, int v) {
   if constexpr (sizeof(E) == 4) return __uint_as_float(raw);
   return v == 0 ? __uint_as_float(raw << 16) : __uint_as_float(raw & 0xffff0000u);
 }
+
 template <typename E>
 __device__ __forceinline__ uint32_t packed(const float* x) {
   if constexpr (sizeof(E) == 4) {
@@ -226,6 +229,7 @@ __device__ __forceinline__ uint32_t packed(const float* x) {
     return __builtin_bit_cast(uint32_t, r);
   }
 }
+
 // A lane's place among the rows r of a span in LDS, and its channels.
 template <int LANES> struct Lane {
   static constexpr int kApart = Geo<LANES>::kApart;
@@ -248,8 +252,8 @@ __device__ __forceinline__ void store_span(char* by, char* base, int64_t ld, int
     __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const uint4v*>(by + 1024 * j + 16 * lane), to, at + j * 4 * uint32_t(ld), 0, 0);
 }
 
-// Where a workgroup stands: blocks that follow each other on one XCD (their index modulo 8)
-// are neighbouring slices of one segment, which share lines.
+// Where a workgroup stands: blocks that follow each other on one XCD (their index modulo 8) are
+// neighbouring slices of one segment, which share lines where a slice has less than one (the gradients).
 struct Place {
   int64_t b;
   unsigned seg, slice;
@@ -294,27 +298,20 @@ template <int N, int NW> struct Exchange {
   float before[NW][N];
 };
 
-// The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes (in
-// turns, where there are more than four), whose lanes are the waves (BACK: from the last).
+// The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes, whose
+// lanes are the waves (BACK: from the last).
 template <int N, int NW, bool BACK> struct Keeper {
-  static constexpr int kOwn = N < NW ? 1 : N / NW, kTurns = kOwn <= 4 ? 1 : kOwn / 4;
-  int base, from, channels;   // first channel of the slice, the wave whose run the lane takes, channels there are
-  bool on, first;
-  State carry[kTurns];
-  __device__ __forceinline__ Keeper(int wave, int lane, int channels_) : channels(channels_) {
-    base = wave * kOwn + lane / 16;
+  static constexpr int kOwn = N < NW ? 1 : N / NW;
+  static_assert(kOwn <= 4, "a wave has four rows");
+  int ch, from;   // the row's channel in the slice, and the wave whose run the lane takes
+  bool on, there, first;
+  State carry = {0.0f, 0.0f};
+  __device__ __forceinline__ Keeper(int wave, int lane, int channels) {
+    ch = wave * kOwn + lane / 16;
     from = BACK ? NW - 1 - lane % 16 : lane % 16;
-    on = lane / 16 < kOwn && base < N;
-    first = on && lane % 16 == 0;
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) carry[t] = {0.0f, 0.0f};
-  }
-  // f(turn, channel) for each of the lane's channels that there are
-  template <typename F>
-  __device__ __forceinline__ void all(F f) const {
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t)
-      if (on && base + 4 * t < channels) f(t, base + 4 * t);
+    on = lane / 16 < kOwn && ch < N;
+    there = on && ch < channels;
+    first = there && lane % 16 == 0;
   }
   // Joins the runs of a row's lanes: up to and with the lane's, and of all.
   static __device__ __forceinline__ Run join_row(Run r, int lane, Run* whole) {
@@ -327,55 +324,43 @@ template <int N, int NW, bool BACK> struct Keeper {
     return r;
   }
   // The runs of a tile's waves.
-  __device__ __forceinline__ Run tile(const Exchange<N, NW>& x, int lane, int t, Run* whole) const {
+  __device__ __forceinline__ Run tile(const Exchange<N, NW>& x, int lane, Run* whole) const {
     Run r = empty_run();
     if (lane % 16 < NW) {
-      const float4 q = x.runs[base + 4 * t][from];
+      const float4 q = x.runs[ch][from];
       r = {q.x, q.y, q.z};
     }
     return join_row(r, lane, whole);
   }
-  // Passes the carried state over `count` segments, of(channel, k) the k-th to be passed: sixteen of
-  // them at a time, a lane each, for one after the other each would wait for its load.
+  // Passes the carried state over `count` segments, of(k) the k-th to be passed: sixteen of them at a
+  // time, a lane each, for one after the other each would wait for its load.
   template <typename F>
   __device__ __forceinline__ void over(int64_t count, int lane, F of) {
-    for (int64_t first = 0; first < count; first += 16) {
-      if (!on) continue;
-#pragma unroll
-      for (int t = 0; t < kTurns; ++t) {
-        Run r = empty_run(), whole;
-        if (first + lane % 16 < count && base + 4 * t < channels) r = of(base + 4 * t, first + lane % 16);
-        join_row(r, lane, &whole);
-        carry[t].pass(whole);
-      }
+    if (!on) return;
+    for (int64_t k = 0; k < count; k += 16) {
+      Run r = empty_run(), whole;
+      if (k + lane % 16 < count && there) r = of(k + lane % 16);
+      join_row(r, lane, &whole);
+      carry.pass(whole);
     }
   }
   // Passes the carried state over a tile; gives each wave its own.
   __device__ __forceinline__ void pass(Exchange<N, NW>& x, int lane) {
     if (!on) return;
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-      Run whole;
-      const Run r = tile(x, lane, t, &whole);
-      State s = carry[t];
-      s.pass(beside<1, false>(r));
-      if (lane % 16 < NW) x.before[from][base + 4 * t] = s.value();
-      carry[t].pass(whole);
-    }
+    Run whole;
+    const Run r = tile(x, lane, &whole);
+    State s = carry;
+    s.pass(beside<1, false>(r));
+    if (lane % 16 < NW) x.before[from][ch] = s.value();
+    carry.pass(whole);
   }
   // Joins a tile before those of `total`; whether nothing of what lies before can be left.
   __device__ __forceinline__ bool extend(const Exchange<N, NW>& x, int lane, Run* total) const {
-    bool gone = true;
-    if (on) {
-#pragma unroll
-      for (int t = 0; t < kTurns; ++t) {
-        Run whole;
-        tile(x, lane, t, &whole);
-        total[t] = join_settled(whole, total[t]);
-        gone = gone && (total[t].A == 0.0f || base + 4 * t >= channels);
-      }
-    }
-    return gone;
+    if (!on) return true;
+    Run whole;
+    tile(x, lane, &whole);
+    *total = join_settled(whole, *total);
+    return total->A == 0.0f || !there;
   }
 };
 
@@ -393,14 +378,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   const Lane<kLanes> l(lane);
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);   // a slice may end behind C
-  typedef Keeper<N, kWaves, false> Keep;
-  Keep keeper(wave, lane, channels);
+  Keeper<N, kWaves, false> keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   if (begin >= n && at.seg > 0) return;
   const bool last = n - begin <= p.seg;
-  if (TOTALS && at.seg == 0 && keeper.first)
-    keeper.all([&](int, int ch) { p.start[cb + ch] = p.h0 != nullptr ? p.h0[cb + ch] : 0.0f; });
+  if (TOTALS && at.seg == 0 && keeper.first) p.start[cb + keeper.ch] = p.h0 != nullptr ? p.h0[cb + keeper.ch] : 0.0f;
   if (TOTALS && last) return;
   const int64_t end = last ? n : begin + p.seg;
   Feed<kLanes> feed;
@@ -417,13 +400,11 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   fetch(first);
   const int64_t ldh = p.C * sizeof(E);
   char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * int64_t(sizeof(E));
-  Run total[Keep::kTurns];
-#pragma unroll
-  for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
+  Run total = empty_run();
   if constexpr (!TOTALS) {
     const float* from = p.segs > 1 ? p.start : p.h0;
-    if (from != nullptr) keeper.all([&](int t, int ch) { keeper.carry[t].hi = from[cb + ch]; });
-    keeper.over(at.seg, lane, [&](int ch, int64_t k) { return p.totals[(at.b * (p.segs - 1) + k) * p.C + c0 + ch]; });
+    if (from != nullptr && keeper.there) keeper.carry.hi = from[cb + keeper.ch];
+    keeper.over(at.seg, lane, [&](int64_t k) { return p.totals[(at.b * (p.segs - 1) + k) * p.C + c0 + keeper.ch]; });
   }
   float decay[V];
 #pragma unroll
@@ -469,7 +450,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
     }
     __syncthreads();
     if constexpr (TOTALS) {
-      return __syncthreads_and(keeper.extend(exchange, lane, total)) != 0;
+      return __syncthreads_and(keeper.extend(exchange, lane, &total)) != 0;
     } else {
       keeper.pass(exchange, lane);
       __syncthreads();
@@ -500,12 +481,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   if (!TOTALS && k < tiles) walk(std::false_type{}, k);
   wait_memory<0>();   // of LDS that the next workgroup may get
   if (!keeper.first) return;
-  keeper.all([&](int t, int ch) {
-    if constexpr (TOTALS)
-      p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + ch] = total[t];
-    else if (last && p.h_final != nullptr)
-      p.h_final[cb + ch] = keeper.carry[t].value();
-  });
+  if constexpr (TOTALS)
+    p.totals[(at.b * (p.segs - 1) + at.seg) * p.C + c0 + keeper.ch] = total;
+  else if (last && p.h_final != nullptr)
+    p.h_final[cb + keeper.ch] = keeper.carry.value();
 }
 
 // Gradients, from a sequence's end: with G_t = a_t (d_h_t + G_{t+1}) the same recurrence, whose
@@ -527,8 +506,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);
   const bool own_lane = uint32_t(l.slot * V) < channels;
-  typedef Keeper<N, kBackWaves, true> Keep;
-  Keep keeper(wave, lane, channels);
+  Keeper<N, kBackWaves, true> keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
@@ -573,13 +551,11 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     raw_decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f;
     decay[v] = scaled_decay<E>(raw_decay[v]), sum[v] = 0.0f;
   }
-  Run total[Keep::kTurns];
-#pragma unroll
-  for (int t = 0; t < Keep::kTurns; ++t) total[t] = empty_run();
+  Run total = empty_run();
   if constexpr (!TOTALS) {
-    if (p.d_final != nullptr) keeper.all([&](int t, int ch) { keeper.carry[t].hi = p.d_final[cb + ch]; });
+    if (p.d_final != nullptr && keeper.there) keeper.carry.hi = p.d_final[cb + keeper.ch];
     const int64_t last = (n + p.seg - 1) / p.seg - 1;   // the last segment with tokens
-    keeper.over(last - at.seg, lane, [&](int ch, int64_t k) { return p.totals[(at.b * (p.segs - 1) + last - k - 1) * p.C + c0 + ch]; });
+    keeper.over(last - at.seg, lane, [&](int64_t k) { return p.totals[(at.b * (p.segs - 1) + last - k - 1) * p.C + c0 + keeper.ch]; });
   }
   auto walk = [&](auto full, int64_t k) {
     constexpr bool FULL = decltype(full)::value;
@@ -662,7 +638,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     }
     __syncthreads();
     if constexpr (TOTALS) {
-      return __syncthreads_and(keeper.extend(exchange, lane, total)) != 0;
+      return __syncthreads_and(keeper.extend(exchange, lane, &total)) != 0;
     } else {
       keeper.pass(exchange, lane);
       __syncthreads();
@@ -712,12 +688,9 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   if (TOTALS && part && !gone) walk(std::false_type{}, k);
   wait_memory<0>();
   if constexpr (TOTALS) {
-    if (keeper.first)
-      keeper.all([&](int t, int ch) {
-        p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + ch] = total[t];
-      });
+    if (keeper.first) p.totals[(at.b * (p.segs - 1) + at.seg - 1) * p.C + c0 + keeper.ch] = total;
   } else {
-    if (at.seg == 0 && p.dh0 != nullptr && keeper.first) keeper.all([&](int t, int ch) { p.dh0[cb + ch] = keeper.carry[t].value(); });
+    if (at.seg == 0 && p.dh0 != nullptr && keeper.first) p.dh0[cb + keeper.ch] = keeper.carry.value();
     if (KIND == GDN_SCAN_POWER && p.ddecay != nullptr) {
       // over the lane groups, then the waves
 #pragma unroll
