@@ -32,13 +32,16 @@ __device__ __forceinline__ float sigmoid_of(float z) {
 }
 
 // out[c] = sum over rows of partial[row][c] for c < cols, split over up to three arrays of n0,
-// n1 and the remaining columns (NULL: dropped). A block has 32 columns, 32 threads a column
-// add up every 32nd row, then a tree of fixed order.
+// n1 and the remaining columns (NULL: dropped). The sums of out1 come times by1, and times by_also
+// in `also` (NULL: times one). A block has 32 columns, 32 threads a column add up every 32nd row,
+// then a tree of fixed order.
 struct ColumnSum {
   const float* partial;
   int rows;
   int64_t cols, n0, n1;
   float *out0, *out1, *out2;
+  float* also = nullptr;
+  const float *by1 = nullptr, *by_also = nullptr;
 };
 static __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSum a) {
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
@@ -55,8 +58,16 @@ static __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSum a) {
     if (threadIdx.x < step) part[threadIdx.x] += part[threadIdx.x + step];
   }
   if (threadIdx.x < 32 && c < a.cols) {
-    float* out = c < a.n0 ? a.out0 : c < a.n0 + a.n1 ? a.out1 : a.out2;
-    if (out != nullptr) out[c < a.n0 ? c : c < a.n0 + a.n1 ? c - a.n0 : c - a.n0 - a.n1] = part[threadIdx.x];
+    const float sum = part[threadIdx.x];
+    const int64_t c1 = c - a.n0;
+    if (c1 < 0) {
+      if (a.out0 != nullptr) a.out0[c] = sum;
+    } else if (c1 < a.n1) {
+      if (a.out1 != nullptr) a.out1[c1] = a.by1 != nullptr ? a.by1[c1] * sum : sum;
+      if (a.also != nullptr) a.also[c1] = a.by_also != nullptr ? a.by_also[c1] * sum : sum;
+    } else if (a.out2 != nullptr) {
+      a.out2[c1 - a.n1] = sum;
+    }
   }
 }
 inline int launch_column_sum(const ColumnSum& a, hipStream_t s) {

@@ -71,6 +71,13 @@ def test_block_norm_absent_inputs(absent, types):
     _compare(c, wide=False, post_norm=True, activation="silu")
 
 
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+@pytest.mark.parametrize("C,T", [(512, 2101), (1544, 1030), (4104, 519), (8200, 517)])
+def test_block_norm_many_rows(C, T, types):
+    """More rows than workgroups in the gradients: each walks several, the last fewer."""
+    _compare(_case(1, T, C, types, seed=C), wide=False, post_norm=True, activation="silu")
+
+
 @pytest.mark.parametrize("C", [8, 512, 2056, 8200])
 def test_block_norm_rows_at_odd_multiples_of_sixteen_bytes(C):
     """Float32 rows that start sixteen bytes after a multiple of 32: views four channels into tensors of
