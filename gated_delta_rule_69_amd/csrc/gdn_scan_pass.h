@@ -6,18 +6,24 @@
 // groups join theirs by DPP, the waves of a workgroup theirs through LDS, in a row of sixteen lanes
 // for each channel, and the workgroup walks the tiles of its segment with the state it carries.
 // Joining two runs of tokens is (A, h) (A', h') -> (A A', A' h + h'): no division, so a decay may be
-// 0, and nothing exceeds what the recurrence itself does.
+// 0.
 //
-// What a run leaves of the state before it is held twice: as the product A and as 1 - A,
-// summed from the 1 - a of its tokens. Where less than half goes, the state loses (1 - A) h
-// instead of being multiplied by a rounded A near 1, whose error a channel that keeps many
-// tokens would add up at every step; and the state a workgroup carries is a sum of two
-// floats, for the same reason.
+// SIGMOID and POWER, whose a is at most 1: what a run leaves of the state before it is held
+// twice, as the product A and as 1 - A, summed from the 1 - a of its tokens. Where less than half
+// goes, the state loses (1 - A) h instead of being multiplied by a rounded A near 1, whose error a
+// channel that keeps many tokens would add up at every step; and the state a workgroup carries
+// is a sum of two floats, for the same reason.
+//
+// LOG, whose a may exceed 1: 1 - A of a run that grew is a large number, in which what a later run
+// takes away is lost to rounding, and A itself may leave float32's range where the state does not
+// (a thousand tokens that grow an empty state). So what a run leaves is held as log2 A, from the sum of
+// its f, in two floats, and 1 - A is formed from that where a state is passed on.
 //
 // Where slices and sequences do not fill the CUs, segments of a sequence run side by side: a first
 // launch finds what each makes of the state before it, walking it from its end until nothing before
-// can be left in float32 (a thousand tokens and more under forget gates of logits around 3), and the
-// second joins those before its own.
+// can be left in float32 (a thousand tokens and more under forget gates of logits around 3; twice as
+// many under LOG, where the tokens before may have grown the state), and the second joins those before
+// its own.
 //
 // Memory bounds it, as long as a CU's loads under way are long ones: rows of 32, 64 and 128 bytes a slice
 // took 308, 196 and 164 us for the second launch of B2 T32768 C2048 (bf16, sigmoid). Now 206 us in both
@@ -55,6 +61,12 @@ constexpr int kLanes = 32, kBackLanes = 8;
 constexpr int kTile = kWaves * Geo<kLanes>::kTokens, kBackTile = kBackWaves * Geo<kBackLanes>::kTokens;
 static_assert(Geo<kBackLanes>::kTokens == kSpan, "a checkpoint is the state before a wave's tokens");
 
+// 1 - e^y for |y| < 1/4: the series' next term, y^8 / 9!, is 2^-34 of the first.
+__device__ __forceinline__ float less_exp(float y) {
+  const float p = 1.0f / 24 + y * (1.0f / 120 + y * (1.0f / 720 + y * (1.0f / 5040 + y * (1.0f / 40320))));
+  return -y * (1.0f + y * (0.5f + y * (1.0f / 6 + y * p)));
+}
+
 // e^y and 1 - e^y for y <= 0 (and what they are above), the second to a few steps of its own: a series
 // where the difference would cancel. For bf16 y comes times log2 e, which takes one instruction for 2^y;
 // for float32 as it is.
@@ -68,10 +80,9 @@ __device__ __forceinline__ void exp_both(float y, float* a, float* c) {
     p = -L + y * (-L * L / 2 + y * (-L * L * L / 6 + y * (-L * L * L * L / 24 + y * (-L * L * L * L * L / 120))));
     p *= y;
     near = fabsf(y) < 0.36f;
-  } else {                          // y^8 / 9! is 2^-34
+  } else {
     *a = expf(y);
-    p = 1.0f / 24 + y * (1.0f / 120 + y * (1.0f / 720 + y * (1.0f / 5040 + y * (1.0f / 40320))));
-    p = -y * (1.0f + y * (0.5f + y * (1.0f / 6 + y * p)));
+    p = less_exp(y);
     near = fabsf(y) < 0.25f;
   }
   // both sides in every lane: a branch for the series costs more than it
@@ -79,8 +90,8 @@ __device__ __forceinline__ void exp_both(float y, float* a, float* c) {
   *c = near ? p : 1.0f - *a;
 }
 
-// A token's factors: h = a h + m g x with c = 1 - a. s and rest (sigmoid(f) and its
-// complement) are the gradients'.
+// A token's factors: h = a h + m g x with c = 1 - a (LOG, but for STEP: c = ln a, finite). s and rest
+// (sigmoid(f) and its complement) are the gradients'.
 struct Gate {
   float a, c, m, s, rest;
 };
@@ -89,11 +100,17 @@ template <typename E>
 __device__ __forceinline__ float scaled_decay(float decay) {
   return sizeof(E) == 2 ? -1.44269504089f * decay : -decay;
 }
-template <typename E, int KIND>
+template <typename E, int KIND, bool STEP = false>
 __device__ __forceinline__ Gate gate_of(float f, float decay) {
   Gate g;
   if constexpr (KIND == GDN_SCAN_LOG) {
-    exp_both<E>(sizeof(E) == 2 ? 1.44269504089f * f : f, &g.a, &g.c);
+    if constexpr (STEP) {
+      exp_both<E>(sizeof(E) == 2 ? 1.44269504089f * f : f, &g.a, &g.c);
+    } else {
+      g.a = exp_of<E>(f);
+      // sums of two floats know no infinity; 1e28 a token is one to any state, and 2^31 of them add up
+      g.c = __builtin_amdgcn_fmed3f(f, -1e28f, 1e28f);
+    }
     g.m = 1.0f;
     g.s = g.rest = 0.0f;
   } else {
@@ -111,29 +128,93 @@ __device__ __forceinline__ Gate gate_of(float f, float decay) {
   return g;
 }
 
-// A run of tokens: what is left of the state before it (A, and C = 1 - A), and what it adds.
+// A run of tokens: what is left of the state before it (A, and C = 1 - A; LOG: the two floats whose
+// sum is log2 A), and what it adds.
 struct Run {
   float A, C, H;
 };
-__device__ __forceinline__ Run empty_run() { return {1.0f, 0.0f, 0.0f}; }
-__device__ __forceinline__ Run join(const Run& first, const Run& then) {
-  return {first.A * then.A, fmaf(then.C, first.A, first.C), fmaf(then.A, first.H, then.H)};
+
+// x 2^(hi + lo): 2 to the whole part by the exponent, so that no factor on the way leaves float32's
+// range unless the result does. Beyond 2^1000 it is 0 or infinite for every x.
+__device__ __forceinline__ float times_exp2(float x, float hi, float lo) {
+  const float n = rintf(__builtin_amdgcn_fmed3f(hi, -1000.0f, 1000.0f));
+  const float r = __builtin_amdgcn_fmed3f((hi - n) + lo, -1.0f, 1.0f);
+  return ldexpf(x * __builtin_amdgcn_exp2f(r), int(n));
 }
 
-// The product of rounded A's is off by a step for each of them, 1 - C by one: where a run leaves more
-// than half, that is its A.
-__device__ __forceinline__ Run settle(const Run& r) { return {r.C < 0.5f ? 1.0f - r.C : r.A, r.C, r.H}; }
-__device__ __forceinline__ Run join_settled(const Run& first, const Run& then) { return settle(join(first, then)); }
+template <bool LOG> struct Runs;
+
+template <> struct Runs<false> {
+  static __device__ __forceinline__ Run empty() { return {1.0f, 0.0f, 0.0f}; }
+  static __device__ __forceinline__ Run join(const Run& first, const Run& then) {
+    return {first.A * then.A, fmaf(then.C, first.A, first.C), fmaf(then.A, first.H, then.H)};
+  }
+  template <typename E>
+  static __device__ __forceinline__ Run token(const Run& first, float a, float c, float add) { return join(first, {a, c, add}); }
+  static __device__ __forceinline__ Run close(const Run& r) { return r; }
+  // The product of rounded A's is off by a step for each of them, 1 - C by one: where a run leaves more
+  // than half, that is its A.
+  static __device__ __forceinline__ Run settle(const Run& r) { return {r.C < 0.5f ? 1.0f - r.C : r.A, r.C, r.H}; }
+  static __device__ __forceinline__ Run join_settled(const Run& first, const Run& then) { return settle(join(first, then)); }
+  // The state x behind the run.
+  static __device__ __forceinline__ float after(const Run& r, float x) { return fmaf(r.A, x, r.H); }
+  // Nothing of what lies before can be left.
+  static __device__ __forceinline__ bool gone(const Run& r) { return r.A == 0.0f; }
+};
+
+template <> struct Runs<true> {
+  static __device__ __forceinline__ Run empty() { return {0.0f, 0.0f, 0.0f}; }
+  // The logarithms' sum, its rounding's rest with the lower parts.
+  static __device__ __forceinline__ Run add(const Run& first, float hi, float lo, float H) {
+    const float sum = first.A + hi, back = sum - first.A;
+    return {sum, first.C + lo + ((first.A - (sum - back)) + (hi - back)), H};
+  }
+  static __device__ __forceinline__ Run join(const Run& first, const Run& then) {
+    return add(first, then.A, then.C, times_exp2(first.H, then.A, then.C) + then.H);
+  }
+  // A lane's own tokens, one by one: A is the sum of f. Eight numbers of eight bits add up without a
+  // rounding as long as they are within 2^13 of each other.
+  template <typename E>
+  static __device__ __forceinline__ Run token(const Run& first, float a, float f, float more) {
+    const float H = fmaf(a, first.H, more);
+    if constexpr (sizeof(E) == 2) return {first.A + f, 0.0f, H};
+    return add(first, f, 0.0f, H);
+  }
+  // From the sum of f to log2 A.
+  static __device__ __forceinline__ Run close(const Run& r) {
+    constexpr float K = 1.44269504089f, REST = 1.92596299e-8f;   // log2 e, and what K is off by
+    const float hi = K * r.A;
+    return {hi, fmaf(K, r.C, fmaf(REST, r.A, fmaf(K, r.A, -hi))), r.H};
+  }
+  static __device__ __forceinline__ Run settle(const Run& r) { return r; }
+  static __device__ __forceinline__ Run join_settled(const Run& first, const Run& then) { return join(first, then); }
+  static __device__ __forceinline__ float after(const Run& r, float x) { return times_exp2(x, r.A, r.C) + r.H; }
+  // The tokens before may have grown the state to the largest float, 2^128: of that less than half of
+  // the smallest, 2^-149, is left. (B2 T32768 C2048 bf16, f around -0.05: 46 us for the first launch, 29 if
+  // it stopped at a product of 2^-149, which states that had grown before would miss.)
+  static __device__ __forceinline__ bool gone(const Run& r) { return r.A <= -279.0f; }
+};
 
 // A state held as hi + lo.
-struct State {
+template <bool LOG> struct State {
   float hi, lo;
   __device__ __forceinline__ void pass(const Run& r) {
-    const bool slow = r.C < 0.5f;
-    const float base = slow ? hi : r.A * hi;
-    const float add = slow ? fmaf(-r.C, hi, r.H) : r.H;
+    bool slow;
+    float base, add, low;
+    if constexpr (LOG) {
+      const float y = 0.69314718056f * r.A, c = fabsf(y) < 0.25f ? less_exp(y) : 1.0f - __builtin_amdgcn_exp2f(r.A);
+      slow = fabsf(c) < 0.5f;
+      base = slow ? hi : times_exp2(hi, r.A, r.C);
+      add = slow ? fmaf(-c, hi, r.H) : r.H;
+      low = times_exp2(lo, r.A, r.C);
+    } else {
+      slow = r.C < 0.5f;
+      base = slow ? hi : r.A * hi;
+      add = slow ? fmaf(-r.C, hi, r.H) : r.H;
+      low = lo * r.A;
+    }
     const float sum = base + add, back = sum - base;
-    lo = lo * r.A + ((base - (sum - back)) + (add - back));
+    lo = low + ((base - (sum - back)) + (add - back));
     hi = sum;
   }
   // hi + lo where lo is a rounding's rest, hi where that is none (infinities)
@@ -272,22 +353,22 @@ template <int N, bool BACK>
 __device__ __forceinline__ float beside(float x, float none) {
   return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(x), (BACK ? 0x100 : 0x110) + N, 0xf, 0xf, false));
 }
-template <int N, bool BACK>
+template <int N, bool BACK, bool LOG>
 __device__ __forceinline__ Run beside(const Run& r) {
-  return {beside<N, BACK>(r.A, 1.0f), beside<N, BACK>(r.C, 0.0f), beside<N, BACK>(r.H, 0.0f)};
+  return {beside<N, BACK>(r.A, Runs<LOG>::empty().A), beside<N, BACK>(r.C, 0.0f), beside<N, BACK>(r.H, 0.0f)};
 }
 
 // Joins over the lane groups: own becomes the runs up to and with the lane's (BACK: from the last one
-// down to it), before those without it. Without C (AH) A is the product.
-template <int V, int LANES, bool BACK, bool AH>
+// down to it), before those without it. Without C (AH; not LOG) A is the product.
+template <int V, int LANES, bool BACK, bool AH, bool LOG>
 __device__ __forceinline__ void join_lanes(Run* own, Run* before) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    auto take = [&](const Run& o) { own[v] = AH ? join(o, own[v]) : join_settled(o, own[v]); };
-    if constexpr (Geo<LANES>::kRuns >= 8) take(beside<2, BACK>(own[v]));
-    if constexpr (Geo<LANES>::kRuns >= 4) take(beside<4, BACK>(own[v]));
-    take(beside<8, BACK>(own[v]));
-    before[v] = beside<Geo<LANES>::kApart, BACK>(own[v]);
+    auto take = [&](const Run& o) { own[v] = AH ? Runs<LOG>::join(o, own[v]) : Runs<LOG>::join_settled(o, own[v]); };
+    if constexpr (Geo<LANES>::kRuns >= 8) take(beside<2, BACK, LOG>(own[v]));
+    if constexpr (Geo<LANES>::kRuns >= 4) take(beside<4, BACK, LOG>(own[v]));
+    take(beside<8, BACK, LOG>(own[v]));
+    before[v] = beside<Geo<LANES>::kApart, BACK, LOG>(own[v]);
   }
 }
 
@@ -300,12 +381,12 @@ template <int N, int NW> struct Exchange {
 
 // The channels that a wave carries the state of, N / NW of them: one a row of sixteen lanes, whose
 // lanes are the waves (BACK: from the last).
-template <int N, int NW, bool BACK> struct Keeper {
+template <int N, int NW, bool BACK, bool LOG> struct Keeper {
   static constexpr int kOwn = N < NW ? 1 : N / NW;
   static_assert(kOwn <= 4, "a wave has four rows");
   int ch, from;   // the row's channel in the slice, and the wave whose run the lane takes
   bool on, there, first;
-  State carry = {0.0f, 0.0f};
+  State<LOG> carry = {0.0f, 0.0f};
   __device__ __forceinline__ Keeper(int wave, int lane, int channels) {
     ch = wave * kOwn + lane / 16;
     from = BACK ? NW - 1 - lane % 16 : lane % 16;
@@ -315,17 +396,17 @@ template <int N, int NW, bool BACK> struct Keeper {
   }
   // Joins the runs of a row's lanes: up to and with the lane's, and of all.
   static __device__ __forceinline__ Run join_row(Run r, int lane, Run* whole) {
-    r = join_settled(beside<1, false>(r), r);
-    r = join_settled(beside<2, false>(r), r);
-    r = join_settled(beside<4, false>(r), r);
-    r = join_settled(beside<8, false>(r), r);
+    r = Runs<LOG>::join_settled(beside<1, false, LOG>(r), r);
+    r = Runs<LOG>::join_settled(beside<2, false, LOG>(r), r);
+    r = Runs<LOG>::join_settled(beside<4, false, LOG>(r), r);
+    r = Runs<LOG>::join_settled(beside<8, false, LOG>(r), r);
     const int end = lane | 15;
     *whole = {__shfl(r.A, end), __shfl(r.C, end), __shfl(r.H, end)};
     return r;
   }
   // The runs of a tile's waves.
   __device__ __forceinline__ Run tile(const Exchange<N, NW>& x, int lane, Run* whole) const {
-    Run r = empty_run();
+    Run r = Runs<LOG>::empty();
     if (lane % 16 < NW) {
       const float4 q = x.runs[ch][from];
       r = {q.x, q.y, q.z};
@@ -338,7 +419,7 @@ template <int N, int NW, bool BACK> struct Keeper {
   __device__ __forceinline__ void over(int64_t count, int lane, F of) {
     if (!on) return;
     for (int64_t k = 0; k < count; k += 16) {
-      Run r = empty_run(), whole;
+      Run r = Runs<LOG>::empty(), whole;
       if (k + lane % 16 < count && there) r = of(k + lane % 16);
       join_row(r, lane, &whole);
       carry.pass(whole);
@@ -349,8 +430,8 @@ template <int N, int NW, bool BACK> struct Keeper {
     if (!on) return;
     Run whole;
     const Run r = tile(x, lane, &whole);
-    State s = carry;
-    s.pass(beside<1, false>(r));
+    State<LOG> s = carry;
+    s.pass(beside<1, false, LOG>(r));
     if (lane % 16 < NW) x.before[from][ch] = s.value();
     carry.pass(whole);
   }
@@ -359,8 +440,8 @@ template <int N, int NW, bool BACK> struct Keeper {
     if (!on) return true;
     Run whole;
     tile(x, lane, &whole);
-    *total = join_settled(whole, *total);
-    return total->A == 0.0f || !there;
+    *total = Runs<LOG>::join_settled(whole, *total);
+    return Runs<LOG>::gone(*total) || !there;
   }
 };
 
@@ -369,6 +450,7 @@ template <int N, int NW, bool BACK> struct Keeper {
 template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   constexpr int V = 4 / int(sizeof(E)), N = Geo<kLanes>::kChannels<E>, NT = IG ? 3 : 2, kTokens = Geo<kLanes>::kTokens;
+  constexpr bool LOG = KIND == GDN_SCAN_LOG;
   __shared__ __attribute__((aligned(16))) char raw[kWaves][NT][64 * 4 * kRun];
   __shared__ __attribute__((aligned(16))) char out[kWaves][TOTALS ? 16 : 64 * 4 * kRun];
   __shared__ Exchange<N, kWaves> exchange;
@@ -378,7 +460,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   const Lane<kLanes> l(lane);
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);   // a slice may end behind C
-  Keeper<N, kWaves, false> keeper(wave, lane, channels);
+  Keeper<N, kWaves, false, LOG> keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   if (begin >= n && at.seg > 0) return;
@@ -400,7 +482,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
   fetch(first);
   const int64_t ldh = p.C * sizeof(E);
   char* h = static_cast<char*>(p.h) + at.b * p.T * ldh + c0 * int64_t(sizeof(E));
-  Run total = empty_run();
+  Run total = Runs<LOG>::empty();
   if constexpr (!TOTALS) {
     const float* from = p.segs > 1 ? p.start : p.h0;
     if (from != nullptr && keeper.there) keeper.carry.hi = from[cb + keeper.ch];
@@ -427,7 +509,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
     float a[kRun][V], b[kRun][V];
     Run own[V], before[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) own[v] = empty_run();
+    for (int v = 0; v < V; ++v) own[v] = Runs<LOG>::empty();
 #pragma unroll
     for (int r = 0; r < kRun; ++r) {
       const bool here = FULL || l.run * kRun + r < left;
@@ -438,12 +520,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
         b[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[0][r], v) : t.m * part_of<E>(in[0][r], v);
         if constexpr (IG) b[r][v] *= sigmoid_of<E>(part_of<E>(in[2][r], v));
         if (!here) b[r][v] = 0.0f;
-        own[v] = join(own[v], Run{a[r][v], here ? t.c : 0.0f, b[r][v]});
+        own[v] = Runs<LOG>::template token<E>(own[v], a[r][v], here ? t.c : 0.0f, b[r][v]);
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) own[v] = settle(own[v]);
-    join_lanes<V, kLanes, false, false>(own, before);
+    for (int v = 0; v < V; ++v) own[v] = Runs<LOG>::settle(Runs<LOG>::close(own[v]));
+    join_lanes<V, kLanes, false, false, LOG>(own, before);
     if (l.run == Geo<kLanes>::kRuns - 1) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
@@ -456,7 +538,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_kernel(Pass p) {
       __syncthreads();
       float y[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) y[v] = fmaf(before[v].A, exchange.before[wave][l.slot * V + v], before[v].H);
+      for (int v = 0; v < V; ++v) y[v] = Runs<LOG>::after(before[v], exchange.before[wave][l.slot * V + v]);
       if (p.marks != nullptr && l.run == 0 && uint32_t(l.slot * V) < channels && left > 0 && t0 % kSpan == 0) {
         float* m = p.marks + (at.b * ((p.T + kSpan - 1) / kSpan) + t0 / kSpan) * p.C + c0 + l.slot * V;
 #pragma unroll
@@ -494,6 +576,7 @@ template <typename E, int KIND, bool IG, bool TOTALS>
 __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   constexpr int V = 4 / int(sizeof(E)), N = Geo<kBackLanes>::kChannels<E>, R = kRun, kRuns = Geo<kBackLanes>::kRuns;
   constexpr int NT = TOTALS ? 2 : IG ? 4 : 3, kLoads = 2 * NT + (TOTALS ? 0 : 1), kStores = TOTALS ? 0 : IG ? 6 : 4;
+  constexpr bool LOG = KIND == GDN_SCAN_LOG;
   __shared__ __attribute__((aligned(16))) char raw[2][kBackWaves][NT][64 * 4 * kRun];
   __shared__ __attribute__((aligned(16))) char raw_marks[2][kBackWaves][TOTALS ? 16 : 256];
   __shared__ __attribute__((aligned(16))) char out[kBackWaves][TOTALS ? 16 : 64 * 4 * kRun];
@@ -506,7 +589,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
   const int64_t c0 = int64_t(at.slice) * N, cb = at.b * p.C + c0;
   const uint32_t channels = p.C - c0 < N ? uint32_t(p.C - c0) : N, width = channels * sizeof(E);
   const bool own_lane = uint32_t(l.slot * V) < channels;
-  Keeper<N, kBackWaves, true> keeper(wave, lane, channels);
+  Keeper<N, kBackWaves, true, LOG> keeper(wave, lane, channels);
   const int64_t n = tokens_of(p.lens, at.b, p.T);
   const int64_t begin = at.seg * p.seg;
   const int64_t stop = std::min(begin + p.seg, p.T), end = std::min(stop, n);
@@ -551,7 +634,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     raw_decay[v] = KIND == GDN_SCAN_POWER && own_lane ? p.decay[c0 + l.slot * V + v] : 0.0f;
     decay[v] = scaled_decay<E>(raw_decay[v]), sum[v] = 0.0f;
   }
-  Run total = empty_run();
+  Run total = Runs<LOG>::empty();
   if constexpr (!TOTALS) {
     if (p.d_final != nullptr && keeper.there) keeper.carry.hi = p.d_final[cb + keeper.ch];
     const int64_t last = (n + p.seg - 1) / p.seg - 1;   // the last segment with tokens
@@ -586,7 +669,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
     float si[R][V], resti[R][V], before[R][V];
     Run own[V], lanes[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) own[v] = empty_run();
+    for (int v = 0; v < V; ++v) own[v] = Runs<LOG>::empty();
     // G of the run, from its last token
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
@@ -597,7 +680,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
         t = gate_of<E, KIND>(part_of<E>(in[0][r], v), decay[v]);
         if (!here) t.a = 1.0f;
         const float up = part_of<E>(in[1][r], v);
-        own[v] = join(own[v], Run{t.a, here ? t.c : 0.0f, here ? t.a * up : 0.0f});
+        own[v] = Runs<LOG>::template token<E>(own[v], t.a, here ? t.c : 0.0f, here ? t.a * up : 0.0f);
         if constexpr (!TOTALS) {
           before[r][v] = KIND == GDN_SCAN_LOG ? part_of<E>(in[2][r], v) : t.m * part_of<E>(in[2][r], v);
           if constexpr (IG) {
@@ -608,19 +691,21 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
         }
       }
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) own[v] = Runs<LOG>::close(own[v]);
     if constexpr (!TOTALS) {
       // h before each token: from what each adds
       Run fwd[V], earlier[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        fwd[v] = {own[v].A, 0.0f, 0.0f};
+        fwd[v] = {own[v].A, LOG ? own[v].C : 0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < R; ++r) fwd[v].H = fmaf(gate[r][v].a, fwd[v].H, before[r][v]);
       }
-      join_lanes<V, kBackLanes, false, true>(fwd, earlier);
+      join_lanes<V, kBackLanes, false, true, LOG>(fwd, earlier);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float y = fmaf(earlier[v].A, mark[v], earlier[v].H);
+        float y = Runs<LOG>::after(earlier[v], mark[v]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float add = before[r][v];
@@ -630,8 +715,8 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) own[v] = settle(own[v]);
-    join_lanes<V, kBackLanes, true, false>(own, lanes);
+    for (int v = 0; v < V; ++v) own[v] = Runs<LOG>::settle(own[v]);
+    join_lanes<V, kBackLanes, true, false, LOG>(own, lanes);
     if (l.run == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) exchange.runs[l.slot * V + v][wave] = make_float4(own[v].A, own[v].C, own[v].H, 0.0f);
@@ -644,7 +729,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void scan_bwd_kernel(Pass p) {
       __syncthreads();
       float G[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) G[v] = fmaf(lanes[v].A, exchange.before[wave][l.slot * V + v], lanes[v].H);
+      for (int v = 0; v < V; ++v) G[v] = Runs<LOG>::after(lanes[v], exchange.before[wave][l.slot * V + v]);
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) {
         const bool here = FULL || l.run * R + r < left;
@@ -752,7 +837,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(Pass p) {
       if (p.marks != nullptr && t % kSpan == 0) store4(p.marks + (b * ((p.T + kSpan - 1) / kSpan) + t / kSpan) * p.C + c, h);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const Gate q = gate_of<E, KIND>(float(rf[k][v]), decay[v]);
+        const Gate q = gate_of<E, KIND, true>(float(rf[k][v]), decay[v]);
         float add = q.m * float(rx[k][v]);
         if constexpr (IG) add *= sigmoid_of<E>(float(ri[k][v]));
         h[v] = q.c < 0.5f ? h[v] + fmaf(-q.c, h[v], add) : fmaf(q.a, h[v], add);

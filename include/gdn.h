@@ -447,7 +447,8 @@ int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_gra
  *
  *     h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t,     elementwise over C channels
  *
- *   LOG      a = e^f (f <= 0; above 0 is not checked and grows the state), m = 1
+ *   LOG      a = e^f, m = 1 (f <= 0 forgets; above 0 the state grows, as far as float32 holds it and
+ *            e^f itself; long stretches of either may follow each other)
  *   SIGMOID  a = sigmoid(f), m = 1 - a
  *   POWER    a = e^{-decay_c sigmoid(f)} (decay [C] >= 0), m = sqrt(1 - a^2)
  * and without i its factor is 1. 1 - a is computed as it is, not as a difference, so that
@@ -464,9 +465,10 @@ int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_gra
  * GDN_ERR_UNSUPPORTED above C = 2^16, B * C = 2^24, and the limits of B, T, B * T and strides
  * of the linear entry points. The state is float32; a sequence's tokens are joined in a tree that
  * goes by the sizes alone. A NaN or Inf in row t makes its channel of h NaN or Inf from t on, at
- * least as long as its weight, the product of the a's since, is over 2^-127, and nothing else;
- * behind that weight nothing is promised (0 times NaN is NaN within a part of the sequence, while
- * rows that weigh nothing are not read from the next). The same holds along the gradients'
+ * least as long as its weight, the product of the a's since (and from any row since, where LOG has
+ * a's over 1), is over 2^-127, and nothing else; behind that weight nothing is promised (0 times
+ * NaN is NaN within a part of the sequence, while rows that weigh nothing are not read from the
+ * next). The same holds along the gradients'
  * formulas, from a row backwards. */
 enum gdn_scan_gate { GDN_SCAN_LOG = 1, GDN_SCAN_SIGMOID = 2, GDN_SCAN_POWER = 3 };
 #define GDN_SCAN_SPAN 64
