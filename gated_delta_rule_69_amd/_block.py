@@ -229,7 +229,8 @@ def gdn_short_conv_fwd(x, w, bias=None, *, activation="silu", s0=None, s_final=N
     """Causal convolution a channel over the last W tokens, z_t = bias + sum_j w[:, j] x_{t-W+1+j}
     and y = silu(z) ("silu") or z (None): x [B, T, C], float32 w [C, W] (W 2, 3 or 4) and bias [C].
     s0 and s_final [B, W - 1, C] hold the last inputs, oldest first, in x's dtype. Returns (y,
-    s_final), allocated when not given; s_final may be s0. ``seq_lens`` as for gdn_gated_scan_fwd."""
+    s_final), allocated when not given; s_final may be s0, and y may be x for up to 8 tokens
+    (contiguous; refused for more, whose rows are read again). ``seq_lens`` as for gdn_gated_scan_fwd."""
     if _elsewhere(x, "x", stream):
         with _on(x, stream):
             return gdn_short_conv_fwd(x, w, bias, activation=activation, s0=s0, s_final=s_final, y=y, seq_lens=seq_lens,
@@ -254,7 +255,7 @@ def gdn_short_conv_fwd(x, w, bias=None, *, activation="silu", s0=None, s_final=N
 
 def gdn_short_conv_step(x, w, bias=None, *, state, activation="silu", y=None, seq_lens=None, stream=None):
     """The same with ``state`` [B, W - 1, C] read and replaced: T = 1 is one decode step. Returns
-    y. A sequence of length 0 keeps its state."""
+    y, which may be x as above. A sequence of length 0 keeps its state."""
     if _elsewhere(x, "x", stream):
         with _on(x, stream):
             return gdn_short_conv_step(x, w, bias, state=state, activation=activation, y=y, seq_lens=seq_lens)

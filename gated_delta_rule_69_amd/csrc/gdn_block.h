@@ -29,6 +29,8 @@ size_t scan_bwd_workspace(const ScanProblem& p);
 int launch_scan_bwd(const ScanProblem& p, const void* d_h, const float* d_h_final, const gdn_scan_grads& g, void* ws,
                     void* stream);
 
+// Tokens up to which a convolution always goes one by one, so that y may be x.
+constexpr int64_t kConvInPlace = 8;
 int launch_conv_fwd(const ConvProblem& p, const void* s0, void* s_final, void* stream);
 size_t conv_bwd_workspace(const ConvProblem& p);
 int launch_conv_bwd(const ConvProblem& p, const void* d_y, const void* d_s_final, const gdn_conv_grads& g, void* ws,

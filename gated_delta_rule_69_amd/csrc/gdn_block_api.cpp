@@ -36,6 +36,17 @@ bool ws_ok(const void* ws, size_t bytes, size_t need) {
 // An array of T rows a sequence: NULL only where there are none.
 bool rows_ok(const void* p, int64_t T) { return aligned16(p) && (T == 0 || p != nullptr); }
 
+int64_t size_of(int dtype) { return dtype == GDN_DTYPE_BF16 ? 2 : 4; }
+
+// Whether `bytes` from `out` on meet one of `rows` rows of `width` bytes from `in` on, `ld` >= width
+// bytes apart. Absent arrays meet nothing.
+bool meets(const void* out, int64_t bytes, const void* in, int64_t rows, int64_t width, int64_t ld) {
+  if (out == nullptr || in == nullptr) return false;
+  const int64_t at = int64_t(reinterpret_cast<uintptr_t>(out)) - int64_t(reinterpret_cast<uintptr_t>(in));
+  const int64_t r = at < width ? 0 : (at - width) / ld + 1;   // the first row that ends behind out's start
+  return r < rows && r * ld < at + bytes;
+}
+
 int hip_status(int rc) { return rc == 0 ? GDN_OK : GDN_ERR_HIP; }
 
 int scan_check(const gdn_scan_args* a, ScanProblem* p) {
@@ -96,6 +107,15 @@ int norm_pointers(const gdn_block_norm_args& a) {
   if (!rows_ok(a.r, a.T) || !aligned16(a.y) || !aligned16(a.gate)) return GDN_ERR_ARG;
   if (!aligned16(a.scale) || !aligned16(a.post_weight) || !aligned16(a.weight)) return GDN_ERR_ARG;
   return GDN_OK;
+}
+
+// y apart from x, or x itself while one thread walks a sequence's tokens in turn: else a run of tokens reads
+// the rows before it after another thread may have replaced them.
+bool conv_rows_apart(const gdn_conv_args& a) {
+  const int64_t width = a.C * size_of(a.dtype), ld = a.x_stride * size_of(a.dtype);
+  const int64_t rows = a.B * a.T;
+  return !meets(a.y, rows * width, a.x, rows, width, ld) ||
+         (a.y == a.x && (ld == width || rows == 1) && a.T <= kConvInPlace);
 }
 
 // In place only row over row, element over element.
@@ -166,7 +186,7 @@ int gdn_short_conv_fwd(const gdn_conv_args* args, void* stream) {
   if (st == GDN_OK) st = conv_pointers(p.a);
   if (st != GDN_OK) return st;
   const gdn_conv_args& a = p.a;
-  if (!rows_ok(a.y, a.T) || !aligned16(a.s0) || !aligned16(a.s_final)) return GDN_ERR_ARG;
+  if (!rows_ok(a.y, a.T) || !aligned16(a.s0) || !aligned16(a.s_final) || !conv_rows_apart(a)) return GDN_ERR_ARG;
   if (a.T == 0 && (a.s_final == nullptr || a.s_final == a.s0)) return GDN_OK;
   return hip_status(launch_conv_fwd(p, a.s0, a.s_final, stream));
 }
@@ -176,7 +196,8 @@ int gdn_short_conv_step(const gdn_conv_args* args, void* state_inout, void* stre
   int st = conv_check(args, &p);
   if (st == GDN_OK) st = conv_pointers(p.a);
   if (st != GDN_OK) return st;
-  if (!rows_ok(p.a.y, p.a.T) || state_inout == nullptr || !aligned16(state_inout)) return GDN_ERR_ARG;
+  if (!rows_ok(p.a.y, p.a.T) || state_inout == nullptr || !aligned16(state_inout) || !conv_rows_apart(p.a))
+    return GDN_ERR_ARG;
   if (p.a.T == 0) return GDN_OK;
   return hip_status(launch_conv_fwd(p, state_inout, state_inout, stream));
 }

@@ -333,7 +333,7 @@ int64_t run_of(const gdn_conv_args& a, bool back) {
 // Few tokens go one by one, more of them where the sequences alone fill the CUs (C 6144, bf16, against
 // runs: one sequence of 8 tokens 6.1 and 5.9 us, of 16 8.9 and 5.4; 64 sequences of 32 20.1 and 20.6, of 64
 // 36 and 23; 512 sequences of 32 97 and 120).
-int64_t few_tokens(const gdn_conv_args& a) { return a.B * columns_of(a, false) >= 1024 ? 32 : 8; }
+int64_t few_tokens(const gdn_conv_args& a) { return a.B * columns_of(a, false) >= 1024 ? 32 : kConvInPlace; }
 
 Conv conv_of(const gdn_conv_args& a, bool back) {
   Conv k{};

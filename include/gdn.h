@@ -530,8 +530,9 @@ int gdn_gated_scan_bwd(const gdn_scan_args* args, const void* d_h, const float* 
  *
  * what mixes a few neighbouring tokens before a recurrence's inputs. The rows before the
  * first token are those of a state, the last W - 1 inputs so far, oldest first.
- *   x, y             [B, T, C], C a multiple of 8; x a view by x_stride, y contiguous and not
- *                    overlapping x
+ *   x, y             [B, T, C], C a multiple of 8; x a view by x_stride, y contiguous. y must not
+ *                    overlap x (GDN_ERR_ARG), but may be x itself where that is contiguous and T at
+ *                    most 8
  *   w                [C, W] float32, bias [C] float32 (NULL: zero)
  *   seq_lens         as above: rows of y behind a length stay as they were
  *   s0, s_final      [B, W - 1, C] in the inputs' type
