@@ -118,9 +118,25 @@ bool conv_rows_apart(const gdn_conv_args& a) {
          (a.y == a.x && (ld == width || rows == 1) && a.T <= kConvInPlace);
 }
 
-// In place only row over row, element over element.
-bool in_place_ok(const void* out, int out_dtype, const void* in, int in_dtype, int64_t ld, int64_t C) {
-  return out == nullptr || out != in || (out_dtype == in_dtype && ld == C);
+// out, `rows` contiguous rows of C elements, apart from in, whose rows lie ld elements from each other; or in
+// itself, row over row and element over element.
+bool apart_or_in_place(const void* out, int out_dtype, const void* in, int in_dtype, int64_t ld, int64_t C, int64_t rows) {
+  const int64_t size = size_of(in_dtype);
+  return !meets(out, rows * C * size_of(out_dtype), in, rows, C * size, ld * size) ||
+         (out == in && out_dtype == in_dtype && (ld == C || rows == 1));
+}
+// The same for rows of the recurrence: a workgroup (or a thread) reads its own rows' channels before it
+// writes them, and no other's.
+bool scan_rows_apart(const gdn_scan_args& a, const void* out) {
+  const int64_t rows = a.B * a.T;
+  return apart_or_in_place(out, a.dtype, a.x, a.dtype, a.x_stride, a.C, rows) &&
+         apart_or_in_place(out, a.dtype, a.f, a.dtype, a.f_stride, a.C, rows) &&
+         apart_or_in_place(out, a.dtype, a.i, a.dtype, a.i_stride, a.C, rows);
+}
+bool norm_rows_apart(const gdn_block_norm_args& a, int64_t rows, const void* out, int dtype) {
+  return apart_or_in_place(out, dtype, a.r, a.residual_dtype, a.r_stride, a.C, rows) &&
+         apart_or_in_place(out, dtype, a.y, a.dtype, a.y_stride, a.C, rows) &&
+         apart_or_in_place(out, dtype, a.gate, a.dtype, a.gate_stride, a.C, rows);
 }
 
 }  // namespace
@@ -142,6 +158,7 @@ int gdn_gated_scan_fwd(const gdn_scan_args* args, void* ws, size_t ws_bytes, voi
   if (st != GDN_OK) return st;
   const gdn_scan_args& a = p.a;
   if (!rows_ok(a.h, a.T) || !aligned16(a.h0) || !aligned16(a.h_final) || !aligned16(a.checkpoints)) return GDN_ERR_ARG;
+  if (!scan_rows_apart(a, a.h)) return GDN_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, scan_fwd_workspace(p))) return GDN_ERR_WORKSPACE;
   if (a.T == 0 && (a.h_final == nullptr || a.h_final == a.h0)) return GDN_OK;
   return hip_status(launch_scan_fwd(p, ws, stream));
@@ -152,7 +169,8 @@ int gdn_gated_scan_step(const gdn_scan_args* args, float* state_inout, void* str
   int st = scan_check(args, &p);
   if (st == GDN_OK) st = scan_pointers(p.a);
   if (st != GDN_OK) return st;
-  if (!rows_ok(p.a.h, p.a.T) || state_inout == nullptr || !aligned16(state_inout)) return GDN_ERR_ARG;
+  if (!rows_ok(p.a.h, p.a.T) || state_inout == nullptr || !aligned16(state_inout) || !scan_rows_apart(p.a, p.a.h))
+    return GDN_ERR_ARG;
   if (p.a.T == 0) return GDN_OK;
   return hip_status(launch_scan_step(p, state_inout, state_inout, stream));
 }
@@ -176,6 +194,11 @@ int gdn_gated_scan_bwd(const gdn_scan_args* args, const void* d_h, const float* 
   if (!aligned16(grads->ddecay) || !aligned16(grads->dh0)) return GDN_ERR_ARG;
   if (a.gate != GDN_SCAN_POWER && grads->ddecay != nullptr) return GDN_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, scan_bwd_workspace(p))) return GDN_ERR_WORKSPACE;
+  for (const void* out : {grads->dx, grads->df, grads->di})
+    if (!scan_rows_apart(a, out) || !apart_or_in_place(out, a.dtype, d_h, a.dtype, a.C, a.C, a.B * a.T)) return GDN_ERR_ARG;
+  // one segment's workgroup writes dh0, others may still read d_h_final
+  const int64_t state = a.B * a.C * int64_t(sizeof(float));
+  if (meets(grads->dh0, state, d_h_final, 1, state, state)) return GDN_ERR_ARG;
   if (a.T == 0 && grads->dh0 == nullptr && grads->ddecay == nullptr) return GDN_OK;
   return hip_status(launch_scan_bwd(p, d_h, d_h_final, *grads, ws, stream));
 }
@@ -219,6 +242,12 @@ int gdn_short_conv_bwd(const gdn_conv_args* args, const void* d_y, const void* d
     return GDN_ERR_ARG;
   if (a.bias == nullptr && grads->dbias != nullptr) return GDN_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, conv_bwd_workspace(p))) return GDN_ERR_WORKSPACE;
+  // a run reads rows of x and d_y, and of d_s_final, behind those whose gradients others write
+  const int64_t rows = a.B * a.T, width = a.C * size_of(a.dtype), state = a.B * (a.W - 1) * width;
+  if (meets(grads->dx, rows * width, a.x, rows, width, a.x_stride * size_of(a.dtype)) ||
+      meets(grads->dx, rows * width, d_y, 1, rows * width, rows * width) ||
+      meets(grads->ds0, state, a.s0, 1, state, state) || meets(grads->ds0, state, d_s_final, 1, state, state))
+    return GDN_ERR_ARG;
   if (a.T == 0 && grads->ds0 == nullptr && grads->dw == nullptr && grads->dbias == nullptr) return GDN_OK;
   return hip_status(launch_conv_bwd(p, d_y, d_s_final, *grads, ws, stream));
 }
@@ -232,12 +261,10 @@ int gdn_block_norm_fwd(const gdn_block_norm_args* args, void* stream) {
   if (a.T == 0) return GDN_OK;
   if ((a.out == nullptr && a.residual_out == nullptr) || a.out == a.residual_out) return GDN_ERR_ARG;
   if (!aligned16(a.out) || !aligned16(a.residual_out)) return GDN_ERR_ARG;
-  for (const auto& [out, dtype] : {std::pair<void*, int>{a.out, a.dtype}, {a.residual_out, a.residual_dtype}}) {
-    if (!in_place_ok(out, dtype, a.r, a.residual_dtype, a.r_stride, a.C) ||
-        !in_place_ok(out, dtype, a.y, a.dtype, a.y_stride, a.C) ||
-        !in_place_ok(out, dtype, a.gate, a.dtype, a.gate_stride, a.C))
-      return GDN_ERR_ARG;
-  }
+  if (!norm_rows_apart(a, p.tokens, a.out, a.dtype) || !norm_rows_apart(a, p.tokens, a.residual_out, a.residual_dtype))
+    return GDN_ERR_ARG;
+  const int64_t all = p.tokens * a.C, bytes = all * size_of(a.residual_dtype);
+  if (meets(a.out, all * size_of(a.dtype), a.residual_out, 1, bytes, bytes)) return GDN_ERR_ARG;
   return hip_status(launch_block_norm_fwd(p, stream));
 }
 
@@ -263,6 +290,12 @@ int gdn_block_norm_bwd(const gdn_block_norm_args* args, const gdn_block_norm_gra
       (a.weight == nullptr && g->dweight != nullptr))
     return GDN_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, block_norm_bwd_workspace(p))) return GDN_ERR_WORKSPACE;
+  for (const auto& [out, dtype] : {std::pair<void*, int>{g->dr, a.residual_dtype}, {g->dy, a.dtype}, {g->dgate, a.dtype}}) {
+    if (!norm_rows_apart(a, p.tokens, out, dtype) ||
+        !apart_or_in_place(out, dtype, g->d_out, a.dtype, a.C, a.C, p.tokens) ||
+        !apart_or_in_place(out, dtype, g->d_residual_out, a.residual_dtype, a.C, a.C, p.tokens))
+      return GDN_ERR_ARG;
+  }
   if (a.T == 0 && g->dscale == nullptr && g->dpost_weight == nullptr && g->dweight == nullptr) return GDN_OK;
   return hip_status(launch_block_norm_bwd(p, *g, ws, stream));
 }

@@ -455,7 +455,8 @@ int gdn_gated_norm_bwd(const gdn_gated_norm_args* args, const gdn_gated_norm_gra
  * channels that keep many tokens keep their last bits.
  *   x, f, i      [B, T, C], C a multiple of 8; views of a larger array by *_stride as for the
  *                linear entry points (at least C elements from token to token)
- *   h            [B, T, C], contiguous, in the inputs' type; must not overlap an input
+ *   h            [B, T, C], contiguous, in the inputs' type; may be x, f or i itself where that is
+ *                contiguous, and must not overlap an input otherwise (GDN_ERR_ARG)
  *   seq_lens     as for the linear entry points: rows of h behind a length stay as they were
  *   h0, h_final  [B, C] float32
  *   checkpoints  [B, ceil(T / GDN_SCAN_SPAN), C] float32: the state before every span of
@@ -502,7 +503,9 @@ int gdn_gated_scan_step(const gdn_scan_args* args, float* state_inout, void* str
 
 /* Gradient outputs of gdn_gated_scan_bwd: dx, df, di [B, T, C] contiguous in args->dtype
  * (di NULL without i), zero behind a sequence's length; ddecay [C] float32 (POWER only;
- * NULL: not written) and dh0 [B, C] float32 (NULL: not written). None may overlap an input. */
+ * NULL: not written) and dh0 [B, C] float32 (NULL: not written). dx, df or di may be x, f, i or d_h
+ * itself where that is contiguous; otherwise none may overlap an input (GDN_ERR_ARG for rows, and for
+ * dh0 over d_h_final). */
 typedef struct gdn_scan_grads {
   void* dx;
   void* df;
@@ -560,7 +563,8 @@ int gdn_short_conv_step(const gdn_conv_args* args, void* state_inout, void* stre
 
 /* Gradient outputs of gdn_short_conv_bwd: dx [B, T, C] contiguous and ds0 [B, W - 1, C]
  * (NULL: not written) in args->dtype, zero behind a sequence's length; dw [C, W] and dbias
- * [C] float32 (NULL: not written). None may overlap an input. */
+ * [C] float32 (NULL: not written). None may overlap an input (GDN_ERR_ARG for dx over x or d_y and
+ * for ds0 over a state). */
 typedef struct gdn_conv_grads {
   void* dx;
   float* dw;
@@ -589,7 +593,8 @@ int gdn_short_conv_bwd(const gdn_conv_args* args, const void* d_y, const void* d
  *                     post_weight are NULL and post_norm 0): u = 0, the norm before a first block
  *   scale, post_weight, weight   [C] float32, NULL means ones
  * r, y and gate may be views by their strides; residual_out and out are contiguous, at least
- * one is given, and each may be r, y or gate itself where that is contiguous and of its type.
+ * one is given, and each may be r, y or gate itself where that is contiguous and of its type; they
+ * must not overlap each other or an input otherwise (GDN_ERR_ARG).
  * Other limits as for the gated recurrence. */
 typedef struct gdn_block_norm_args {
   int32_t dtype;           /* enum gdn_dtype: y, gate, out                            */
@@ -615,8 +620,10 @@ int gdn_block_norm_fwd(const gdn_block_norm_args* args, void* stream);
 /* Gradients: d_residual_out (residual_dtype) and d_out (dtype), contiguous, at least one of
  * them given (NULL: zero), in; dr (residual_dtype), dy and dgate (dtype), contiguous, NULL:
  * not written, and dscale, dpost_weight, dweight [C] float32 (NULL: not written) out. What an
- * absent input would have as a gradient must be NULL. args->residual_out and out are ignored;
- * dr may be d_residual_out. The weight sums run in a fixed order. */
+ * absent input would have as a gradient must be NULL. args->residual_out and out are ignored.
+ * dr, dy and dgate may each be a [B, T, C] input itself where that is contiguous and of its type (dr
+ * d_residual_out), and must not overlap one otherwise (GDN_ERR_ARG). The weight sums run in a fixed
+ * order. */
 typedef struct gdn_block_norm_grads {
   const void* d_residual_out;
   const void* d_out;
