@@ -34,7 +34,8 @@ __device__ __forceinline__ float sigmoid_of(float z) {
 // out[c] = sum over rows of partial[row][c] for c < cols, split over up to three arrays of n0,
 // n1 and the remaining columns (NULL: dropped). The sums of out1 come times by1, and times by_also
 // in `also` (NULL: times one). A block has 32 columns, 32 threads a column add up every 32nd row,
-// then a tree of fixed order.
+// then a tree of fixed order. Rows may be millions (one a sequence): a thread's sum is one of two floats,
+// or 2^15 equal terms would be off by 10^-4 of it.
 struct ColumnSum {
   const float* partial;
   int rows;
@@ -45,10 +46,15 @@ struct ColumnSum {
 };
 static __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSum a) {
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
-  float s = 0.0f;
+  float s = 0.0f, low = 0.0f;
   if (c < a.cols) {
 #pragma unroll 4
-    for (int r = threadIdx.x / 32; r < a.rows; r += 32) s += a.partial[r * a.cols + c];
+    for (int r = threadIdx.x / 32; r < a.rows; r += 32) {
+      const float x = a.partial[r * a.cols + c], sum = s + x, back = sum - s;
+      low += (s - (sum - back)) + (x - back);
+      s = sum;
+    }
+    if (low == low) s += low;   // not behind an infinity
   }
   __shared__ float part[1024];
   part[threadIdx.x] = s;
