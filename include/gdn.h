@@ -587,7 +587,9 @@ int gdn_short_conv_bwd(const gdn_conv_args* args, const void* d_y, const void* d
  *     u  = y (sum y^2 / C + eps)^{-1/2} post_weight   (post_norm), or y
  *     r' = residual_scale r + scale act(gate) u
  *     n  = r' (sum r'^2 / C + eps)^{-1/2} weight
- * with r the residual stream; the sums and n are of r' before it is rounded.
+ * with r the residual stream; the sums and n are of r' before it is rounded. Sums of squares are
+ * float32: a row whose sum passes 3.4e38 (values of 1.8e19 / sqrt(C), 1.4e17 at C = 16,384) has a
+ * norm of zeros; with eps = 0 values under 1e-19 lose bits, and a row of zeros is 0 times infinity.
  *   r, residual_out   [B, T, C] in residual_dtype; C a multiple of 8 up to 16,384
  *   y, gate, out      [B, T, C] in dtype. gate NULL: act(gate) is 1. y NULL (then gate, scale and
  *                     post_weight are NULL and post_norm 0): u = 0, the norm before a first block

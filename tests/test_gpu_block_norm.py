@@ -224,3 +224,18 @@ def test_block_norm_gradients_against_differences():
             down = loss()
             flat[j] = keep
             assert abs((up - down) / (2 * e) - grad[j].item()) < 1e-3 * grad.abs().max().item(), (n, j)
+
+
+@pytest.mark.parametrize("C", [64, 2048, 16384])
+def test_block_norm_up_to_the_largest_squares(C):
+    """Values up to 1.8e19 / sqrt(C), whose squares add up to the largest float: norms of 1 before and after
+    a block (a root, a reciprocal and two products of roundings: 1e-6), and finite gradients."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    big = torch.full((1, 2, C), 1.8e19 / C ** 0.5, device=dev())
+    big[0, 1] = 1e-15
+    for kw in (dict(), dict(y=big, post_norm=True)):
+        _, n = gdn.gdn_block_norm_fwd(torch.zeros_like(big) if kw else big, eps=0.0, **kw)
+        assert (n - 1).abs().max() < 1e-6
+    g = gdn.gdn_block_norm_bwd(big, d_out=torch.ones_like(big), eps=0.0, weight=torch.ones(C, device=dev()))
+    assert torch.isfinite(g["dr"]).all() and ((g["dw"] - 2).abs() < 1e-5).all()
