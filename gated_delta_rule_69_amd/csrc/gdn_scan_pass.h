@@ -25,12 +25,15 @@
 // many under LOG, where the tokens before may have grown the state), and the second joins those before
 // its own.
 //
-// Memory bounds it, as long as a CU's loads under way are long ones: rows of 32, 64 and 128 bytes a slice
-// took 308, 196 and 164 us for the second launch of B2 T32768 C2048 (bf16, sigmoid). Now 206 us in both
-// launches (805 MB, 3.9 TB/s; 176 with C 2112, whose rows do not start at the same 4 KiB), 145 for B8 T1024
-// C8192 with an input gate (537 MB), where one launch does; B1 T4096 C2048 25 us, two short launches. The
-// gradients of B2 T4096 C2048 with power and input gate 80 us (235 MB): their vector instructions, a
-// hundred a channel and token, are as much as their bytes.
+// Memory bounds it, as long as a CU's loads under way are long ones: the launch that writes h of B2 T32768
+// C2048 (bf16, sigmoid; 805 MB) takes 314 us with rows of 32 bytes a slice (and no segments), 202 with 64
+// and 173 with 128. Both launches 206 us (3.9 TB/s; 177 with C 2112, whose rows do not start at the same 4
+// KiB). What the first launch may leave out goes by the gates: of those 28 us under sigmoid gates of
+// logits around 3, 46 under the same decays by LOG, 140 under power gates whose channels keep thousands of
+// tokens (300 in all, 389 with an input gate). One launch does for B8 T1024 C8192 with power and input gate
+// (143 us, 537 MB); B1 T4096 C2048 takes 25 to 36 us, two short launches. The gradients of B2 T4096 C2048 with
+// power and input gate 77 us (235 MB, 3.0 TB/s): 250 registers, two waves a SIMD, whose eighty vector
+// instructions a channel and token take 45 % of the issue slots.
 #pragma once
 
 #include <algorithm>
@@ -257,7 +260,8 @@ __device__ __forceinline__ uint4v rows_from(const char* base, int64_t ld, int64_
 
 // Rows on their way from memory to LDS, ahead of their use: a wave's own, so that nothing but its own
 // count of loads says when they are there. Lane l of a load brings sixteen bytes to the wave's place
-// 16 l: the rows r of the runs lie side by side there, at 256 r + kRow run, free of bank conflicts. The
+// 16 l: the rows r of the runs lie side by side there, at 256 r + kRow run, so that a wave reads 256 bytes
+// in a row (what the LDS counters show of bank conflicts is the exchange between waves). The
 // loads are written as assembly, which has no registers to guard; the compiler's own counts only ever
 // wait for more.
 template <int LANES> struct Feed {
