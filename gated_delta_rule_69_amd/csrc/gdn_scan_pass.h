@@ -137,11 +137,12 @@ struct Run {
   float A, C, H;
 };
 
-// x 2^(hi + lo): 2 to the whole part by the exponent, so that no factor on the way leaves float32's
-// range unless the result does. Beyond 2^1000 it is 0 or infinite for every x.
+// x 2^(hi + lo): 2 to the whole part by the exponent, rounded up so that the rest of it makes no x
+// larger: nothing on the way leaves float32's range unless the result does. Beyond 2^1000 that is 0 or
+// infinite for every x.
 __device__ __forceinline__ float times_exp2(float x, float hi, float lo) {
-  const float n = rintf(__builtin_amdgcn_fmed3f(hi, -1000.0f, 1000.0f));
-  const float r = __builtin_amdgcn_fmed3f((hi - n) + lo, -1.0f, 1.0f);
+  const float n = ceilf(__builtin_amdgcn_fmed3f(hi, -1000.0f, 1000.0f));
+  const float r = __builtin_amdgcn_fmed3f((hi - n) + lo, -2.0f, 2.0f);
   return ldexpf(x * __builtin_amdgcn_exp2f(r), int(n));
 }
 

@@ -27,7 +27,7 @@ def _near(got, want, size, name):
     assert (e <= most + 1e-37).all(), f"{name} at {worst}: {f64(got)[worst]} for {want[worst]}, off by {e[worst]:.2e} of at most {most[worst]:.2e}"
 
 
-def _compare(x, f, i, h0, d_h, dh_final, lens=None):
+def _compare(x, f, i, h0, d_h, dh_final, lens=None, low=0.0):
     import gated_delta_rule_69_amd as gdn
     from block_util import lengths
     from layer_util import dev, f64
@@ -46,7 +46,7 @@ def _compare(x, f, i, h0, d_h, dh_final, lens=None):
     for ck in (marks, None):
         g = gdn.gdn_gated_scan_bwd(up(x), up(f), up(i), d_h=up(d_h), h0=up(h0), dh_final=up(dh_final), checkpoints=ck, **kw)
         for n, t in g.items():
-            _near(t, grads[n], bounds[n] * (2.0 if n == "df" else 1.0), n)
+            _near(t, grads[n], bounds[n] * 2.0 + low / 1e-5 if n == "df" else bounds[n], n)
     state = up(h0).clone()
     one = gdn.gdn_gated_scan_step(up(x), up(f), up(i), state=state, **kw)
     # one by one: each token rounds, an exponential to 2^-23 and a sum, on top of the above
@@ -125,3 +125,18 @@ def test_growth_after_a_reset(dt):
     f[:, 100], f[0, 101], f[1, 300:303], f[:, 690] = -INF, -INF, -INF, -INF
     x, d_h = (torch.randn((B, T, C), generator=gen).to(dtype) for _ in range(2))
     _compare(x, f.to(dtype), None, torch.randn((B, C), generator=gen), d_h, torch.randn((B, C), generator=gen))
+
+
+@pytest.mark.parametrize("f", [-0.1343, -0.09, -0.05, 0.0, -3.0])
+@pytest.mark.parametrize("T", [40, 2000])
+def test_decay_from_the_end_of_float32(T, f):
+    """The largest states, whose decays have any fraction of a power of two.
+
+    df = l a h, and where one of h and l falls below float32's normal range each of its tokens rounds to
+    half of 2^-149, T of them at most (what they decay by since only takes from that); the other factor is up
+    to 3.3e38. So df is off by T 2^-150 3.3e38 on top: l = 1e-37 e^-12 has ten bits, e^-24 of it none."""
+    x = torch.zeros((1, T, 16))
+    h0 = torch.full((1, 16), 3.3e38)
+    low = T * 2.0 ** -150 * 3.3e38
+    _compare(x, torch.full((1, T, 16), f), None, h0, x, torch.full((1, 16), 1e-37), low=low)
+    _compare(x, torch.full((1, T, 16), f), None, torch.ones((1, 16)), x, h0, low=low)
