@@ -132,11 +132,11 @@ def gdn_gated_scan_fwd(x, f, i=None, *, gate="sigmoid", decay=None, h0=None, h_f
                        workspace=None, stream=None, want_state=True, want_checkpoints=False):
     """The gated recurrence a channel over prompts, h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t, on
     x, f and i [B, T, C] (without ``i`` its factor is 1). ``gate`` says what f is: "log", a = e^f
-    (f above 0 grows the state) and m = 1; "sigmoid", a = sigmoid(f) and m = 1 - a; "power", a = e^(-decay sigmoid(f)) with a
-    float32 ``decay`` [C] >= 0, and m = sqrt(1 - a^2). Returns (h, h_final), allocated when not
-    given; h0 and h_final are float32 [B, C], and h_final may be h0. h may be x, f or i where that
-    is contiguous. With ``want_checkpoints`` also
-    the states before every 64 tokens, float32 [B, ceil(T / 64), C], which spare the gradients a
+    (f above 0 grows the state) and m = 1; "sigmoid", a = sigmoid(f) and m = 1 - a; "power",
+    a = e^(-decay sigmoid(f)) with a float32 ``decay`` [C] >= 0, and m = sqrt(1 - a^2). Returns (h,
+    h_final), allocated when not given; h0 and h_final are float32 [B, C], and h_final may be h0; h
+    may be x, f or i where that is contiguous. With ``want_checkpoints`` also the states before
+    every 64 tokens, float32 [B, ceil(T / 64), C], which spare the gradients a
     pass over the inputs. ``seq_lens`` [B] int32 gives each sequence's tokens in a padded batch:
     rows of h behind them are left as they are in a given h, and zero in one allocated here."""
     if _elsewhere(x, "x", stream):
