@@ -140,3 +140,40 @@ def test_decay_from_the_end_of_float32(T, f):
     low = T * 2.0 ** -150 * 3.3e38
     _compare(x, torch.full((1, T, 16), f), None, h0, x, torch.full((1, 16), 1e-37), low=low)
     _compare(x, torch.full((1, T, 16), f), None, torch.ones((1, 16)), x, h0, low=low)
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid", "power"])
+@pytest.mark.parametrize("n,value", [("x", float("nan")), ("x", INF), ("f", float("nan")), ("i", float("nan"))])
+@pytest.mark.parametrize("T,at", [(12, 3), (300, 37), (4000, 700)])
+def test_nan_and_inf_stay_in_their_channel_for_every_gate(T, at, n, value, gate):
+    """From its row on, under decays that leave weights over 2^-127; nothing before and beside it changes, and
+    in the gradients nothing beside its channel."""
+    import gated_delta_rule_69_amd as gdn
+    from layer_util import dev
+    gen = torch.Generator().manual_seed(T)
+    B, C = 2, 24
+    t = {k: torch.randn((B, T, C), generator=gen).to(dev()) for k in ("x", "f", "i", "d_h")}
+    if gate != "power":
+        t["f"] = t["f"] * 0.01 if gate == "log" else t["f"].abs() + 4.5
+    decay = torch.full((C,), 0.01, device=dev()) if gate == "power" else None
+
+    def run():
+        a = (t["x"], t["f"], t["i"])
+        kw = dict(gate=gate, decay=decay)
+        return (gdn.gdn_gated_scan_fwd(*a, **kw)[0], gdn.gdn_gated_scan_bwd(*a, d_h=t["d_h"], **kw),
+                gdn.gdn_gated_scan_step(*a, state=torch.zeros((B, C), device=dev()), **kw))
+
+    clean = run()
+    t[n][1, at, 5] = value
+    got = run()
+    for h, want in ((got[0], clean[0]), (got[2], clean[2])):
+        assert not torch.isfinite(h[1, at:, 5]).any()
+        h[1, at:, 5] = want[1, at:, 5]
+        assert torch.equal(h, want)
+    for k, g in got[1].items():
+        want = clean[1][k]
+        (g[5:6] if g.dim() == 1 else g[1, ..., 5]).copy_(want[5:6] if g.dim() == 1 else want[1, ..., 5])
+        assert torch.equal(g, want), k
+    if n == "f":   # l runs through a from the row on backwards
+        g = gdn.gdn_gated_scan_bwd(t["x"], t["f"], t["i"], d_h=t["d_h"], gate=gate, decay=decay)
+        assert not torch.isfinite(g["dx"][1, :at, 5]).any() and not torch.isfinite(g["dh0"][1, 5])
